@@ -43,6 +43,27 @@ class HashLayout(ctypes.Structure):
                 ("history_len", ctypes.c_int64)]
 
 
+class PageLayout(ctypes.Structure):
+    _fields_ = [("block_size", ctypes.c_int32), ("max_blocks", ctypes.c_int32), ("n_blocks", ctypes.c_int64)]
+
+
+class _PlanOut(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("token_start", "start_pos", "seq_lens", "status", "free_left", "slots",
+                                                     "positions", "requests", "live")]
+
+
+class NormLayout(ctypes.Structure):
+    _fields_ = [("hc", ctypes.c_int32), ("dim", ctypes.c_int32), ("y_streams", ctypes.c_int32),
+                ("stream_format", ctypes.c_int32), ("gate", ctypes.c_int32), ("post_norm", ctypes.c_int32),
+                ("pre_norm", ctypes.c_int32), ("alpha", ctypes.c_float), ("beta", ctypes.c_float),
+                ("post_eps", ctypes.c_float), ("pre_eps", ctypes.c_float)]
+
+
+class LinearLayout(ctypes.Structure):
+    _fields_ = [("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32), ("activation", ctypes.c_int32),
+                ("glu", ctypes.c_int32), ("stream_format", ctypes.c_int32)]
+
+
 class EngramError(RuntimeError):
     def __init__(self, where: str, status: int):
         msg = _lib.engram_status_str(status).decode()
@@ -72,6 +93,19 @@ _lib.engram_forward_noalloc.restype = ctypes.c_int
 _lib.engram_forward_check.argtypes = [_vp, _sz, _vp]
 _lib.engram_set_spin_budget.argtypes = [ctypes.c_uint32]
 _lib.engram_set_spin_budget.restype = ctypes.c_uint32
+_lib.engram_batch_plan.argtypes = [ctypes.POINTER(PageLayout), _vp, _vp, _i64, _vp, _vp, _vp, _i64,
+                                   ctypes.POINTER(_PlanOut), _vp, _vp]
+_lib.engram_hash_ids_paged.argtypes = [ctypes.POINTER(HashLayout), ctypes.POINTER(PageLayout), _vp, _vp, _vp, _vp, _vp, _vp,
+                                       _i64, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp]
+_lib.engram_residual_norm.argtypes = [ctypes.POINTER(NormLayout), _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _vp,
+                                      _vp, _vp]
+_lib.engram_linear.argtypes = [ctypes.POINTER(LinearLayout), _vp, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _i64, _vp]
+_lib.engram_page_layout_check.argtypes = [ctypes.POINTER(PageLayout)]
+_lib.engram_norm_layout_check.argtypes = [ctypes.POINTER(NormLayout)]
+_lib.engram_linear_layout_check.argtypes = [ctypes.POINTER(LinearLayout)]
+for _f in (_lib.engram_batch_plan, _lib.engram_hash_ids_paged, _lib.engram_residual_norm, _lib.engram_linear,
+           _lib.engram_page_layout_check, _lib.engram_norm_layout_check, _lib.engram_linear_layout_check):
+    _f.restype = ctypes.c_int
 for _f in (_lib.engram_layout_check, _lib.engram_param_counts, _lib.engram_gather_dequant,
            _lib.engram_kv_proj, _lib.engram_gate_apply, _lib.engram_forward, _lib.engram_hash_ids,
            _lib.engram_forward_check):
@@ -81,7 +115,8 @@ EXPORTED = ["engram_layout_check", "engram_param_counts", "engram_forward_worksp
             "engram_forward_staging_bytes",
             "engram_gather_dequant", "engram_kv_proj", "engram_gate_apply", "engram_forward",
             "engram_hash_ids", "engram_status_str", "engram_forward_check", "engram_set_spin_budget",
-            "engram_forward_noalloc"]
+            "engram_forward_noalloc", "engram_batch_plan", "engram_hash_ids_paged", "engram_residual_norm",
+            "engram_linear", "engram_page_layout_check", "engram_norm_layout_check", "engram_linear_layout_check"]
 
 
 SCALE_FP32, SCALE_E8M0 = 0, 1  # engram_scale_format
@@ -517,3 +552,266 @@ def _check_forward_args(layout: EngramLayout, x, hash_ids, token_mask, table, sc
     _same_device(x, hash_ids=hash_ids, table=table, scales=scales, wkv=wkv, q_weight=q_weight,
                  k_weight=k_weight, token_mask=token_mask, out=out, err_count=err_count)
     return B, T
+
+
+# ----------------------------------------------------------------------------------------
+# The serving operators around the forward: a plan of ragged requests, their row ids, the norms
+# around a block, a projection with its epilogue.  They launch on the current stream of their
+# tensors' device.
+# ----------------------------------------------------------------------------------------
+
+STREAM_BF16, STREAM_FP32 = 0, 1                    # engram_stream_format
+GATE_NONE, GATE_TOKEN, GATE_FEATURE = 0, 1, 2      # engram_gate_kind
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU, ACT_SIGMOID = range(6)  # engram_activation
+
+_STREAM = {STREAM_BF16: torch.bfloat16, STREAM_FP32: torch.float32}
+
+
+def _launch(where: str, device: torch.device, fn, *args) -> None:
+    """Calls a C entry point on `device`'s current stream (as its last argument), with that device
+    current for the call."""
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if st != ENGRAM_OK:
+        raise EngramError(where, st)
+
+
+def _tensor(name: str, t: torch.Tensor, shape: tuple, dtype) -> int:
+    """The address of a contiguous tensor of this shape and dtype."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(name: str, t: torch.Tensor, lead: tuple, row: tuple) -> int:
+    """The stride in elements between the rows of a tensor [*lead, *row] whose rows are contiguous
+    and evenly spaced."""
+    if t.shape != (*lead, *row):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(*lead, *row)}")
+    size = math.prod(row)
+    if t.is_contiguous():
+        return size
+    n, want, step = len(lead), 1, t.stride()
+    for d in range(len(row) - 1, -1, -1):
+        if row[d] != 1 and step[n + d] != want:
+            raise ValueError(f"{name}: the last {len(row)} dimensions must be contiguous")
+        want *= row[d]
+    stride = None
+    want = 0
+    for d in range(n - 1, -1, -1):
+        if lead[d] == 1:
+            continue
+        if stride is None:
+            stride, want = step[d], step[d]
+        elif step[d] != want:
+            raise ValueError(f"{name}: the rows must be evenly spaced")
+        want *= lead[d]
+    return size if stride is None else stride
+
+
+def _on(device: torch.device, *ts) -> None:
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, got {device}")
+    for t in ts:
+        if t is not None and t.device != device:
+            raise ValueError(f"a tensor is on {t.device}, expected {device}")
+
+
+def make_page_layout(block_size: int, max_blocks: int, n_blocks: int) -> PageLayout:
+    """A pool of n_blocks pages of block_size positions, at most max_blocks of them per request."""
+    return PageLayout(block_size, max_blocks, n_blocks)
+
+
+class BatchPlan:
+    """The buffers engram_batch_plan writes (engram_batch_plan_out in include/engram.h), kept by the
+    caller from step to step.  seq_lens and free_left are the next step's cached_lens and free_count:
+    use two plans in turn, or copy them (a call never writes what it reads)."""
+
+    FIELDS = ("token_start", "start_pos", "seq_lens", "status", "free_left", "slots", "positions", "requests", "live")
+
+    def __init__(self, n_requests: int, max_tokens: int, device="cuda"):
+        def make(n, dtype=torch.int32):
+            return torch.zeros(n, dtype=dtype, device=device)
+        self.n_requests, self.max_tokens = n_requests, max_tokens
+        self.token_start, self.start_pos, self.seq_lens = make(n_requests + 1), make(n_requests), make(n_requests)
+        self.status, self.free_left = make(n_requests), make(1)
+        self.slots, self.positions = make(max_tokens, torch.int64), make(max_tokens)
+        self.requests, self.live = make(max_tokens), make(max_tokens, torch.uint8)
+        self.device = self.slots.device
+
+
+def engram_batch_plan(layout: PageLayout, new_lens: torch.Tensor, cached_lens: torch.Tensor, block_table: torch.Tensor,
+                      free_list: torch.Tensor, free_count: torch.Tensor, plan: BatchPlan,
+                      err_count: Optional[torch.Tensor] = None) -> BatchPlan:
+    """Plans a step of ragged requests into `plan` (engram_batch_plan in include/engram.h): admits
+    requests by tokens and pages, takes and gives back pages (block_table [R, max_blocks] and
+    free_list [n_blocks] are updated in place), and lays out the admitted tokens."""
+    R, i32 = plan.n_requests, torch.int32
+    new = _tensor("new_lens", new_lens, (R,), i32)
+    held = _tensor("cached_lens", cached_lens, (R,), i32)
+    table = _tensor("block_table", block_table, (R, layout.max_blocks), i32)
+    pool = _tensor("free_list", free_list, (layout.n_blocks,), i32)
+    count = _tensor("free_count", free_count, (1,), i32)
+    _check_err(err_count)
+    # the plan's buffers are attributes: they may have been replaced since it was made
+    out = _PlanOut(_tensor("plan.token_start", plan.token_start, (R + 1,), i32),
+                   _tensor("plan.start_pos", plan.start_pos, (R,), i32),
+                   _tensor("plan.seq_lens", plan.seq_lens, (R,), i32),
+                   _tensor("plan.status", plan.status, (R,), i32),
+                   _tensor("plan.free_left", plan.free_left, (1,), i32),
+                   _tensor("plan.slots", plan.slots, (plan.max_tokens,), torch.int64),
+                   _tensor("plan.positions", plan.positions, (plan.max_tokens,), i32),
+                   _tensor("plan.requests", plan.requests, (plan.max_tokens,), i32),
+                   _tensor("plan.live", plan.live, (plan.max_tokens,), torch.uint8))
+    _on(free_list.device, new_lens, cached_lens, block_table, free_count, err_count, plan.token_start, plan.start_pos,
+        plan.seq_lens, plan.status, plan.free_left, plan.slots, plan.positions, plan.requests, plan.live)
+    _launch("engram_batch_plan", free_list.device, _lib.engram_batch_plan, layout, new, held, R, table, pool, count,
+            plan.max_tokens, out, None if err_count is None else err_count.data_ptr())
+    return plan
+
+
+def engram_hash_ids_paged(layout: HashLayout, pages: PageLayout, token_map: torch.Tensor, multipliers: torch.Tensor,
+                          primes: torch.Tensor, offsets: torch.Tensor, input_ids: torch.Tensor, plan: BatchPlan,
+                          block_table: torch.Tensor, history: torch.Tensor, token_mask: Optional[torch.Tensor] = None,
+                          out: Optional[torch.Tensor] = None, err_count: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Row ids [n_layers, n_tokens, (max_ngram - 1) * n_heads] int64 of a plan's flat tokens input_ids
+    [plan.max_tokens] (engram_hash_ids_paged in include/engram.h); history [n_blocks, block_size]
+    int64, addressed through the plan and block_table, is read and updated in place."""
+    n, R, i64, i32 = plan.max_tokens, plan.n_requests, torch.int64, torch.int32
+    cols = (layout.max_ngram - 1) * layout.n_heads
+    if token_map.dtype == torch.int32:
+        tmap = _tensor("token_map", token_map, (layout.vocab,), torch.int32)
+    else:
+        tmap = _tensor("token_map", token_map, (layout.vocab,), torch.uint32)
+    mult = _tensor("multipliers", multipliers, (layout.n_layers, layout.max_ngram), i64)
+    _numel("primes", primes, (layout.n_layers, layout.max_ngram - 1, layout.n_heads))
+    _contig("primes", primes, i64)
+    _numel("offsets", offsets, (layout.n_layers, cols))
+    _contig("offsets", offsets, i64)
+    ids = _tensor("input_ids", input_ids, (n,), i64)
+    mask = None
+    if token_mask is not None:
+        mask = _tensor("token_mask", token_mask, (n,), torch.bool if token_mask.dtype == torch.bool else torch.uint8)
+    slots = _tensor("plan.slots", plan.slots, (n,), i64)
+    pos = _tensor("plan.positions", plan.positions, (n,), i32)
+    req = _tensor("plan.requests", plan.requests, (n,), i32)
+    start = _tensor("plan.start_pos", plan.start_pos, (R,), i32)
+    table = _tensor("block_table", block_table, (R, pages.max_blocks), i32)
+    hist = _tensor("history", history, (pages.n_blocks, pages.block_size), i64)
+    _check_err(err_count)
+    if out is None:
+        out = torch.empty((layout.n_layers, n, cols), dtype=i64, device=input_ids.device)
+    to = _tensor("out", out, (layout.n_layers, n, cols), i64)
+    _on(input_ids.device, token_map, multipliers, primes, offsets, token_mask, plan.slots, plan.positions, plan.requests,
+        plan.start_pos, block_table, history, out, err_count)
+    _launch("engram_hash_ids_paged", input_ids.device, _lib.engram_hash_ids_paged, layout, pages, tmap, mult,
+            primes.data_ptr(), offsets.data_ptr(), ids, mask, n, slots, pos, req, start, R, table, hist, to,
+            None if err_count is None else err_count.data_ptr())
+    return out
+
+
+def make_norm_layout(hc: int, dim: int, y_streams: Optional[int] = None, gate: int = GATE_NONE, post_norm: bool = True,
+                     pre_norm: bool = True, alpha: float = 1.0, beta: float = 1.0, post_eps: float = 1e-20,
+                     pre_eps: float = 1e-20, stream_format: int = STREAM_BF16) -> NormLayout:
+    """Layout of engram_residual_norm; y_streams: hc (the default), or 1 for a block output shared by
+    every stream."""
+    return NormLayout(hc, dim, hc if y_streams is None else y_streams, stream_format, gate, bool(post_norm), bool(pre_norm),
+                      alpha, beta, post_eps, pre_eps)
+
+
+def engram_residual_norm(layout: NormLayout, x: torch.Tensor, y: Optional[torch.Tensor] = None,
+                         gate: Optional[torch.Tensor] = None, post_weight: Optional[torch.Tensor] = None,
+                         pre_weight: Optional[torch.Tensor] = None, token_mask: Optional[torch.Tensor] = None,
+                         out: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None):
+    """Closes a block and opens the next (engram_residual_norm in include/engram.h): returns
+    (out, h) with out = alpha * x + beta * gate * norm(y) and h = norm(out).  x [B, T, hc, dim]
+    contiguous; y and a gate per feature [B, T, y_streams, dim] may be slices of wider rows; out may
+    be x.  Without y, h = norm(x) and out is x; without pre_norm, h is None."""
+    if x.dim() != 4:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected [B, T, hc, dim]")
+    B, T = x.shape[0], x.shape[1]
+    full = (B, T, layout.hc, layout.dim)
+    stream = _STREAM.get(layout.stream_format, torch.bfloat16)
+    xp = _tensor("x", x, full, stream)
+    yp = gp = op = hp = mp = None
+    y_stride = gate_stride = 0
+    if y is not None:
+        if y.dtype != torch.bfloat16:
+            raise TypeError(f"y has dtype {y.dtype}, expected {torch.bfloat16}")
+        y_stride = _rows("y", y, (B, T), (layout.y_streams, layout.dim))
+        yp = y.data_ptr()
+        if out is None:
+            out = torch.empty_like(x)
+        op = _tensor("out", out, full, stream)
+        if (gate is None) != (layout.gate == GATE_NONE):
+            raise ValueError("gate does not match the layout's gate kind")
+        if layout.gate == GATE_TOKEN:
+            gp = _tensor("gate", gate, full[:3], torch.float32)
+        elif gate is not None:
+            if gate.dtype != torch.bfloat16:
+                raise TypeError(f"gate has dtype {gate.dtype}, expected {torch.bfloat16}")
+            gate_stride = _rows("gate", gate, (B, T), (layout.y_streams, layout.dim))
+            gp = gate.data_ptr()
+    elif gate is not None or out is not None:
+        raise ValueError("gate and out need y")
+    if layout.pre_norm:
+        if h is None:
+            h = torch.empty(full, dtype=torch.bfloat16, device=x.device)
+        hp = _tensor("h", h, full, torch.bfloat16)
+    elif h is not None:
+        raise ValueError("h needs pre_norm")
+    weights = (layout.hc, layout.dim)
+    post = None if post_weight is None else _tensor("post_weight", post_weight, weights, torch.float32)
+    pre = None if pre_weight is None else _tensor("pre_weight", pre_weight, weights, torch.float32)
+    if token_mask is not None:
+        mp = _tensor("token_mask", token_mask, (B, T), torch.bool if token_mask.dtype == torch.bool else torch.uint8)
+    _on(x.device, y, gate, post_weight, pre_weight, token_mask, out, h)
+    _launch("engram_residual_norm", x.device, _lib.engram_residual_norm, layout, xp, yp, y_stride, gp, gate_stride, post, pre,
+            mp, B, T, op, hp)
+    return (x if y is None else out), h
+
+
+def make_linear_layout(in_features: int, out_features: int, activation: int = ACT_NONE, glu: bool = False,
+                       stream_format: int = STREAM_BF16) -> LinearLayout:
+    return LinearLayout(in_features, out_features, activation, bool(glu), stream_format)
+
+
+def engram_linear(layout: LinearLayout, x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                  residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out [..., N] = residual + act(x [..., K] @ w^T + bias), or with the layout's glu
+    residual + act(gate) * value from a weight of 2 N rows (engram_linear in include/engram.h).  x,
+    residual and out may be slices of wider rows; out may be the residual."""
+    K, N = layout.in_features, layout.out_features
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"x has dtype {x.dtype}, expected {torch.bfloat16}")
+    if x.dim() < 1:
+        raise ValueError("x has no dimensions")
+    lead = tuple(x.shape[:-1])
+    M = math.prod(lead)
+    x_stride = _rows("x", x, lead, (K,))
+    rows = 2 * N if layout.glu else N
+    wp = _tensor("w", w, (rows, K), torch.bfloat16)
+    bp = None if bias is None else _tensor("bias", bias, (rows,), torch.float32)
+    stream = _STREAM.get(layout.stream_format, torch.bfloat16)
+    rp, r_stride = None, 0
+    if residual is not None:
+        if residual.dtype != stream:
+            raise TypeError(f"residual has dtype {residual.dtype}, expected {stream}")
+        r_stride = _rows("residual", residual, lead, (N,))
+        rp = residual.data_ptr()
+    if out is None:
+        out = torch.empty((*lead, N), dtype=stream, device=x.device)
+    elif out.dtype != stream:
+        raise TypeError(f"out has dtype {out.dtype}, expected {stream}")
+    o_stride = _rows("out", out, lead, (N,))
+    _on(x.device, w, bias, residual, out)
+    _launch("engram_linear", x.device, _lib.engram_linear, layout, x.data_ptr(), x_stride, wp, bp, rp, r_stride, M,
+            out.data_ptr(), o_stride)
+    return out

@@ -21,7 +21,8 @@ COMMON = ["--offload-arch=" + ARCH, "-O3", "-fPIC", "-std=c++17",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
           "-fno-gpu-flush-denormals-to-zero", "-Wno-unused-command-line-argument"]
 
-ENGRAM_SRC = ["engram_api.hip", "gather_gate.hip", "hash.hip", "stream.hip", "tiled.hip"]
+ENGRAM_SRC = ["engram_api.hip", "gather_gate.hip", "hash.hip", "stream.hip", "tiled.hip",
+              "serving_api.hip", "batch_plan.hip", "hash_paged.hip", "residual_norm.hip", "linear.hip"]
 LIB_ENGRAM = os.path.join(HERE, "libengram.so")
 LIB_SYNTH = os.path.join(ROOT, "synth", "libsynth_fill.so")
 LIB_ORACLE = os.path.join(ROOT, "oracle", "liboracle.so")

@@ -12,6 +12,23 @@
 
 using namespace engram;
 
+// Per-device facts, queried once per device.
+engram_status engram::device_info(DeviceInfo* out) {
+  static DeviceInfo cache[64];
+  static bool have[64] = {false};
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return ENGRAM_E_HIP;
+  if (!have[dev]) {
+    hipDeviceProp_t prop;
+    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return ENGRAM_E_HIP;
+    cache[dev].cus = prop.multiProcessorCount;
+    cache[dev].gfx950 = strncmp(prop.gcnArchName, "gfx950", 6) == 0;
+    have[dev] = true;
+  }
+  *out = cache[dev];
+  return cache[dev].gfx950 ? ENGRAM_OK : ENGRAM_E_DEVICE;
+}
+
 namespace {
 
 constexpr uint32_t kSpinBudgetDefault = 1u << 22;  // ~1 s of sleeping polls before a wait gives up
@@ -27,28 +44,6 @@ constexpr int64_t kTiledMinTokens = 256;
 constexpr int64_t kTiledMinTokensFused = 65;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct DeviceInfo {
-  int cus = 0;
-  bool gfx950 = false;
-};
-
-// Per-device facts, queried once per device.
-engram_status device_info(DeviceInfo* out) {
-  static DeviceInfo cache[64];
-  static bool have[64] = {false};
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return ENGRAM_E_HIP;
-  if (!have[dev]) {
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return ENGRAM_E_HIP;
-    cache[dev].cus = prop.multiProcessorCount;
-    cache[dev].gfx950 = strncmp(prop.gcnArchName, "gfx950", 6) == 0;
-    have[dev] = true;
-  }
-  *out = cache[dev];
-  return cache[dev].gfx950 ? ENGRAM_OK : ENGRAM_E_DEVICE;
-}
 
 engram_status check_tokens(int64_t B, int64_t T, int64_t* M) {
   if (B < 0 || T < 0) return ENGRAM_E_SHAPE;

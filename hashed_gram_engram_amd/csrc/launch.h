@@ -5,7 +5,15 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/engram.h"
+
 namespace engram {
+
+struct DeviceInfo {
+  int cus = 0;
+  bool gfx950 = false;
+};
+engram_status device_info(DeviceInfo* out);  // of the current device; ENGRAM_E_DEVICE: not gfx950
 
 struct GatherArgs {
   const uint8_t* table;

@@ -253,6 +253,163 @@ engram_status engram_hash_ids(const engram_hash_layout* layout, const uint32_t* 
                               int64_t* history, int64_t* hash_ids, int32_t* err_count,
                               engram_stream_t stream);
 
+/* ---- The serving operators around the Engram forward ------------------------------------------
+ * A serving step of ragged requests: engram_batch_plan (where each request's tokens live),
+ * engram_hash_ids_paged (their row ids), engram_forward, then the block around it:
+ * engram_residual_norm (closes one block and opens the next) and engram_linear (a projection with
+ * bias, activation and residual).  The conventions above hold; none of them needs a workspace,
+ * none keeps state, and calls that write different buffers may overlap in time. */
+
+/* Storage of a residual stream (x, out of engram_residual_norm; residual, out of engram_linear). */
+typedef enum { ENGRAM_STREAM_BF16 = 0, ENGRAM_STREAM_FP32 = 1 } engram_stream_format;
+
+/* A pool of n_blocks pages of block_size positions; a request holds up to max_blocks of them.
+ * Page ids are int32; a slot is page * block_size + position % block_size (int64). */
+typedef struct {
+  int32_t block_size; /* >= 1 */
+  int32_t max_blocks; /* >= 1; max_blocks * block_size <= 2^30 */
+  int64_t n_blocks;   /* 1 .. 2^31 - 1 */
+} engram_page_layout;
+
+/* What engram_batch_plan writes, all device pointers, all required.  None may overlap an input. */
+typedef struct {
+  int32_t* token_start; /* [R + 1] first flat token of each request; [R] = admitted tokens */
+  int32_t* start_pos;   /* [R] position of the request's first new token (its cached length)   */
+  int32_t* seq_lens;    /* [R] length after this step: the next step's cached_lens             */
+  int32_t* status;      /* [R] 0 = planned; refused: 1 = past max_tokens, 2 = no page left,
+                           3 = a length outside [0, max_blocks * block_size]                   */
+  int32_t* free_left;   /* [1] pages left: the next step's free_count                          */
+  int64_t* slots;       /* [max_tokens] slot of each flat token, -1 behind the last            */
+  int32_t* positions;   /* [max_tokens] its position in its sequence, -1 behind the last       */
+  int32_t* requests;    /* [max_tokens] its request, -1 behind the last                        */
+  uint8_t* live;        /* [max_tokens] 1, or 0 behind the last (a token_mask of engram_forward) */
+} engram_batch_plan_out;
+
+/* Block tables and slot maps of one step, from its requests' lengths.  R requests (at most 4096):
+ *   new_lens    [R] int32  tokens this step adds: 0 = idle, negative = finished (its pages go back)
+ *   cached_lens [R] int32  tokens the request holds already
+ *   block_table [R, max_blocks] int32 in/out: entry b is the page of positions b * block_size ..;
+ *               the entries past ceil(cached_len / block_size) are not read; those the step needs
+ *               are written
+ *   free_list   [n_blocks] int32 in/out: a stack of free pages, its top at free_count[0] - 1
+ *   free_count  [1] int32 (clamped to [0, n_blocks])
+ * The pages of finished requests are put on the stack first, requests ascending, entries ascending
+ * (a page past n_blocks entries is dropped and counts an error).  Requests with new tokens are then
+ * admitted in order: first by tokens (the first request that would pass max_tokens, and every later
+ * one with new tokens, is refused with status 1), then by pages (the first that needs more than the
+ * stack holds, and every later one that needs a page, is refused with status 2).  A refused request
+ * keeps its state and gets no token in this step.  Pages are taken from the top of the stack,
+ * requests ascending, entries ascending.  The admitted requests' tokens are laid out one after the
+ * other: token i of request r is flat token token_start[r] + i, at position cached_lens[r] + i.
+ * A page id outside [0, n_blocks) gives its tokens slot -1; each such token and each refused
+ * request adds 1 to *err_count (may be NULL).
+ * The lengths and the count go out to other arrays than they came in by (start_pos, seq_lens,
+ * free_left), so the same call on the same inputs gives the same plan again. */
+engram_status engram_batch_plan(const engram_page_layout* layout, const int32_t* new_lens,
+                                const int32_t* cached_lens, int64_t R, int32_t* block_table,
+                                int32_t* free_list, const int32_t* free_count, int64_t max_tokens,
+                                const engram_batch_plan_out* plan, int32_t* err_count,
+                                engram_stream_t stream);
+
+/* engram_hash_ids for the ragged tokens of a plan, with the look-back history in pages:
+ *   token_map, multipliers, primes, offsets as in engram_hash_ids (layout->history_len is not used)
+ *   input_ids  [n_tokens] int64 raw ids of the flat tokens, n_tokens = the plan's max_tokens
+ *   token_mask [n_tokens] uint8 or NULL (all live): 0 = takes no part in an n-gram
+ *   slots, positions, requests [n_tokens], start_pos [R], block_table [R, max_blocks]: the plan's
+ *   history    [n_blocks, block_size] int64 in/out: compressed id of each slot
+ *   hash_ids   [n_layers, n_tokens, n_cols] int64 out
+ * A token at position p of request r reads look-back s from this call's tokens where p - s >=
+ * start_pos[r] (flat token i - s), else from history[block_table[r, (p - s) / block_size],
+ * (p - s) % block_size]; its own compressed id goes to history[slots[i]].  A token without a
+ * request (requests[i] outside [0, R)) gets the row ids of pad_id look-backs; its id is not read
+ * and no history is written.  A look-back whose page is outside [0, n_blocks) or whose entry is
+ * past max_blocks is dead and adds 1 to *err_count, as an id outside the map does; a slot outside
+ * the pool is not written. */
+engram_status engram_hash_ids_paged(const engram_hash_layout* layout, const engram_page_layout* pages,
+                                    const uint32_t* token_map, const int64_t* multipliers,
+                                    const int64_t* primes, const int64_t* offsets,
+                                    const int64_t* input_ids, const uint8_t* token_mask,
+                                    int64_t n_tokens, const int64_t* slots, const int32_t* positions,
+                                    const int32_t* requests, const int32_t* start_pos, int64_t R,
+                                    const int32_t* block_table, int64_t* history, int64_t* hash_ids,
+                                    int32_t* err_count, engram_stream_t stream);
+
+/* The gate of engram_residual_norm: none, one fp32 value per token and stream (what
+ * engram_gate_apply writes), or one bf16 logit per feature of y (the gate is its sigmoid). */
+typedef enum { ENGRAM_GATE_NONE = 0, ENGRAM_GATE_TOKEN = 1, ENGRAM_GATE_FEATURE = 2 } engram_gate_kind;
+
+typedef struct {
+  int32_t hc;            /* residual streams, 1 .. 64                                          */
+  int32_t dim;           /* features, a multiple of 8, at most 65536                           */
+  int32_t y_streams;     /* hc, or 1: one block output shared by every stream                  */
+  int32_t stream_format; /* engram_stream_format of x and out                                  */
+  int32_t gate;          /* engram_gate_kind                                                   */
+  int32_t post_norm;     /* 1: y is normalised before it is added                              */
+  int32_t pre_norm;      /* 1: h, the normalised stream for the next block, is written         */
+  float alpha, beta;     /* scales of the stream and of the block output; finite               */
+  float post_eps, pre_eps;
+} engram_norm_layout;
+
+/* Norms behind and before a block, with its gate and residual scale, in one pass:
+ *   x    [B, T, hc, dim] bf16 or fp32   the residual streams
+ *   y    [B, T, y_streams, dim] bf16    the block's output, y_stride elements from token to token
+ *        (a multiple of 8; e.g. the value part of engram_kv_proj's rows), NULL = no block before:
+ *        only h is computed, of x (out must be NULL)
+ *   gate [B, T, hc] fp32 (TOKEN), or [B, T, y_streams, dim] bf16, gate_stride elements from token to
+ *        token (FEATURE); NULL without a gate
+ *   post_weight, pre_weight [hc, dim] fp32, NULL = ones (post_weight also without post_norm: a
+ *        scale per feature)
+ *   token_mask [B, T] uint8, 0 = closed: the streams pass through bit for bit and y and the gate are
+ *        not looked at; NULL = all open
+ *   out  [B, T, hc, dim] in x's format; may be x
+ *   h    [B, T, hc, dim] bf16; NULL without pre_norm
+ * Per (token, stream s), fp32 throughout, rounded once on output:
+ *   n = y * rsqrt(mean(y^2) + post_eps) * post_weight,  r = alpha * x + beta * gate * n (closed: x),
+ *   out = r,  h = r * rsqrt(mean(r^2) + pre_eps) * pre_weight  (of r before its rounding). */
+engram_status engram_residual_norm(const engram_norm_layout* layout, const void* x, const uint16_t* y,
+                                   int64_t y_stride, const void* gate, int64_t gate_stride,
+                                   const float* post_weight, const float* pre_weight,
+                                   const uint8_t* token_mask, int64_t B, int64_t T, void* out,
+                                   uint16_t* h, engram_stream_t stream);
+
+/* Activations of engram_linear: z, max(z, 0), z Phi(z) with the normal distribution function Phi,
+ * z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2, z / (1 + exp(-z)), 1 / (1 + exp(-z)). */
+typedef enum {
+  ENGRAM_ACT_NONE = 0,
+  ENGRAM_ACT_RELU = 1,
+  ENGRAM_ACT_GELU = 2,
+  ENGRAM_ACT_GELU_TANH = 3,
+  ENGRAM_ACT_SILU = 4,
+  ENGRAM_ACT_SIGMOID = 5
+} engram_activation;
+
+typedef struct {
+  int32_t in_features;   /* K, a multiple of 8, at most 2^20                                   */
+  int32_t out_features;  /* N, 1 .. 2^24                                                       */
+  int32_t activation;    /* engram_activation                                                  */
+  int32_t glu;           /* 1: the weight has 2 N rows, N of the gate, then N of the value     */
+  int32_t stream_format; /* engram_stream_format of residual and out                           */
+} engram_linear_layout;
+
+/* Matrix product with bias, activation and residual:
+ *   x   [M, K] bf16, x_stride elements from row to row (a multiple of 8, at least K)
+ *   w   [N or 2 N, K] bf16 (Linear weight layout [out, in]); bias [N or 2 N] fp32 or NULL
+ *   residual, out [M, N] bf16 or fp32, their own strides (at least N); residual may be NULL, or out
+ *   out[m, n] = residual[m, n] + act(z[m, n])                        z = x w^T + bias
+ *   with glu:   residual[m, n] + act(z[m, n]) * z[m, N + n]
+ * fp32 accumulation, bias, activation and residual sum, rounded once to out.  out must not overlap
+ * x, w, or a residual at another address or stride.  residual and out need 16-byte alignment of
+ * their first element only (rows of odd lengths are fine).  M == 0 is a no-op. */
+engram_status engram_linear(const engram_linear_layout* layout, const uint16_t* x, int64_t x_stride,
+                            const uint16_t* w, const float* bias, const void* residual,
+                            int64_t residual_stride, int64_t M, void* out, int64_t out_stride,
+                            engram_stream_t stream);
+
+/* Host-only checks of the layouts above; no device work. */
+engram_status engram_page_layout_check(const engram_page_layout* layout);
+engram_status engram_norm_layout_check(const engram_norm_layout* layout);
+engram_status engram_linear_layout_check(const engram_linear_layout* layout);
+
 /* Static description of a status code. */
 const char* engram_status_str(engram_status status);
 
