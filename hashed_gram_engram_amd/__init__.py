@@ -99,7 +99,9 @@ _lib.engram_hash_ids_paged.argtypes = [ctypes.POINTER(HashLayout), ctypes.POINTE
                                        _i64, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp]
 _lib.engram_residual_norm.argtypes = [ctypes.POINTER(NormLayout), _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _vp,
                                       _vp, _vp]
-_lib.engram_linear.argtypes = [ctypes.POINTER(LinearLayout), _vp, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _i64, _vp]
+_lib.engram_linear.argtypes = [ctypes.POINTER(LinearLayout), _vp, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _sz, _vp]
+_lib.engram_linear_workspace_bytes.argtypes = [ctypes.POINTER(LinearLayout), _i64]
+_lib.engram_linear_workspace_bytes.restype = _sz
 _lib.engram_page_layout_check.argtypes = [ctypes.POINTER(PageLayout)]
 _lib.engram_norm_layout_check.argtypes = [ctypes.POINTER(NormLayout)]
 _lib.engram_linear_layout_check.argtypes = [ctypes.POINTER(LinearLayout)]
@@ -116,7 +118,7 @@ EXPORTED = ["engram_layout_check", "engram_param_counts", "engram_forward_worksp
             "engram_gather_dequant", "engram_kv_proj", "engram_gate_apply", "engram_forward",
             "engram_hash_ids", "engram_status_str", "engram_forward_check", "engram_set_spin_budget",
             "engram_forward_noalloc", "engram_batch_plan", "engram_hash_ids_paged", "engram_residual_norm",
-            "engram_linear", "engram_page_layout_check", "engram_norm_layout_check", "engram_linear_layout_check"]
+            "engram_linear", "engram_linear_workspace_bytes", "engram_page_layout_check", "engram_norm_layout_check", "engram_linear_layout_check"]
 
 
 SCALE_FP32, SCALE_E8M0 = 0, 1  # engram_scale_format
@@ -783,11 +785,18 @@ def make_linear_layout(in_features: int, out_features: int, activation: int = AC
     return LinearLayout(in_features, out_features, activation, bool(glu), stream_format)
 
 
+def engram_linear_workspace_bytes(layout: LinearLayout, M: int) -> int:
+    return int(_lib.engram_linear_workspace_bytes(ctypes.byref(layout), M))
+
+
 def engram_linear(layout: LinearLayout, x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
-                  residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                  residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """out [..., N] = residual + act(x [..., K] @ w^T + bias), or with the layout's glu
     residual + act(gate) * value from a weight of 2 N rows (engram_linear in include/engram.h).  x,
-    residual and out may be slices of wider rows; out may be the residual."""
+    residual and out may be slices of wider rows; out may be the residual.  Without a workspace
+    (engram_linear_workspace_bytes) the call takes one from torch's allocator where it needs one: calls
+    on other streams, and captured graphs, then have their own."""
     K, N = layout.in_features, layout.out_features
     if x.dtype != torch.bfloat16:
         raise TypeError(f"x has dtype {x.dtype}, expected {torch.bfloat16}")
@@ -811,7 +820,14 @@ def engram_linear(layout: LinearLayout, x: torch.Tensor, w: torch.Tensor, bias: 
     elif out.dtype != stream:
         raise TypeError(f"out has dtype {out.dtype}, expected {stream}")
     o_stride = _rows("out", out, lead, (N,))
-    _on(x.device, w, bias, residual, out)
+    _on(x.device, w, bias, residual, out, workspace)
+    if workspace is None:
+        need = _lib.engram_linear_workspace_bytes(layout, M)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    else:
+        _contig("workspace", workspace)
     _launch("engram_linear", x.device, _lib.engram_linear, layout, x.data_ptr(), x_stride, wp, bp, rp, r_stride, M,
-            out.data_ptr(), o_stride)
+            out.data_ptr(), o_stride, None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel() * workspace.element_size())
     return out

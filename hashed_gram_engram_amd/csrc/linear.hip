@@ -14,6 +14,8 @@
 //
 // Features past K (K is a multiple of 8) are copied from 16 zero bytes; weight rows past N and tokens
 // past M repeat the last one and are not stored.
+#include <math.h>
+
 #include "common.h"
 #include "serving.h"
 
@@ -23,39 +25,59 @@ namespace {
 
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
-__device__ const u32x4 kZero16 = {0u, 0u, 0u, 0u};
-
-constexpr int kStageB = 128;  // bytes of a row's stage: 64 features
-
 // ---------------------------------------------------------------- epilogue
-__device__ __forceinline__ float activate(float z, int act) {
-  switch (act) {
-    case 1: return fmaxf(z, 0.0f);
-    case 2: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-    // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
-    case 3: return z / (1.0f + expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
-    case 4: return z / (1.0f + expf(-z));
-    case 5: return 1.0f / (1.0f + expf(-z));
-    default: return z;
+// act(z) of 8 values; one branch for all of them.
+__device__ __forceinline__ void activate8(float (&z)[8], int act) {
+  if (act == 0) return;
+  if (act == 1) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = z[e] < 0.0f ? 0.0f : z[e];  // a NaN stays one
+  } else if (act == 2) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = 0.5f * z[e] * (1.0f + erff(z[e] * 0.70710678118654752f));
+  } else if (act == 5) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = 1.0f / (1.0f + expf(-z[e]));
+  } else {
+    // z / (1 + exp(-u)): u = z, or 2 sqrt(2 / pi) (z + 0.044715 z^3) since (1 + tanh v) / 2 = 1 / (1 + exp(-2 v))
+    const float c1 = act == 3 ? 1.5957691216057308f : 1.0f, c3 = act == 3 ? 0.071354816272f : 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = z[e] / (1.0f + expf(-z[e] * (c1 + c3 * z[e] * z[e])));
   }
 }
 
-// Columns c .. c + 3 of z, plus the bias of weight rows r .. r + 3 (rows past the last repeat it).
-__device__ __forceinline__ f32x4 add_bias(f32x4 z, const float* bias, int64_t row, int64_t last) {
-  if (bias == nullptr) return z;
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) z[e] += bias[row + e < last ? row + e : last];
-  return z;
+  for (int e = 0; e < 4; ++e) {
+    v[e] = a[e];
+    v[4 + e] = b[e];
+  }
 }
 
-// One row segment of 8 output features, fp32 -> out, with the residual.
-__device__ __forceinline__ void store8(const LinearArgs& a, int64_t m, int n, f32x4 lo, f32x4 hi, bool vec) {
-  float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+// bias[row .. row + 7] (`valid` of them are the weight's; the others, and all without a bias, 0).
+__device__ __forceinline__ void load_bias(const float* bias, int64_t row, int valid, float (&b)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) b[e] = 0.0f;
+  if (bias == nullptr) return;
+  if (valid >= 8 && (row & 3) == 0) {
+    load8(bias + row, b);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < valid) b[e] = bias[row + e];
+}
+
+// Output features n .. n + 7 of token m (those below N): v plus the residual, rounded once.
+__device__ __forceinline__ void store8(const LinearArgs& a, int64_t m, int n, float (&v)[8], bool vec) {
   const int64_t o = m * a.out_stride + n, q = m * a.residual_stride + n;
+  const bool whole = vec && n + 8 <= a.N;
   if (a.fp32) {
     float* out = static_cast<float*>(a.out) + o;
     const float* res = static_cast<const float*>(a.residual) + q;
-    if (vec && n + 8 <= a.N) {
+    if (whole) {
+      f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
       if (a.residual != nullptr) {
         lo += *reinterpret_cast<const f32x4*>(res);
         hi += *reinterpret_cast<const f32x4*>(res + 4);
@@ -64,13 +86,14 @@ __device__ __forceinline__ void store8(const LinearArgs& a, int64_t m, int n, f3
       *reinterpret_cast<f32x4*>(out + 4) = hi;
       return;
     }
+#pragma unroll
     for (int e = 0; e < 8; ++e)
       if (n + e < a.N) out[e] = v[e] + (a.residual != nullptr ? res[e] : 0.0f);
     return;
   }
   uint16_t* out = static_cast<uint16_t*>(a.out) + o;
   const uint16_t* res = static_cast<const uint16_t*>(a.residual) + q;
-  if (vec && n + 8 <= a.N) {
+  if (whole) {
     if (a.residual != nullptr) {
       const u32x4 w = *reinterpret_cast<const u32x4*>(res);
 #pragma unroll
@@ -83,6 +106,7 @@ __device__ __forceinline__ void store8(const LinearArgs& a, int64_t m, int n, f3
         u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
     return;
   }
+#pragma unroll
   for (int e = 0; e < 8; ++e)
     if (n + e < a.N)
       out[e] = uint16_t(pack_bf16x2(v[e] + (a.residual != nullptr ? bf16_lo(res[e]) : 0.0f), 0.0f));
@@ -101,46 +125,60 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// Floats of a row of a wave's epilogue buffer (16 bytes of padding: rows start on other banks).
+template <int TN>
+constexpr int epilogue_row() { return TN * 16 + 4; }
+template <int TN>
+constexpr int epilogue_bytes() { return 16 * epilogue_row<TN>() * 4; }
+
 // A wave's part of the tile: TN x TM blocks of 16 weight rows x 16 tokens, block (i, j) holding rows
 // 16 i + 4 (l >> 4) + 0..3 of token 16 j + (l & 15).  16 tokens at a time pass through the wave's own
-// piece of LDS (rows of W floats, 16 bytes of padding), so that stores are whole row segments.
+// piece of LDS, so that a lane gets 8 consecutive output features of a token (with GLU: blocks 2 i of
+// the gate, 2 i + 1 of the value) and stores are whole row segments.
 template <int TN, int TM, bool GLU>
 __device__ __forceinline__ void epilogue(const LinearArgs& a, const f32x4 (&acc)[TN][TM], char* lds, int64_t m0, int n0,
                                          int lane) {
-  constexpr int kBlocks = GLU ? TN / 2 : TN;
-  constexpr int kCols = kBlocks * 16;           // output features of the wave
-  constexpr int kRow = kCols + 4;               // floats per LDS row
-  constexpr int kLanes = kCols / 8;             // lanes per row when read back
-  constexpr int kRows = kWave / kLanes;         // rows per pass
+  constexpr int kRow = epilogue_row<TN>();
+  constexpr int kLanes = (GLU ? TN / 2 : TN) * 2;  // of 8 output features each
+  constexpr bool kFixed = kWave % kLanes == 0;     // a lane's features are the same in every pass
   float* buf = reinterpret_cast<float*>(lds);
   const bool vec = vector_rows(a);
-  const int64_t last = int64_t(a.N) - 1;
+  float b[8], bu[8];
+  auto biases = [&](int n) {
+    load_bias(a.bias, n, a.N - n, b);
+    if constexpr (GLU) load_bias(a.bias, int64_t(a.N) + n, a.N - n, bu);
+  };
+  if constexpr (kFixed) biases(n0 + 8 * (lane % kLanes));
+#pragma unroll 1
+  for (int jj = 0; jj < TM; ++jj) {
 #pragma unroll
-  for (int j = 0; j < TM; ++j) {
+    for (int j = 0; j < TM; ++j)
+      if (j == jj) {  // (registers have no index)
 #pragma unroll
-    for (int i = 0; i < kBlocks; ++i) {
-      const int c = 16 * i + 4 * (lane >> 4);
-      f32x4 z;
-      if constexpr (GLU) {
-        z = add_bias(acc[2 * i][j], a.bias, n0 + c, last);
-        const f32x4 u = add_bias(acc[2 * i + 1][j], a.bias, int64_t(a.N) + n0 + c, last + a.N);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) z[e] = activate(z[e], a.act) * u[e];
-      } else {
-        z = add_bias(acc[i][j], a.bias, n0 + c, last);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) z[e] = activate(z[e], a.act);
+        for (int i = 0; i < TN; ++i)
+          *reinterpret_cast<f32x4*>(buf + (lane & 15) * kRow + 16 * i + 4 * (lane >> 4)) = acc[i][j];
       }
-      *reinterpret_cast<f32x4*>(buf + (lane & 15) * kRow + c) = z;
-    }
     wave_lds_fence();
+#pragma unroll 1
+    for (int e = lane; e < 16 * kLanes; e += kWave) {
+      const int t = e / kLanes, c = 8 * (e - t * kLanes);
+      const int64_t m = m0 + 16 * jj + t;
+      const int n = n0 + c;
+      if (m >= a.M || n >= a.N) continue;
+      if constexpr (!kFixed) biases(n);
+      float z[8];
+      const float* p = buf + t * kRow + (GLU ? (c >> 4) * 32 + (c & 15) : c);
+      load8(p, z);
 #pragma unroll
-    for (int p = 0; p < 16; p += kRows) {
-      const int t = p + lane / kLanes, c = 8 * (lane % kLanes);
-      const int64_t m = m0 + 16 * j + t;
-      if ((kRows <= 16 || t < 16) && m < a.M && n0 + c < a.N)
-        store8(a, m, n0 + c, *reinterpret_cast<const f32x4*>(buf + t * kRow + c),
-               *reinterpret_cast<const f32x4*>(buf + t * kRow + c + 4), vec);
+      for (int k = 0; k < 8; ++k) z[k] += b[k];
+      activate8(z, a.act);
+      if constexpr (GLU) {
+        float u[8];
+        load8(p + 16, u);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) z[k] *= u[k] + bu[k];
+      }
+      store8(a, m, n, z, vec);
     }
     wave_lds_fence();
   }
@@ -151,6 +189,13 @@ template <int N>
 __device__ __forceinline__ void wait_copies() {
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// Every LDS read of the wave has returned.  (The builtin, not inline assembly: the compiler then knows
+// that the fragments are there and puts no wait of its own behind the next reads.)
+__device__ __forceinline__ void wait_reads() {
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_sched_barrier(0);
 }
 __device__ __forceinline__ void group_barrier() {
   __builtin_amdgcn_sched_barrier(0);
@@ -174,48 +219,180 @@ __device__ __forceinline__ int64_t xcd_tile(int64_t b, int64_t tiles) {
   return x * q + (x < rem ? x : rem) + (b >> 3);
 }
 
+constexpr int kBK = 64;         // features of a stage
+constexpr int kRowB = kBK * 2;  // bytes of a row of a stage
+
+// 16-byte chunk c of row r of a stage lies at position c ^ swizzle(r): the 16 rows of a fragment read
+// cover all 64 banks once.
+__device__ __forceinline__ int swizzle(int r) { return (r >> 1) & 7; }
+
+// Tiles in order: groups of 8 token blocks, and in a group token blocks fastest, so that the tiles that
+// run on an XCD at one time share token panels as well as weight panels in its L2.
+__device__ __forceinline__ void tile_of(int64_t tile, int64_t tbs, int64_t cbs, int64_t* tb, int64_t* cb) {
+  constexpr int64_t kGroup = 8;
+  const int64_t g = tile / (kGroup * cbs), in = tile - g * kGroup * cbs;
+  const int64_t size = tbs - g * kGroup < kGroup ? tbs - g * kGroup : kGroup;
+  *tb = g * kGroup + in % size;
+  *cb = in / size;
+}
+
+// What a workgroup computes: a tile, and of its K the whole stages [first, first + stages) and, in the
+// last part, the features past the last whole stage.  Split over K, part 0 of every tile comes first:
+// the workgroups of an XCD then share panels as without a split.
+struct Share {
+  int64_t tile, tb, cb;
+  int part, first, stages;
+  bool tail;
+};
+__device__ __forceinline__ Share share_of(const LinearArgs& a, int64_t tbs, int64_t cbs) {
+  Share s;
+  const int64_t tiles = tbs * cbs, at = xcd_tile(blockIdx.x, gridDim.x);
+  s.part = int(at / tiles);
+  s.tile = at - s.part * tiles;
+  tile_of(s.tile, tbs, cbs, &s.tb, &s.cb);
+  const int S = a.K / kBK;
+  s.first = int(int64_t(S) * s.part / a.parts);
+  s.stages = int(int64_t(S) * (s.part + 1) / a.parts) - s.first;
+  s.tail = s.part == a.parts - 1 && a.K % kBK != 0;
+  return s;
+}
+
+// The features past the last whole stage: fragments straight from memory, zeros past K.  r0: the wave's
+// first row of the tile, m0: its first token.
+template <int TN, int TM, bool GLU>
+__device__ __forceinline__ void tail(const LinearArgs& a, f32x4 (&acc)[TN][TM], int64_t n0, int r0, int64_t m0, int lane) {
+  const int r16 = lane & 15, g = lane >> 4;
+#pragma unroll 1
+  for (int k0 = a.K / kBK * kBK; k0 < a.K; k0 += 32) {
+    const int k = k0 + 8 * g;
+    u32x4 x[TM];
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      const int64_t m = m0 + j * 16 + r16;
+      x[j] = k < a.K ? *reinterpret_cast<const u32x4*>(a.x + (m < a.M ? m : a.M - 1) * a.x_stride + k)
+                     : u32x4{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      const u32x4 w = k < a.K ? *reinterpret_cast<const u32x4*>(a.w + weight_row<GLU>(a, n0, r0 + i * 16 + r16) * a.K + k)
+                              : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int j = 0; j < TM; ++j) acc[i][j] = mfma16x16x32(w, x[j], acc[i][j]);
+    }
+  }
+}
+
+// Split over K: a wave's fp32 blocks in the order it holds them, 1 KB a block, at wave slot `at` of the
+// workspace.
+template <int TN, int TM>
+__device__ __forceinline__ void store_partial(const LinearArgs& a, const f32x4 (&acc)[TN][TM], int64_t at, int lane) {
+  f32x4* p = reinterpret_cast<f32x4*>(a.partials) + at * (TN * TM * kWave) + lane;
+#pragma unroll
+  for (int i = 0; i < TN; ++i)
+#pragma unroll
+    for (int j = 0; j < TM; ++j) p[(i * TM + j) * kWave] = acc[i][j];
+}
+
+// Adds the parts of a wave's blocks in order and finishes them.  One wave per workgroup.
+template <int BM, int BN, int WM, int WN, bool GLU>
+__global__ __launch_bounds__(kWave) void k_linear_join(LinearArgs a) {
+  constexpr int TM = BM / WM / 16, TN = BN / WN / 16, kOutCols = GLU ? BN / 2 : BN;
+  __shared__ __attribute__((aligned(16))) char lds[epilogue_bytes<TN>()];
+  const int lane = threadIdx.x;
+  const int64_t tbs = (a.M + BM - 1) / BM, cbs = (int64_t(a.N) + kOutCols - 1) / kOutCols, slots = tbs * cbs * WM * WN;
+  const int64_t at = blockIdx.x;
+  const int wv = int(at % (WM * WN));
+  int64_t tb, cb;
+  tile_of(at / (WM * WN), tbs, cbs, &tb, &cb);
+  const f32x4* p = reinterpret_cast<const f32x4*>(a.partials) + at * (TN * TM * kWave) + lane;
+  f32x4 acc[TN][TM];
+#pragma unroll
+  for (int i = 0; i < TN; ++i)
+#pragma unroll
+    for (int j = 0; j < TM; ++j) acc[i][j] = p[(i * TM + j) * kWave];
+  for (int part = 1; part < a.parts; ++part) {
+    p += slots * (TN * TM * kWave);
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j) acc[i][j] += p[(i * TM + j) * kWave];
+  }
+  // which part of the tile a wave holds: as in k_linear_big (the 256 x 256 tile) and k_linear
+  constexpr bool kGroups = BM == 256 && BN == 256;
+  const int wm = kGroups ? wv % WM : wv / WN, wn = kGroups ? wv / WM : wv % WN;
+  epilogue<TN, TM, GLU>(a, acc, lds, tb * BM + wm * TM * 16, int(cb * kOutCols) + wn * (GLU ? TN * 8 : TN * 16), lane);
+}
+
+// Orders one region of the K loop: R fragment reads, M MFMAs and C copies, the reads first and the
+// copies spread out, each behind an MFMA.  A copy instruction occupies a CU's address unit for 16
+// cycles and an MFMA its matrix unit for 16: a burst of either stalls the wave that the other needs.
+template <int R, int M, int C>
+__device__ __forceinline__ void interleave() {
+  constexpr int kMfma = 0x8, kVmem = 0x20, kRead = 0x100;
+  // the reads over the first three quarters of the MFMAs, the copies over all of them
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    const int r0 = min(R, i * R * 4 / (3 * M)), r1 = min(R, (i + 1) * R * 4 / (3 * M));
+    const int c0 = i * C / M, c1 = (i + 1) * C / M;
+    if (r1 > r0) __builtin_amdgcn_sched_group_barrier(kRead, 1, 0);
+    if (r1 > r0 + 1) __builtin_amdgcn_sched_group_barrier(kRead, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+    if (c1 > c0) __builtin_amdgcn_sched_group_barrier(kVmem, 1, 0);
+  }
+}
+
 template <int BM, int BN, int WM, int WN, int ST, bool GLU>
-__global__ __launch_bounds__(WM* WN* kWave) void k_linear(LinearArgs a) {
+__global__ __launch_bounds__(WM* WN* kWave, BM / WM * BN / WN > 8192 ? 1 : 2) void k_linear(LinearArgs a) {
   constexpr int kWaves = WM * WN;
-  constexpr int kRowsT = BM + BN;                 // rows of a stage
-  constexpr int kSlot = kRowsT * kStageB;
-  constexpr int kCopies = kRowsT / 8 / kWaves;    // copy instructions per wave and stage, 8 rows each
+  constexpr int kRowsT = BM + BN;                 // rows of a stage: the weight's, then the tokens'
+  constexpr int kSlot = kRowsT * kRowB;
+  constexpr int kAll = kRowsT / 8;                // copy instructions of a stage
+  constexpr int kCopies = kAll / kWaves;          // of one wave
+  constexpr int kFirst = kCopies / 2;             // of these, issued in the second half of a stage
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
   constexpr int kOutCols = GLU ? BN / 2 : BN;
-  static_assert(kRowsT % (8 * kWaves) == 0 && (!GLU || TN % 2 == 0), "tile");
-  constexpr int kEpi = 16 * ((GLU ? TN / 2 : TN) * 16 + 4) * 4;  // bytes of a wave's epilogue buffer
+  static_assert(kAll % kWaves == 0 && BN % 16 == 0 && (!GLU || TN % 2 == 0), "tile");
+  constexpr int kEpi = epilogue_bytes<TN>();
   static_assert(kEpi * kWaves <= ST * kSlot, "epilogue buffer");
   extern __shared__ __attribute__((aligned(16))) char lds[];
 
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t tbs = (a.M + BM - 1) / BM;
-  const int64_t tile = xcd_tile(blockIdx.x, gridDim.x);
-  const int64_t m0 = (tile % tbs) * BM;
-  const int64_t n0 = (tile / tbs) * kOutCols;
-  const int S = (a.K + 63) / 64;
+  const int64_t tbs = (a.M + BM - 1) / BM, cbs = (int64_t(a.N) + kOutCols - 1) / kOutCols;
+  const Share sh = share_of(a, tbs, cbs);
+  const int64_t m0 = sh.tb * BM, n0 = sh.cb * kOutCols;
+  const int S = sh.stages;
 
-  // lane l of a copy fills bytes 16 l of 1 KB: row 8 q + (l >> 3), position l & 7, chunk (l & 7) ^ (l >> 3)
-  const int rr = lane >> 3, chunk = (lane & 7) ^ rr;
-  const char* src[kCopies];
+  const int turned = S > 0 ? int(sh.cb % S) : 0;
+
+  // lane l of copy q fills bytes 16 l of 1 KB: row 8 q + l / 8, position l % 8.  Its 8 rows start at
+  // a wave-uniform address; the lane's part is a 32-bit offset.
+  const char* base[kCopies];
+  uint32_t off[kCopies];
 #pragma unroll
   for (int i = 0; i < kCopies; ++i) {
-    const int r = (wv * kCopies + i) * 8 + rr;
+    const int r = (wv * kCopies + i) * 8;
+    const uint32_t at = 16 * ((lane & 7) ^ swizzle(r + (lane >> 3)));
     if (r < BN) {
-      src[i] = reinterpret_cast<const char*>(a.w + weight_row<GLU>(a, n0, r) * a.K) + 16 * chunk;
+      const int64_t first = weight_row<GLU>(a, n0, r);
+      base[i] = reinterpret_cast<const char*>(a.w + first * a.K);
+      off[i] = uint32_t(weight_row<GLU>(a, n0, r + (lane >> 3)) - first) * uint32_t(a.K) * 2 + at;
     } else {
-      int64_t m = m0 + r - BN;
-      m = m < a.M ? m : a.M - 1;
-      src[i] = reinterpret_cast<const char*>(a.x + m * a.x_stride) + 16 * chunk;
+      const int64_t last = a.M - 1, m = m0 + r - BN, first = m < last ? m : last;
+      base[i] = reinterpret_cast<const char*>(a.x + first * a.x_stride);
+      const int64_t mine = m + (lane >> 3) < last ? m + (lane >> 3) : last;
+      off[i] = uint32_t(mine - first) * uint32_t(a.x_stride) * 2 + at;
     }
   }
-  auto copy_stage = [&](int t) {
-    char* dst = lds + (t % ST) * kSlot;
-    const bool past = t * 64 + 8 * chunk >= a.K;
+  // copies i0 .. i1 - 1 of stage t; stages past the last repeat it (into a slot that nobody reads any
+  // more), so that every turn has issued the same number of copies
+  auto copy = [&](int t, int slot, int i0, int i1) {
+    char* dst = lds + slot * kSlot + wv * kCopies * 1024;
+    int k = (t < S ? t : S - 1) + turned;
+    k = k < S ? k : k - S;
+    const size_t at = size_t(sh.first + k) * kRowB;
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i) {
-      const char* s = past ? reinterpret_cast<const char*>(&kZero16) : src[i] + size_t(t) * kStageB;
-      __builtin_amdgcn_global_load_lds((const void*)s, (lds_ptr_t)(dst + (wv * kCopies + i) * 1024), 16, 0, 0);
-    }
+    for (int i = i0; i < i1; ++i)
+      __builtin_amdgcn_global_load_lds((const void*)(base[i] + at + off[i]), (lds_ptr_t)(dst + i * 1024), 16, 0, 0);
   };
 
   f32x4 acc[TN][TM];
@@ -226,62 +403,380 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_linear(LinearArgs a) {
 
   const int wn = wv % WN, wm = wv / WN;
   const int r16 = lane & 15, g = lane >> 4;
-  for (int t = 0; t < ST - 1 && t < S; ++t) copy_stage(t);
-  for (int t = 0; t < S; ++t) {
-    // stage t has landed when only the copies of the ST - 2 stages behind it are in flight
-    if (S - 1 - t >= ST - 2) wait_copies<(ST - 2) * kCopies>();
-    else wait_copies<0>();
-    group_barrier();  // everyone's copies of stage t; everyone is done with stage t - 1
-    if (t + ST - 1 < S) copy_stage(t + ST - 1);
-    const char* W = lds + (t % ST) * kSlot + wn * TN * 16 * kStageB;
-    const char* X = lds + (t % ST) * kSlot + (BN + wm * TM * 16) * kStageB;
+  struct Frags {
+    u32x4 w[TN], x[TM];
+  };
+  const int w_off = (wn * TN * 16 + r16) * kRowB, x_off = (BN + wm * TM * 16 + r16) * kRowB;
+  auto read = [&](Frags& f, int slot, int hh) {
+    const char* b = lds + slot * kSlot + 16 * ((4 * hh + g) ^ swizzle(r16));
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      const int off = r16 * kStageB + 16 * ((4 * hh + g) ^ (r16 & 7));
-      u32x4 fw[TN], fx[TM];
+    for (int i = 0; i < TN; ++i) f.w[i] = *reinterpret_cast<const u32x4*>(b + w_off + i * 16 * kRowB);
 #pragma unroll
-      for (int i = 0; i < TN; ++i) fw[i] = *reinterpret_cast<const u32x4*>(W + i * 16 * kStageB + off);
+    for (int j = 0; j < TM; ++j) f.x[j] = *reinterpret_cast<const u32x4*>(b + x_off + j * 16 * kRowB);
+  };
+  auto multiply = [&](const Frags& f) {
 #pragma unroll
-      for (int j = 0; j < TM; ++j) fx[j] = *reinterpret_cast<const u32x4*>(X + j * 16 * kStageB + off);
+    for (int i = 0; i < TN; ++i)
 #pragma unroll
-      for (int i = 0; i < TN; ++i)
+      for (int j = 0; j < TM; ++j) acc[i][j] = mfma16x16x32(f.w[i], f.x[j], acc[i][j]);
+  };
+  if (S > 0) {
 #pragma unroll
-        for (int j = 0; j < TM; ++j) acc[i][j] = mfma16x16x32(fw[i], fx[j], acc[i][j]);
+    for (int t = 0; t < ST - 1; ++t) copy(t, t, 0, kCopies);
+    copy(ST - 1, ST - 1, 0, kFirst);
+    wait_copies<(ST - 2) * kCopies + kFirst>();
+    group_barrier();
+    Frags f[2];
+    read(f[0], 0, 0);
+    int slot = 0, before = ST - 1;
+    for (int t = 0; t < S; ++t) {
+      const int next = slot + 1 == ST ? 0 : slot + 1;
+      wait_reads();
+      // first half; the rest of stage t - 1 + ST goes into stage t - 1's slot
+      read(f[1], slot, 1);
+      multiply(f[0]);
+      copy(t - 1 + ST, before, kFirst, kCopies);
+      interleave<TN + TM, TN * TM, kCopies - kFirst>();
+      // Stage t + 1 is in LDS for everyone once only the copies of stages t + 2 .. t + ST - 1 are in
+      // flight, and nobody reads stage t's slot any more once every wave has its last fragments.
+      wait_copies<(ST - 2) * kCopies>();
+      wait_reads();
+      group_barrier();
+      // second half; stage t + ST starts into stage t's slot
+      read(f[0], next, 0);  // (past the last stage: a repeat, not used)
+      multiply(f[1]);
+      copy(t + ST, slot, 0, kFirst);
+      interleave<TN + TM, TN * TM, kFirst>();
+      __builtin_amdgcn_sched_barrier(0);
+      before = slot;
+      slot = next;
     }
+    wait_copies<0>();
+  }
+  if (sh.tail) {
+    tail<TN, TM, GLU>(a, acc, n0, wn * TN * 16, m0 + wm * TM * 16, lane);
+  }
+  if (a.parts > 1) {
+    store_partial<TN, TM>(a, acc, (sh.part * tbs * cbs + sh.tile) * kWaves + wv, lane);
+    return;
   }
   __syncthreads();  // the ring is free
   epilogue<TN, TM, GLU>(a, acc, lds + wv * kEpi, m0 + wm * TM * 16, int(n0) + wn * (GLU ? TN * 8 : TN * 16), lane);
 }
 
-template <int BM, int BN, int WM, int WN, int ST, bool GLU>
-hipError_t launch_tile(const LinearArgs& a, hipStream_t stream) {
-  constexpr int kOut = GLU ? BN / 2 : BN;
-  constexpr int kBytes = ST * (BM + BN) * kStageB;
-  const int64_t tiles = (a.M + BM - 1) / BM * ((int64_t(a.N) + kOut - 1) / kOut);
-  if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
-  const void* fn = reinterpret_cast<const void*>(&k_linear<BM, BN, WM, WN, ST, GLU>);
-  if constexpr (kBytes > 65536) {
-    const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, kBytes);
-    if (e != hipSuccess) return e;
+// ---------------------------------------------------------------- tiles of 256 x 256
+// Eight waves, two per SIMD.  Waves 0-3 (group 0) own weight rows 0-127 of the tile, waves 4-7
+// (group 1) rows 128-255; in a group, wave w & 3 owns tokens 64 (w & 3) .. + 63, so a wave holds 8 x 4
+// blocks.  The groups alternate: while one group's wave of a SIMD issues the 32 MFMAs of half a
+// stage, the other's reads the fragments of its half; a barrier separates the phases, four to a stage.
+//
+// Weight stages have a ring of three slots and are copied two stages ahead, token stages a ring of two
+// (5 x 32 KB).  Stage J is multiplied in phases 4 J .. 4 J + 3 and its last fragments are read in phase
+// 4 J + 2.  Every wave issues 2 copies in every phase: the tokens of stage J + 1 in phases 4 J - 1 and
+// 4 J, the weight rows of stage J + 2 in 4 J + 1 and 4 J + 2 (both slots held stage J - 1).  At the end
+// of phase 4 J + 2 a wave waits until only its 4 weight copies of stage J + 2 are in flight: stage
+// J + 1 is then there for its first reader (group 0, phase 4 J + 3).  Copies past the last stage
+// repeat it, so that the counts hold.  (The 64 copies of a stage take the CU's memory path about 1600
+// cycles, its 4 phases of MFMAs 2048: copies in one phase would make that phase three times as long.)
+constexpr int kBig = 256;
+constexpr int kOpB = kBig * kRowB;  // one operand of one stage
+constexpr int kBigLds = 5 * kOpB;   // weight slots 0..2, token slots 3, 4
+typedef f32x4 BigAcc[8][4];
+
+struct BigPipe {
+  const char* w_base[4];
+  const char* x_base[4];
+  uint32_t w_off[4], x_off[4];
+  uint32_t frag[2];  // per-lane byte offset of a fragment read (half 0, 1)
+  int wv, w_row, x_row;  // wave; byte offsets of its first weight and token row
+};
+
+__device__ __forceinline__ void big_copy(const char* const (&base)[4], const uint32_t (&off)[4], char* slot, int wv,
+                                         int t, int i) {
+  __builtin_amdgcn_global_load_lds((const void*)(base[i] + size_t(t) * kRowB + off[i]),
+                                   (lds_ptr_t)(slot + (4 * wv + i) * 1024), 16, 0, 0);
+}
+__device__ __forceinline__ void big_read(u32x4 (&F)[12], const BigPipe& p, const char* W, const char* X, int hh) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) F[i] = *reinterpret_cast<const u32x4*>(W + p.w_row + p.frag[hh] + i * 16 * kRowB);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) F[8 + j] = *reinterpret_cast<const u32x4*>(X + p.x_row + p.frag[hh] + j * 16 * kRowB);
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+}
+__device__ __forceinline__ void big_mma(BigAcc& acc, const u32x4 (&F)[12], int i0, int i1) {
+#pragma unroll
+  for (int i = i0; i < i1; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = mfma16x16x32(F[i], F[8 + j], acc[i][j]);
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+template <int G>
+__device__ __forceinline__ void big_loop(BigAcc& acc, const BigPipe& p, char* lds, int s0, int S, int turned) {
+  u32x4 F[12];
+  auto stage = [&](int t) {
+    const int k = (t < S ? t : S - 1) + turned;
+    return s0 + (k < S ? k : k - S);
+  };
+  // the two copies of a phase: tokens (weight rows) i, i + 1 of stage t
+  auto tokens = [&](int t, int i) {
+    big_copy(p.x_base, p.x_off, lds + (3 + (t & 1)) * kOpB, p.wv, stage(t), i);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto weights = [&](int t, int slot, int i) {
+    big_copy(p.w_base, p.w_off, lds + slot * kOpB, p.wv, stage(t), i);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) weights(0, 0, i);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) tokens(0, i);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) weights(1, 1, i);
+  tokens(1, 0);
+  tokens(1, 1);
+  wait_copies<6>();
+  group_barrier();
+  if constexpr (G == 0) big_read(F, p, lds, lds + 3 * kOpB, 0);
+  group_barrier();
+  int w0 = 0;  // weight slot of stage J
+  for (int J = 0; J < S; ++J) {
+    const int w1 = w0 == 2 ? 0 : w0 + 1, w2 = w1 == 2 ? 0 : w1 + 1;
+    const char* W = lds + w0 * kOpB;
+    const char* X = lds + (3 + (J & 1)) * kOpB;
+    if constexpr (G == 0) {
+      big_mma(acc, F, 0, 3);  // 4 J: half 0
+      tokens(J + 1, 2);
+      big_mma(acc, F, 3, 6);
+      tokens(J + 1, 3);
+      big_mma(acc, F, 6, 8);
+      group_barrier();
+      weights(J + 2, w2, 0);  // 4 J + 1: read half 1
+      weights(J + 2, w2, 1);
+      big_read(F, p, W, X, 1);
+      group_barrier();
+      big_mma(acc, F, 0, 3);  // 4 J + 2: half 1
+      weights(J + 2, w2, 2);
+      big_mma(acc, F, 3, 6);
+      weights(J + 2, w2, 3);
+      big_mma(acc, F, 6, 8);
+      wait_copies<4>();
+      group_barrier();
+      tokens(J + 2, 0);  // 4 J + 3: read half 0 of stage J + 1
+      tokens(J + 2, 1);
+      big_read(F, p, lds + w1 * kOpB, lds + (3 + ((J + 1) & 1)) * kOpB, 0);
+      group_barrier();
+    } else {
+      tokens(J + 1, 2);  // 4 J: read half 0
+      tokens(J + 1, 3);
+      big_read(F, p, W, X, 0);
+      group_barrier();
+      big_mma(acc, F, 0, 3);  // 4 J + 1: half 0
+      weights(J + 2, w2, 0);
+      big_mma(acc, F, 3, 6);
+      weights(J + 2, w2, 1);
+      big_mma(acc, F, 6, 8);
+      group_barrier();
+      weights(J + 2, w2, 2);  // 4 J + 2: read half 1
+      weights(J + 2, w2, 3);
+      big_read(F, p, W, X, 1);
+      wait_copies<4>();
+      group_barrier();
+      big_mma(acc, F, 0, 3);  // 4 J + 3: half 1
+      tokens(J + 2, 0);
+      big_mma(acc, F, 3, 6);
+      tokens(J + 2, 1);
+      big_mma(acc, F, 6, 8);
+      group_barrier();
+    }
+    w0 = w1;
   }
-  LinearArgs args = a;
-  void* params[] = {&args};
-  return hipLaunchKernel(fn, dim3(unsigned(tiles)), dim3(WM * WN * kWave), params, kBytes, stream);
+  wait_copies<0>();
+  group_barrier();
 }
 
 template <bool GLU>
-hipError_t launch_any(const LinearArgs& a, hipStream_t stream) {
-  if (a.M <= 16) return launch_tile<32, 64, 2, 2, 4, GLU>(a, stream);
-  if (a.M <= 64) return launch_tile<64, 64, 2, 2, 3, GLU>(a, stream);
-  return launch_tile<128, 128, 2, 2, 2, GLU>(a, stream);
+__global__ __launch_bounds__(512, 2) void k_linear_big(LinearArgs a) {
+  constexpr int kOut = GLU ? kBig / 2 : kBig;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t tbs = (a.M + kBig - 1) / kBig, cbs = (int64_t(a.N) + kOut - 1) / kOut;
+  const Share sh = share_of(a, tbs, cbs);
+  const int64_t m0 = sh.tb * kBig, n0 = sh.cb * kOut;
+  BigPipe p;
+  p.wv = wv;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = (4 * wv + i) * 8, mine = r + (lane >> 3);
+    const uint32_t at = 16 * ((lane & 7) ^ swizzle(mine));
+    const int64_t row = weight_row<GLU>(a, n0, r);
+    p.w_base[i] = reinterpret_cast<const char*>(a.w + row * a.K);
+    p.w_off[i] = uint32_t(weight_row<GLU>(a, n0, mine) - row) * uint32_t(a.K) * 2 + at;
+    const int64_t last = a.M - 1, first = m0 + r < last ? m0 + r : last, m = m0 + mine < last ? m0 + mine : last;
+    p.x_base[i] = reinterpret_cast<const char*>(a.x + first * a.x_stride);
+    p.x_off[i] = uint32_t(m - first) * uint32_t(a.x_stride) * 2 + at;
+  }
+  const int r16 = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int hh = 0; hh < 2; ++hh) p.frag[hh] = uint32_t(r16 * kRowB + 16 * ((4 * hh + g) ^ swizzle(r16)));
+  p.w_row = (wv >> 2) * 128 * kRowB;
+  p.x_row = (wv & 3) * 64 * kRowB;
+  BigAcc acc;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (sh.stages > 0) {
+    const int turned = int(sh.cb % sh.stages);
+    if (wv < 4) big_loop<0>(acc, p, lds, sh.first, sh.stages, turned);
+    else big_loop<1>(acc, p, lds, sh.first, sh.stages, turned);
+  }
+  if (sh.tail) tail<8, 4, GLU>(a, acc, n0, (wv >> 2) * 128, m0 + (wv & 3) * 64, lane);
+  if (a.parts > 1) {
+    store_partial<8, 4>(a, acc, (sh.part * tbs * cbs + sh.tile) * 8 + wv, lane);
+    return;
+  }
+  constexpr int kEpi = epilogue_bytes<8>();
+  epilogue<8, 4, GLU>(a, acc, lds + wv * kEpi, m0 + (wv & 3) * 64, int(n0) + (wv >> 2) * (GLU ? 64 : 128), lane);
+}
+
+// Launches `fn` over `tiles` tiles times a.parts parts, then the kernel that joins the parts.
+hipError_t launch_parts(const LinearArgs& a, const void* fn, int bytes, int waves, const void* join, int64_t tiles,
+                        hipStream_t stream) {
+  if (a.parts < 1 || tiles > 0x7FFFFFFF / a.parts || tiles * waves > 0x7FFFFFFF) return hipErrorInvalidValue;
+  hipError_t e = bytes > 65536 ? hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) : hipSuccess;
+  if (e != hipSuccess) return e;
+  LinearArgs args = a;
+  void* params[] = {&args};
+  e = hipLaunchKernel(fn, dim3(unsigned(tiles * a.parts)), dim3(waves * kWave), params, bytes, stream);
+  if (e != hipSuccess || a.parts == 1) return e;
+  return hipLaunchKernel(join, dim3(unsigned(tiles * waves)), dim3(kWave), params, 0, stream);
+}
+
+template <bool GLU>
+hipError_t launch_big(const LinearArgs& a, hipStream_t stream) {
+  constexpr int kOut = GLU ? kBig / 2 : kBig;
+  const int64_t tiles = (a.M + kBig - 1) / kBig * ((int64_t(a.N) + kOut - 1) / kOut);
+  return launch_parts(a, reinterpret_cast<const void*>(&k_linear_big<GLU>), kBigLds, 8,
+                      reinterpret_cast<const void*>(&k_linear_join<kBig, kBig, 4, 2, GLU>), tiles, stream);
+}
+
+template <int BM, int BN, int WM, int WN, int ST, bool GLU>
+hipError_t launch_tile(const LinearArgs& a, hipStream_t stream) {
+  constexpr int kOut = GLU ? BN / 2 : BN;
+  constexpr int kBytes = ST * (BM + BN) * kRowB;
+  static_assert(kBytes <= 160 * 1024, "LDS");
+  const int64_t tiles = (a.M + BM - 1) / BM * ((int64_t(a.N) + kOut - 1) / kOut);
+  return launch_parts(a, reinterpret_cast<const void*>(&k_linear<BM, BN, WM, WN, ST, GLU>), kBytes, WM * WN,
+                      reinterpret_cast<const void*>(&k_linear_join<BM, BN, WM, WN, GLU>), tiles, stream);
+}
+
+// ---------------------------------------------------------------- choice of tile and split
+// Tiles: tokens x weight rows, waves, ring slots (0: k_linear_big).  The gated form needs an even number
+// of 16-row blocks per wave, hence other shapes here and there.
+struct TileShape {
+  int bm, bn, waves, slots;
+};
+constexpr TileShape kTiles[2][15] = {
+    {{256, 256, 8, 0}, {128, 256, 8, 3}, {256, 128, 8, 3}, {160, 160, 4, 3}, {128, 160, 4, 4}, {192, 128, 4, 4},
+     {128, 128, 4, 4}, {128, 128, 4, 2}, {64, 256, 8, 4}, {64, 128, 4, 6}, {64, 64, 4, 4}, {32, 128, 4, 6},
+     {32, 64, 4, 8}, {32, 32, 2, 8}, {16, 16, 1, 12}},
+    {{256, 256, 8, 0}, {128, 256, 8, 3}, {256, 128, 8, 3}, {160, 128, 4, 4}, {128, 192, 4, 4}, {192, 128, 4, 4},
+     {128, 128, 4, 4}, {128, 128, 4, 2}, {64, 256, 8, 4}, {64, 128, 4, 6}, {64, 64, 4, 4}, {32, 128, 4, 6},
+     {32, 64, 4, 8}, {32, 32, 2, 8}, {16, 32, 1, 12}}};
+
+template <bool GLU>
+hipError_t launch_shape(int tile, const LinearArgs& a, hipStream_t stream) {
+  switch (tile) {
+    case 0: return launch_big<GLU>(a, stream);
+    case 1: return launch_tile<128, 256, 4, 2, 3, GLU>(a, stream);
+    case 2: return launch_tile<256, 128, 4, 2, 3, GLU>(a, stream);
+    case 3: return launch_tile<160, GLU ? 128 : 160, 2, 2, GLU ? 4 : 3, GLU>(a, stream);
+    case 4: return launch_tile<128, GLU ? 192 : 160, 2, 2, 4, GLU>(a, stream);
+    case 5: return launch_tile<192, 128, 2, 2, 4, GLU>(a, stream);
+    case 6: return launch_tile<128, 128, 2, 2, 4, GLU>(a, stream);
+    case 7: return launch_tile<128, 128, 2, 2, 2, GLU>(a, stream);
+    case 8: return launch_tile<64, 256, 2, 4, 4, GLU>(a, stream);
+    case 9: return launch_tile<64, 128, 2, 2, 6, GLU>(a, stream);
+    case 10: return launch_tile<64, 64, 2, 2, 4, GLU>(a, stream);
+    case 11: return launch_tile<32, 128, 1, 4, 6, GLU>(a, stream);
+    case 12: return launch_tile<32, 64, GLU ? 2 : 1, GLU ? 2 : 4, 8, GLU>(a, stream);
+    case 13: return launch_tile<32, 32, GLU ? 2 : 1, GLU ? 1 : 2, 8, GLU>(a, stream);
+    case 14: return launch_tile<16, GLU ? 32 : 16, 1, 1, 12, GLU>(a, stream);
+  }
+  return hipErrorInvalidValue;
+}
+
+// Microseconds that a tile shape and a split take, as a model of what bounds them: per stage and
+// compute unit, the copies (68 KB per us into its LDS) or the MFMAs (8.4 TFLOP/s); per round of
+// workgroups a prologue and an epilogue; over all, the bytes at 5.7 TB/s; the parts written and read at
+// 6.4 TB/s and a second launch.  Fitted to 75 shapes, 1..8192 tokens, K 128..10240, N 72..25600, with every
+// tile and split timed: the choice is within 3% of the best one on average (15% at worst; the first rule,
+// by token count alone, was 60% above it).
+double model_us(const TileShape& t, int parts, int64_t M, int K, int64_t rows, int64_t N, int cus) {
+  const double tiles = double((M + t.bm - 1) / t.bm) * double((rows + t.bn - 1) / t.bn);
+  const int lds = t.slots == 0 ? kBigLds : t.slots * (t.bm + t.bn) * kRowB;
+  int fit = 160 * 1024 / lds;  // workgroups of a compute unit
+  const int by_waves = t.waves >= 4 ? 8 / t.waves : 8;
+  fit = fit < by_waves ? fit : by_waves;
+  const double work = tiles * parts, stages = K / 64.0 / parts;
+  double n = ceil(work / cus);
+  n = n < fit ? n : fit;
+  double rounds = work / (cus * n);
+  rounds = rounds < 4 ? ceil(rounds) : rounds + 0.5;
+  const double copies = n * (t.bm + t.bn) * kRowB / 1024 / 68.0, mfma = n * t.bm * t.bn * 128 / 8.4e6;
+  double stage = copies > mfma ? copies : mfma;
+  stage = stage > 0.08 ? stage : 0.08;
+  const double tile_us = 1.0 + rounds * (stages * stage + 2.8 + t.bm * t.bn * 1.85e-4);
+  const double mem_us = 1.0 + 2.0 * (double(M) * K + double(rows) * K + double(M) * N) / 5.7e6;
+  double us = tile_us > mem_us ? tile_us + 0.2 * mem_us : mem_us + 0.2 * tile_us;
+  if (parts > 1) us += 2.4 + parts * tiles * t.bm * t.bn * 8 / 6.4e6;
+  return us;
+}
+
+constexpr int64_t kMostPartBytes = int64_t(512) << 20;
+
+// The tile, the parts and the bytes of their workspace.
+struct LinearChoice {
+  int tile = 0, parts = 1;
+  int64_t bytes = 0;
+};
+LinearChoice choose(int64_t M, int K, int N, bool glu, int cus) {
+  LinearChoice best;
+  double least = 1e30;
+  const int64_t rows = glu ? 2 * int64_t(N) : N;
+  for (int i = 0; i < 15; ++i) {
+    const TileShape& t = kTiles[glu][i];
+    const int64_t tiles = (M + t.bm - 1) / t.bm * ((rows + t.bn - 1) / t.bn);
+    if (tiles > (int64_t(1) << 24)) continue;  // far below what a launch takes
+    for (int parts : {1, 2, 3, 4, 6, 8}) {
+      const int64_t bytes = parts > 1 ? tiles * parts * t.bm * t.bn * 4 : 0;
+      // split only while the parts fill the device at most about three times and are not too short
+      if (parts > 1 && (tiles * parts > 3 * cus || K / 64 / parts < 4 || bytes > kMostPartBytes)) break;
+      const double us = model_us(t, parts, M, K, rows, N, cus);
+      if (us < least) {
+        least = us;
+        best.tile = i;
+        best.parts = parts;
+        best.bytes = bytes;
+      }
+    }
+  }
+  return best;
 }
 
 }  // namespace
 
-hipError_t launch_linear(const LinearArgs& a, int num_cus, hipStream_t stream) {
-  (void)num_cus;
+int64_t linear_workspace_bytes(int64_t M, int K, int N, bool glu, int cus) {
+  return M > 0 ? choose(M, K, N, glu, cus).bytes : 0;
+}
+
+hipError_t launch_linear(const LinearArgs& a, int cus, hipStream_t stream) {
   if (a.M <= 0) return hipSuccess;
-  return a.glu ? launch_any<true>(a, stream) : launch_any<false>(a, stream);
+  const LinearChoice c = choose(a.M, a.K, a.N, a.glu != 0, cus);
+  LinearArgs args = a;
+  args.parts = c.parts;
+  return a.glu ? launch_shape<true>(c.tile, args, stream) : launch_shape<false>(c.tile, args, stream);
 }
 
 }  // namespace engram

@@ -75,7 +75,13 @@ struct LinearArgs {
   int64_t M, x_stride, residual_stride, out_stride;
   int K, N;  // N: output features (the weight has 2 N rows with glu)
   int act, glu, fp32;
+  // split over K: parts > 1 leave their fp32 blocks in `partials`, a second kernel joins them
+  int parts;
+  float* partials;
 };
-hipError_t launch_linear(const LinearArgs& a, int num_cus, hipStream_t stream);
+// Bytes of `partials` (16-byte aligned) that launch_linear needs on a device of `cus` compute units; 0
+// where it does not split K.
+int64_t linear_workspace_bytes(int64_t M, int K, int N, bool glu, int cus);
+hipError_t launch_linear(const LinearArgs& a, int cus, hipStream_t stream);  // (sets a.parts itself)
 
 }  // namespace engram

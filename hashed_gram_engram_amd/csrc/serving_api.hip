@@ -205,9 +205,16 @@ engram_status engram_residual_norm(const engram_norm_layout* l, const void* x, c
   return launched(launch_residual_norm(a, hip_stream(stream)));
 }
 
+size_t engram_linear_workspace_bytes(const engram_linear_layout* l, int64_t M) {
+  if (engram_linear_layout_check(l) != ENGRAM_OK || M <= 0 || M > 0x7FFFFFFF) return 0;
+  DeviceInfo di;
+  const int cus = device_info(&di) == ENGRAM_OK ? di.cus : 256;
+  return size_t(linear_workspace_bytes(M, l->in_features, l->out_features, l->glu != 0, cus));
+}
+
 engram_status engram_linear(const engram_linear_layout* l, const uint16_t* x, int64_t x_stride, const uint16_t* w,
                             const float* bias, const void* residual, int64_t residual_stride, int64_t M, void* out,
-                            int64_t out_stride, engram_stream_t stream) {
+                            int64_t out_stride, void* workspace, size_t workspace_bytes, engram_stream_t stream) {
   engram_status st = engram_linear_layout_check(l);
   if (st != ENGRAM_OK) return st;
   if (M < 0 || M > 0x7FFFFFFF) return ENGRAM_E_SHAPE;
@@ -215,11 +222,11 @@ engram_status engram_linear(const engram_linear_layout* l, const uint16_t* x, in
   if (!x || !w || !out) return ENGRAM_E_NULL;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 16) || !aligned(residual, 16) || !aligned(out, 16))
     return ENGRAM_E_ALIGN;
-  if (x_stride < l->in_features || x_stride % 8 != 0 || out_stride < l->out_features) return ENGRAM_E_SHAPE;
+  if (x_stride < l->in_features || x_stride % 8 != 0 || x_stride > (int64_t(1) << 28) || out_stride < l->out_features) return ENGRAM_E_SHAPE;
   if (residual != nullptr && residual_stride < l->out_features) return ENGRAM_E_SHAPE;
   // offsets into a tensor stay far from 64 bits
   const int64_t far = (int64_t(1) << 56) / M;
-  if (x_stride > far || out_stride > far || (residual != nullptr && residual_stride > far)) return ENGRAM_E_SHAPE;
+  if (out_stride > far || (residual != nullptr && residual_stride > far)) return ENGRAM_E_SHAPE;
   if (residual == out && residual_stride != out_stride) return ENGRAM_E_SHAPE;
   DeviceInfo di;
   if ((st = device_info(&di)) != ENGRAM_OK) return st;
@@ -239,6 +246,10 @@ engram_status engram_linear(const engram_linear_layout* l, const uint16_t* x, in
   a.act = l->activation;
   a.glu = l->glu;
   a.fp32 = l->stream_format == ENGRAM_STREAM_FP32;
+  const int64_t need = linear_workspace_bytes(M, a.K, a.N, a.glu != 0, di.cus);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < size_t(need) || !aligned(workspace, 16)))
+    return ENGRAM_E_WORKSPACE;
+  a.partials = static_cast<float*>(workspace);
   return launched(launch_linear(a, di.cus, hip_stream(stream)));
 }
 

@@ -392,7 +392,7 @@ typedef struct {
 } engram_linear_layout;
 
 /* Matrix product with bias, activation and residual:
- *   x   [M, K] bf16, x_stride elements from row to row (a multiple of 8, at least K)
+ *   x   [M, K] bf16, x_stride elements from row to row (a multiple of 8, K .. 2^28)
  *   w   [N or 2 N, K] bf16 (Linear weight layout [out, in]); bias [N or 2 N] fp32 or NULL
  *   residual, out [M, N] bf16 or fp32, their own strides (at least N); residual may be NULL, or out
  *   out[m, n] = residual[m, n] + act(z[m, n])                        z = x w^T + bias
@@ -403,7 +403,13 @@ typedef struct {
 engram_status engram_linear(const engram_linear_layout* layout, const uint16_t* x, int64_t x_stride,
                             const uint16_t* w, const float* bias, const void* residual,
                             int64_t residual_stride, int64_t M, void* out, int64_t out_stride,
-                            engram_stream_t stream);
+                            void* workspace, size_t workspace_bytes, engram_stream_t stream);
+
+/* Bytes of workspace engram_linear needs for M rows on the current device: room for the fp32 partial
+ * tiles where K is split (shapes with few tiles), else 0 (workspace may then be NULL).  Its contents need
+ * no clearing and mean nothing after the call; calls that overlap in time (other streams, captured
+ * graphs) must use different workspaces. */
+size_t engram_linear_workspace_bytes(const engram_linear_layout* layout, int64_t M);
 
 /* Host-only checks of the layouts above; no device work. */
 engram_status engram_page_layout_check(const engram_page_layout* layout);

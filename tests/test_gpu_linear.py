@@ -26,11 +26,24 @@ SIZES = [(1, 64, 16), (1, 8, 1), (1, 5120, 5120), (2, 72, 33), (5, 1000, 257), (
          (200, 2048, 1280), (257, 1288, 513), (300, 8, 700), (512, 512, 2048), (777, 1032, 777), (1025, 256, 1281)]
 
 
-@pytest.mark.parametrize("M,K,N", SIZES)
-def test_exact_on_whole_numbers(M, K, N):
+# shapes that take every tile, whole and split over K (plain, then gated), as engram_linear chooses them on
+# 256 compute units; odd on purpose in tokens, features and the rest of K past whole stages
+TILES = [(2067, 256, 4991), (1803, 832, 3400), (822, 4912, 3006), (512, 4560, 5198), (1537, 312, 3597), (136, 5144, 3845),
+         (1678, 120, 2371), (1887, 5352, 260), (822, 280, 5993), (161, 3840, 5879), (385, 64, 4707), (65, 4816, 5955),
+         (1043, 64, 3868), (1594, 64, 2501), (163, 3536, 5707), (229, 416, 4108), (35, 4008, 5463), (202, 64, 4108),
+         (68, 3168, 2882), (2048, 4096, 4096), (1000, 10240, 5120)]
+GATED_TILES = [(963, 248, 4830), (1561, 840, 1828), (331, 4936, 2714), (1163, 1032, 3214), (194, 4736, 4267), (391, 120, 4618),
+               (146, 4336, 1833), (323, 280, 5664), (66, 4072, 5545), (925, 304, 3182), (173, 4016, 2770), (67, 4688, 2727),
+               (385, 64, 4707), (258, 64, 5478), (180, 3296, 2738), (33, 2936, 4279), (71, 64, 4218), (73, 3392, 1381),
+               (691, 3888, 17), (301, 5120, 10240)]
+
+
+@pytest.mark.parametrize("M,K,N,glus", [(*s, (False, True)) for s in SIZES] + [(*s, (False,)) for s in TILES] +
+                         [(*s, (True,)) for s in GATED_TILES])
+def test_exact_on_whole_numbers(M, K, N, glus):
     say(f"[gpu] linear: {M} x {K} x {N}, whole numbers")
     g = torch.Generator(device="cuda").manual_seed(M * 7 + N)
-    for glu in (False, True):
+    for glu in glus:
         rows = 2 * N if glu else N
         x, w, b, r = whole(g, M, K), whole(g, rows, K), whole(g, rows), whole(g, M, N)
         # |z| <= 9 K + 3 < 2^17; gated products are kept below 2^24 by a sparse weight
@@ -165,3 +178,59 @@ def test_on_a_side_stream_and_captured():
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(out, ref), (M, k)
+
+
+def test_workspace_is_checked_and_kept_to():
+    say("[gpu] linear: a caller's workspace, one that is too small, bytes around it")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    M, K, N = 100, 5120, 1030
+    l = lay(K, N, fp32=True)
+    need = eg.engram_linear_workspace_bytes(l, M)
+    assert need > 0 and eg.engram_linear_workspace_bytes(lay(64, 64), 4) == 0
+    x, w = whole(g, M, K).bfloat16(), whole(g, N, K).bfloat16()
+    ref = x.double() @ w.double().T
+    buf = torch.full((need + 512,), 171, dtype=torch.uint8, device="cuda")
+    got = eg.engram_linear(l, x, w, workspace=buf[256:256 + need])
+    assert torch.equal(got.double(), ref) and (buf[:256] == 171).all() and (buf[256 + need:] == 171).all()
+    out = torch.full((M, N), 3.0, device="cuda")
+    for bad in (buf[:need - 16], buf[8:8 + need]):
+        with pytest.raises(eg.EngramError) as e:
+            eg.engram_linear(l, x, w, out=out, workspace=bad)
+        assert e.value.status == -5
+    torch.cuda.synchronize()
+    assert (out == 3).all()
+
+
+def test_split_calls_at_the_same_time():
+    say("[gpu] linear: split calls on two streams, and two captured graphs replayed together")
+    g = torch.Generator(device="cuda").manual_seed(6)
+    M, K, N = 100, 5120, 1030
+    l = lay(K, N, fp32=True)
+    assert eg.engram_linear_workspace_bytes(l, M) > 0
+    xs = [whole(g, M, K).bfloat16() for _ in range(2)]
+    w = whole(g, N, K).bfloat16()
+    refs = [x.double() @ w.double().T for x in xs]
+    outs = [torch.empty((M, N), device="cuda") for _ in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for x, o, s in zip(xs, outs, streams):
+            with torch.cuda.stream(s):
+                eg.engram_linear(l, x, w, out=o)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o.double(), r) for o, r in zip(outs, refs))
+    graphs = []
+    for x, o in zip(xs, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            eg.engram_linear(l, x, w, out=o)
+    for k in range(3):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for _ in range(10):
+            for gr, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    gr.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o.double(), r) for o, r in zip(outs, refs)), k

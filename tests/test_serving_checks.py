@@ -116,14 +116,14 @@ def test_linear_refusals():
     lay = eg.make_linear_layout(64, 40)
 
     def call(layout=lay, x=P, xs=64, w=P, b=None, r=None, rs=0, M=3, out=P, os=40):
-        return LIB.engram_linear(layout, x, xs, w, b, r, rs, M, out, os, None)
+        return LIB.engram_linear(layout, x, xs, w, b, r, rs, M, out, os, None, 0, None)
     assert call(layout=eg.make_linear_layout(60, 40)) == -2
     assert call(M=-1) == -3 and call(M=1 << 31) == -3 and call(M=0, x=None, w=None, out=None) == 0
     for k in ("x", "w", "out"):
         assert call(**{k: None}) == -1 and call(**{k: HALF}) == -4, k
     assert call(b=HALF) == -4 and call(r=HALF, rs=40) == -4
     assert call(xs=56) == -3 and call(xs=68) == -3 and call(os=39) == -3 and call(r=HALF.__class__(1 << 13), rs=39) == -3
-    assert call(xs=1 << 60) == -3
+    assert call(xs=(1 << 28) + 8) == -3 and call(os=1 << 60) == -3
     assert call(r=P, rs=48, out=P, os=40) == -3  # in place with another stride
 
 
