@@ -6,8 +6,10 @@
 // to the last store: x, y and a gate per feature are read once, r and h written once.  The two sums
 // are fp32: NV * 8 squares in a thread, then a tree over the T threads.
 //
-// What bounds it: HBM for long inputs (x and y read, r and h written); launch and one memory round
-// trip for a decode step.
+// What bounds it: HBM for long inputs (x and y read, r and h written: 8192 tokens x 4 streams x 5120 with a
+// shared y move 1.09 GB in 231 us, 4.7 TB/s, where a large copy reaches 4.8); launch and a chain of memory
+// round trips for a decode step (64 such tokens 4.7 us).  r and h are stored past the caches (nothing of
+// this launch reads them again): 244 -> 231 us.
 #include "common.h"
 #include "serving.h"
 
@@ -82,6 +84,23 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_residual_norm(NormArgs a)
       if (open) yv[k] = *reinterpret_cast<const u32x4*>(a.y + m * a.y_stride + int64_t(ys) * a.dim + 8 * v);
     }
   }
+  // with few vectors a thread (short inputs: the time is a chain of memory round trips) the weights are
+  // fetched along with them
+  constexpr bool kEarly = NV <= 2;
+  float wp[kEarly ? NV : 1][8], wh[kEarly ? NV : 1][8];
+  auto weight = [&](const float* w, int k, float (&to)[8]) {
+    const int v = lane + k * T;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) to[e] = 1.0f;
+    if (w != nullptr && v < nvec) load8(w + int64_t(s) * a.dim + 8 * v, to);
+  };
+  if constexpr (kEarly) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      if (open) weight(a.post_weight, k, wp[k]);
+      if (a.h != nullptr) weight(a.pre_weight, k, wh[k]);
+    }
+  }
   float scale = a.beta;
   if (a.gate_kind == 1 && open) scale *= static_cast<const float*>(a.gate)[row];
   if (a.post_norm && has_y) {
@@ -105,9 +124,9 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_residual_norm(NormArgs a)
       unpack8(yv[k], n);
       if (a.post_weight != nullptr) {
         float w[8];
-        load8(a.post_weight + int64_t(s) * a.dim + 8 * v, w);
+        if constexpr (!kEarly) weight(a.post_weight, k, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) n[e] *= w[e];
+        for (int e = 0; e < 8; ++e) n[e] *= kEarly ? wp[kEarly ? k : 0][e] : w[e];
       }
       if (a.gate_kind == 2) {
         float z[8];
@@ -127,10 +146,10 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_residual_norm(NormArgs a)
       if (v >= nvec) continue;
       if constexpr (FP32) {
         float* o = static_cast<float*>(a.out) + row * a.dim + 8 * v;
-        *reinterpret_cast<f32x4*>(o) = f32x4{r[k][0], r[k][1], r[k][2], r[k][3]};
-        *reinterpret_cast<f32x4*>(o + 4) = f32x4{r[k][4], r[k][5], r[k][6], r[k][7]};
+        __builtin_nontemporal_store(f32x4{r[k][0], r[k][1], r[k][2], r[k][3]}, reinterpret_cast<f32x4*>(o));
+        __builtin_nontemporal_store(f32x4{r[k][4], r[k][5], r[k][6], r[k][7]}, reinterpret_cast<f32x4*>(o + 4));
       } else {
-        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + row * a.dim + 8 * v) = pack8(r[k]);
+        __builtin_nontemporal_store(pack8(r[k]), reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + row * a.dim + 8 * v));
       }
     }
   }
@@ -151,11 +170,11 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_residual_norm(NormArgs a)
       for (int e = 0; e < 8; ++e) n[e] = r[k][e] * rstd;
       if (a.pre_weight != nullptr) {
         float w[8];
-        load8(a.pre_weight + int64_t(s) * a.dim + 8 * v, w);
+        if constexpr (!kEarly) weight(a.pre_weight, k, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) n[e] *= w[e];
+        for (int e = 0; e < 8; ++e) n[e] *= kEarly ? wh[kEarly ? k : 0][e] : w[e];
       }
-      *reinterpret_cast<u32x4*>(a.h + row * a.dim + 8 * v) = pack8(n);
+      __builtin_nontemporal_store(pack8(n), reinterpret_cast<u32x4*>(a.h + row * a.dim + 8 * v));
     }
   }
 }
@@ -172,20 +191,37 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
   return hipLaunchKernel(fn, dim3(unsigned(grid)), dim3(T < 256 ? 256 : T), params, 0, stream);
 }
 
+template <int T>
+hipError_t launch_threads(const NormArgs& a, hipStream_t stream) {
+  const int nv = ((a.dim >> 3) + T - 1) / T;
+  if (nv <= 1) return launch_norm<T, 1>(a, stream);
+  if (nv <= 2) return launch_norm<T, 2>(a, stream);
+  if (nv <= 3) return launch_norm<T, 3>(a, stream);
+  if (nv <= 4) return launch_norm<T, 4>(a, stream);
+  if (nv <= 5) return launch_norm<T, 5>(a, stream);
+  if constexpr (T == 1024)
+    if (nv <= 8) return launch_norm<T, 8>(a, stream);
+  return hipErrorInvalidValue;
+}
+
 }  // namespace
 
-hipError_t launch_residual_norm(const NormArgs& a, hipStream_t stream) {
+// Threads of a row: as few as hold it in 5 vectors each, so that a long input's waves have many loads in
+// flight and sum with few barriers; while the rows leave threads of the device idle (2048 fit a compute
+// unit) twice as many, up to one vector each.  Measured at dim 5120: 32,768 rows 231 us with 128 threads
+// a row, 328 us with 512; 256 rows 6.9 us with 128, 4.7 us with 512.
+hipError_t launch_residual_norm(const NormArgs& a, int cus, hipStream_t stream) {
   const int nvec = a.dim >> 3;
-  if (nvec <= 64) return launch_norm<64, 1>(a, stream);
-  if (nvec <= 128) return launch_norm<64, 2>(a, stream);
-  if (nvec <= 256) return launch_norm<128, 2>(a, stream);
-  if (nvec <= 512) return launch_norm<128, 4>(a, stream);
-  if (nvec <= 640) return launch_norm<128, 5>(a, stream);
-  if (nvec <= 1024) return launch_norm<256, 4>(a, stream);
-  if (nvec <= 2048) return launch_norm<256, 8>(a, stream);
-  if (nvec <= 4096) return launch_norm<1024, 4>(a, stream);
-  if (nvec <= 8192) return launch_norm<1024, 8>(a, stream);
-  return hipErrorInvalidValue;
+  int t = 64;
+  while (t < 1024 && nvec > 5 * t) t *= 2;
+  while (t < 1024 && 2 * t <= nvec && a.M * a.hc * 2 * t <= int64_t(2048) * cus) t *= 2;
+  switch (t) {
+    case 64: return launch_threads<64>(a, stream);
+    case 128: return launch_threads<128>(a, stream);
+    case 256: return launch_threads<256>(a, stream);
+    case 512: return launch_threads<512>(a, stream);
+    default: return launch_threads<1024>(a, stream);
+  }
 }
 
 }  // namespace engram

@@ -64,7 +64,7 @@ struct NormArgs {
   int hc, dim, y_streams, gate_kind, post_norm, fp32;
   float alpha, beta, post_eps, pre_eps;
 };
-hipError_t launch_residual_norm(const NormArgs& a, hipStream_t stream);
+hipError_t launch_residual_norm(const NormArgs& a, int cus, hipStream_t stream);
 
 struct LinearArgs {
   const uint16_t* x;

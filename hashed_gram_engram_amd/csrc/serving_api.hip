@@ -24,7 +24,7 @@ extern "C" {
 
 engram_status engram_page_layout_check(const engram_page_layout* l) {
   if (l == nullptr) return ENGRAM_E_NULL;
-  if (l->block_size < 1 || l->max_blocks < 1 || l->n_blocks < 1 || l->n_blocks > 0x7FFFFFFF) return ENGRAM_E_LAYOUT;
+  if (l->block_size < 1 || l->max_blocks < 1 || l->n_blocks < 1 || l->n_blocks > (int64_t(1) << 30)) return ENGRAM_E_LAYOUT;
   if (int64_t(l->block_size) * l->max_blocks > (int64_t(1) << 30)) return ENGRAM_E_LAYOUT;
   return ENGRAM_OK;
 }
@@ -202,7 +202,7 @@ engram_status engram_residual_norm(const engram_norm_layout* l, const void* x, c
   a.beta = l->beta;
   a.post_eps = l->post_eps;
   a.pre_eps = l->pre_eps;
-  return launched(launch_residual_norm(a, hip_stream(stream)));
+  return launched(launch_residual_norm(a, di.cus, hip_stream(stream)));
 }
 
 size_t engram_linear_workspace_bytes(const engram_linear_layout* l, int64_t M) {
