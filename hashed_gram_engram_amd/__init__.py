@@ -566,38 +566,48 @@ STREAM_BF16, STREAM_FP32 = 0, 1                    # engram_stream_format
 GATE_NONE, GATE_TOKEN, GATE_FEATURE = 0, 1, 2      # engram_gate_kind
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU, ACT_SIGMOID = range(6)  # engram_activation
 
-_STREAM = {STREAM_BF16: torch.bfloat16, STREAM_FP32: torch.float32}
+
+# the HIP stream handle of a device's current stream (torch.cuda.current_stream, without the object)
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _launch(where: str, device: torch.device, fn, *args) -> None:
-    """Calls a C entry point on `device`'s current stream (as its last argument), with that device
-    current for the call."""
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+def _launch(where: str, device: int, fn, *args) -> None:
+    """Calls a C entry point on the current stream of the device (as its last argument), with that
+    device current for the call.  device: the tensors' index, -1 for host memory."""
+    if device < 0:
+        raise ValueError("tensors must be on a GPU, got cpu")
+    if device == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(device))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            st = fn(*args, _raw_stream(device))
     if st != ENGRAM_OK:
         raise EngramError(where, st)
 
 
-def _tensor(name: str, t: torch.Tensor, shape: tuple, dtype) -> int:
-    """The address of a contiguous tensor of this shape and dtype."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+def _tensor(name: str, t: torch.Tensor, shape: tuple, dtype, device: int) -> int:
+    """The address of a contiguous tensor of this shape and dtype on the device."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        if t.dtype != dtype:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        raise ValueError(f"{name} is on {t.device}, not with the other tensors")
     return t.data_ptr()
 
 
-def _rows(name: str, t: torch.Tensor, lead: tuple, row: tuple) -> int:
-    """The stride in elements between the rows of a tensor [*lead, *row] whose rows are contiguous
-    and evenly spaced."""
-    if t.shape != (*lead, *row):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(*lead, *row)}")
-    size = math.prod(row)
+def _rows(name: str, t: torch.Tensor, lead: tuple, row: tuple, dtype, device: int) -> int:
+    """The stride in elements between the rows of a tensor [*lead, *row] of this dtype whose rows are
+    contiguous and evenly spaced."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != lead + row:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {lead + row}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not with the other tensors")
+    size = row[0] if len(row) == 1 else row[0] * row[1]
     if t.is_contiguous():
         return size
     n, want, step = len(lead), 1, t.stride()
@@ -606,7 +616,6 @@ def _rows(name: str, t: torch.Tensor, lead: tuple, row: tuple) -> int:
             raise ValueError(f"{name}: the last {len(row)} dimensions must be contiguous")
         want *= row[d]
     stride = None
-    want = 0
     for d in range(n - 1, -1, -1):
         if lead[d] == 1:
             continue
@@ -618,12 +627,13 @@ def _rows(name: str, t: torch.Tensor, lead: tuple, row: tuple) -> int:
     return size if stride is None else stride
 
 
-def _on(device: torch.device, *ts) -> None:
-    if device.type != "cuda":
-        raise ValueError(f"tensors must be on a GPU, got {device}")
-    for t in ts:
-        if t is not None and t.device != device:
-            raise ValueError(f"a tensor is on {t.device}, expected {device}")
+def _counter(err_count: Optional[torch.Tensor], device: int):
+    if err_count is None:
+        return None
+    _check_err(err_count)
+    if err_count.get_device() != device:
+        raise ValueError(f"err_count is on {err_count.device}, not with the other tensors")
+    return err_count.data_ptr()
 
 
 def make_page_layout(block_size: int, max_blocks: int, n_blocks: int) -> PageLayout:
@@ -655,27 +665,24 @@ def engram_batch_plan(layout: PageLayout, new_lens: torch.Tensor, cached_lens: t
     """Plans a step of ragged requests into `plan` (engram_batch_plan in include/engram.h): admits
     requests by tokens and pages, takes and gives back pages (block_table [R, max_blocks] and
     free_list [n_blocks] are updated in place), and lays out the admitted tokens."""
-    R, i32 = plan.n_requests, torch.int32
-    new = _tensor("new_lens", new_lens, (R,), i32)
-    held = _tensor("cached_lens", cached_lens, (R,), i32)
-    table = _tensor("block_table", block_table, (R, layout.max_blocks), i32)
-    pool = _tensor("free_list", free_list, (layout.n_blocks,), i32)
-    count = _tensor("free_count", free_count, (1,), i32)
-    _check_err(err_count)
+    R, T, i32, dev = plan.n_requests, plan.max_tokens, torch.int32, free_list.get_device()
+    new = _tensor("new_lens", new_lens, (R,), i32, dev)
+    held = _tensor("cached_lens", cached_lens, (R,), i32, dev)
+    table = _tensor("block_table", block_table, (R, layout.max_blocks), i32, dev)
+    pool = _tensor("free_list", free_list, (layout.n_blocks,), i32, dev)
+    count = _tensor("free_count", free_count, (1,), i32, dev)
     # the plan's buffers are attributes: they may have been replaced since it was made
-    out = _PlanOut(_tensor("plan.token_start", plan.token_start, (R + 1,), i32),
-                   _tensor("plan.start_pos", plan.start_pos, (R,), i32),
-                   _tensor("plan.seq_lens", plan.seq_lens, (R,), i32),
-                   _tensor("plan.status", plan.status, (R,), i32),
-                   _tensor("plan.free_left", plan.free_left, (1,), i32),
-                   _tensor("plan.slots", plan.slots, (plan.max_tokens,), torch.int64),
-                   _tensor("plan.positions", plan.positions, (plan.max_tokens,), i32),
-                   _tensor("plan.requests", plan.requests, (plan.max_tokens,), i32),
-                   _tensor("plan.live", plan.live, (plan.max_tokens,), torch.uint8))
-    _on(free_list.device, new_lens, cached_lens, block_table, free_count, err_count, plan.token_start, plan.start_pos,
-        plan.seq_lens, plan.status, plan.free_left, plan.slots, plan.positions, plan.requests, plan.live)
-    _launch("engram_batch_plan", free_list.device, _lib.engram_batch_plan, layout, new, held, R, table, pool, count,
-            plan.max_tokens, out, None if err_count is None else err_count.data_ptr())
+    out = _PlanOut(_tensor("plan.token_start", plan.token_start, (R + 1,), i32, dev),
+                   _tensor("plan.start_pos", plan.start_pos, (R,), i32, dev),
+                   _tensor("plan.seq_lens", plan.seq_lens, (R,), i32, dev),
+                   _tensor("plan.status", plan.status, (R,), i32, dev),
+                   _tensor("plan.free_left", plan.free_left, (1,), i32, dev),
+                   _tensor("plan.slots", plan.slots, (T,), torch.int64, dev),
+                   _tensor("plan.positions", plan.positions, (T,), i32, dev),
+                   _tensor("plan.requests", plan.requests, (T,), i32, dev),
+                   _tensor("plan.live", plan.live, (T,), torch.uint8, dev))
+    _launch("engram_batch_plan", dev, _lib.engram_batch_plan, layout, new, held, R, table, pool, count, T, out,
+            _counter(err_count, dev))
     return plan
 
 
@@ -686,36 +693,27 @@ def engram_hash_ids_paged(layout: HashLayout, pages: PageLayout, token_map: torc
     """Row ids [n_layers, n_tokens, (max_ngram - 1) * n_heads] int64 of a plan's flat tokens input_ids
     [plan.max_tokens] (engram_hash_ids_paged in include/engram.h); history [n_blocks, block_size]
     int64, addressed through the plan and block_table, is read and updated in place."""
-    n, R, i64, i32 = plan.max_tokens, plan.n_requests, torch.int64, torch.int32
-    cols = (layout.max_ngram - 1) * layout.n_heads
-    if token_map.dtype == torch.int32:
-        tmap = _tensor("token_map", token_map, (layout.vocab,), torch.int32)
-    else:
-        tmap = _tensor("token_map", token_map, (layout.vocab,), torch.uint32)
-    mult = _tensor("multipliers", multipliers, (layout.n_layers, layout.max_ngram), i64)
-    _numel("primes", primes, (layout.n_layers, layout.max_ngram - 1, layout.n_heads))
-    _contig("primes", primes, i64)
-    _numel("offsets", offsets, (layout.n_layers, cols))
-    _contig("offsets", offsets, i64)
-    ids = _tensor("input_ids", input_ids, (n,), i64)
+    n, R, i64, i32, dev = plan.max_tokens, plan.n_requests, torch.int64, torch.int32, input_ids.get_device()
+    layers, heads, orders = layout.n_layers, layout.n_heads, layout.max_ngram - 1
+    tmap = _tensor("token_map", token_map, (layout.vocab,), i32 if token_map.dtype is i32 else torch.uint32, dev)
+    mult = _tensor("multipliers", multipliers, (layers, orders + 1), i64, dev)
+    prime = _tensor("primes", primes, (layers, orders, heads), i64, dev)
+    offs = _tensor("offsets", offsets, (layers, orders * heads), i64, dev)
+    ids = _tensor("input_ids", input_ids, (n,), i64, dev)
     mask = None
     if token_mask is not None:
-        mask = _tensor("token_mask", token_mask, (n,), torch.bool if token_mask.dtype == torch.bool else torch.uint8)
-    slots = _tensor("plan.slots", plan.slots, (n,), i64)
-    pos = _tensor("plan.positions", plan.positions, (n,), i32)
-    req = _tensor("plan.requests", plan.requests, (n,), i32)
-    start = _tensor("plan.start_pos", plan.start_pos, (R,), i32)
-    table = _tensor("block_table", block_table, (R, pages.max_blocks), i32)
-    hist = _tensor("history", history, (pages.n_blocks, pages.block_size), i64)
-    _check_err(err_count)
+        mask = _tensor("token_mask", token_mask, (n,), torch.bool if token_mask.dtype is torch.bool else torch.uint8, dev)
+    slots = _tensor("plan.slots", plan.slots, (n,), i64, dev)
+    pos = _tensor("plan.positions", plan.positions, (n,), i32, dev)
+    req = _tensor("plan.requests", plan.requests, (n,), i32, dev)
+    start = _tensor("plan.start_pos", plan.start_pos, (R,), i32, dev)
+    table = _tensor("block_table", block_table, (R, pages.max_blocks), i32, dev)
+    hist = _tensor("history", history, (pages.n_blocks, pages.block_size), i64, dev)
     if out is None:
-        out = torch.empty((layout.n_layers, n, cols), dtype=i64, device=input_ids.device)
-    to = _tensor("out", out, (layout.n_layers, n, cols), i64)
-    _on(input_ids.device, token_map, multipliers, primes, offsets, token_mask, plan.slots, plan.positions, plan.requests,
-        plan.start_pos, block_table, history, out, err_count)
-    _launch("engram_hash_ids_paged", input_ids.device, _lib.engram_hash_ids_paged, layout, pages, tmap, mult,
-            primes.data_ptr(), offsets.data_ptr(), ids, mask, n, slots, pos, req, start, R, table, hist, to,
-            None if err_count is None else err_count.data_ptr())
+        out = torch.empty((layers, n, orders * heads), dtype=i64, device=input_ids.device)
+    to = _tensor("out", out, (layers, n, orders * heads), i64, dev)
+    _launch("engram_hash_ids_paged", dev, _lib.engram_hash_ids_paged, layout, pages, tmap, mult, prime, offs, ids, mask, n, slots,
+            pos, req, start, R, table, hist, to, _counter(err_count, dev))
     return out
 
 
@@ -738,45 +736,47 @@ def engram_residual_norm(layout: NormLayout, x: torch.Tensor, y: Optional[torch.
     be x.  Without y, h = norm(x) and out is x; without pre_norm, h is None."""
     if x.dim() != 4:
         raise ValueError(f"x has shape {tuple(x.shape)}, expected [B, T, hc, dim]")
-    B, T = x.shape[0], x.shape[1]
-    full = (B, T, layout.hc, layout.dim)
-    stream = _STREAM.get(layout.stream_format, torch.bfloat16)
-    xp = _tensor("x", x, full, stream)
+    B, T, hc, dim = x.shape
+    dev, bf16 = x.get_device(), torch.bfloat16
+    if (hc, dim) != (layout.hc, layout.dim):
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected [B, T, {layout.hc}, {layout.dim}]")
+    full = (B, T, hc, dim)
+    stream = torch.float32 if layout.stream_format == STREAM_FP32 else bf16
+    xp = _tensor("x", x, full, stream, dev)
     yp = gp = op = hp = mp = None
     y_stride = gate_stride = 0
     if y is not None:
-        if y.dtype != torch.bfloat16:
-            raise TypeError(f"y has dtype {y.dtype}, expected {torch.bfloat16}")
-        y_stride = _rows("y", y, (B, T), (layout.y_streams, layout.dim))
+        rows = (layout.y_streams, dim)
+        y_stride = _rows("y", y, (B, T), rows, bf16, dev)
         yp = y.data_ptr()
         if out is None:
             out = torch.empty_like(x)
-        op = _tensor("out", out, full, stream)
+            op = out.data_ptr()
+        else:
+            op = _tensor("out", out, full, stream, dev)
         if (gate is None) != (layout.gate == GATE_NONE):
             raise ValueError("gate does not match the layout's gate kind")
         if layout.gate == GATE_TOKEN:
-            gp = _tensor("gate", gate, full[:3], torch.float32)
+            gp = _tensor("gate", gate, (B, T, hc), torch.float32, dev)
         elif gate is not None:
-            if gate.dtype != torch.bfloat16:
-                raise TypeError(f"gate has dtype {gate.dtype}, expected {torch.bfloat16}")
-            gate_stride = _rows("gate", gate, (B, T), (layout.y_streams, layout.dim))
+            gate_stride = _rows("gate", gate, (B, T), rows, bf16, dev)
             gp = gate.data_ptr()
     elif gate is not None or out is not None:
         raise ValueError("gate and out need y")
     if layout.pre_norm:
         if h is None:
-            h = torch.empty(full, dtype=torch.bfloat16, device=x.device)
-        hp = _tensor("h", h, full, torch.bfloat16)
+            h = torch.empty(full, dtype=bf16, device=x.device)
+            hp = h.data_ptr()
+        else:
+            hp = _tensor("h", h, full, bf16, dev)
     elif h is not None:
         raise ValueError("h needs pre_norm")
-    weights = (layout.hc, layout.dim)
-    post = None if post_weight is None else _tensor("post_weight", post_weight, weights, torch.float32)
-    pre = None if pre_weight is None else _tensor("pre_weight", pre_weight, weights, torch.float32)
+    post = None if post_weight is None else _tensor("post_weight", post_weight, (hc, dim), torch.float32, dev)
+    pre = None if pre_weight is None else _tensor("pre_weight", pre_weight, (hc, dim), torch.float32, dev)
     if token_mask is not None:
-        mp = _tensor("token_mask", token_mask, (B, T), torch.bool if token_mask.dtype == torch.bool else torch.uint8)
-    _on(x.device, y, gate, post_weight, pre_weight, token_mask, out, h)
-    _launch("engram_residual_norm", x.device, _lib.engram_residual_norm, layout, xp, yp, y_stride, gp, gate_stride, post, pre,
-            mp, B, T, op, hp)
+        mp = _tensor("token_mask", token_mask, (B, T), torch.bool if token_mask.dtype is torch.bool else torch.uint8, dev)
+    _launch("engram_residual_norm", dev, _lib.engram_residual_norm, layout, xp, yp, y_stride, gp, gate_stride, post, pre, mp, B, T,
+            op, hp)
     return (x if y is None else out), h
 
 
@@ -797,37 +797,33 @@ def engram_linear(layout: LinearLayout, x: torch.Tensor, w: torch.Tensor, bias: 
     residual and out may be slices of wider rows; out may be the residual.  Without a workspace
     (engram_linear_workspace_bytes) the call takes one from torch's allocator where it needs one: calls
     on other streams, and captured graphs, then have their own."""
-    K, N = layout.in_features, layout.out_features
-    if x.dtype != torch.bfloat16:
-        raise TypeError(f"x has dtype {x.dtype}, expected {torch.bfloat16}")
+    K, N, dev, bf16 = layout.in_features, layout.out_features, x.get_device(), torch.bfloat16
     if x.dim() < 1:
         raise ValueError("x has no dimensions")
     lead = tuple(x.shape[:-1])
     M = math.prod(lead)
-    x_stride = _rows("x", x, lead, (K,))
+    x_stride = _rows("x", x, lead, (K,), bf16, dev)
     rows = 2 * N if layout.glu else N
-    wp = _tensor("w", w, (rows, K), torch.bfloat16)
-    bp = None if bias is None else _tensor("bias", bias, (rows,), torch.float32)
-    stream = _STREAM.get(layout.stream_format, torch.bfloat16)
+    wp = _tensor("w", w, (rows, K), bf16, dev)
+    bp = None if bias is None else _tensor("bias", bias, (rows,), torch.float32, dev)
+    stream = torch.float32 if layout.stream_format == STREAM_FP32 else bf16
     rp, r_stride = None, 0
     if residual is not None:
-        if residual.dtype != stream:
-            raise TypeError(f"residual has dtype {residual.dtype}, expected {stream}")
-        r_stride = _rows("residual", residual, lead, (N,))
+        r_stride = _rows("residual", residual, lead, (N,), stream, dev)
         rp = residual.data_ptr()
     if out is None:
-        out = torch.empty((*lead, N), dtype=stream, device=x.device)
-    elif out.dtype != stream:
-        raise TypeError(f"out has dtype {out.dtype}, expected {stream}")
-    o_stride = _rows("out", out, lead, (N,))
-    _on(x.device, w, bias, residual, out, workspace)
-    if workspace is None:
-        need = _lib.engram_linear_workspace_bytes(layout, M)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        out, o_stride = torch.empty((*lead, N), dtype=stream, device=x.device), N
     else:
+        o_stride = _rows("out", out, lead, (N,), stream, dev)
+    need = _lib.engram_linear_workspace_bytes(layout, M) if workspace is None else 0
+    if need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    ws, ws_bytes = None, 0
+    if workspace is not None:
         _contig("workspace", workspace)
-    _launch("engram_linear", x.device, _lib.engram_linear, layout, x.data_ptr(), x_stride, wp, bp, rp, r_stride, M,
-            out.data_ptr(), o_stride, None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel() * workspace.element_size())
+        if workspace.get_device() != dev:
+            raise ValueError(f"workspace is on {workspace.device}, not with the other tensors")
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _launch("engram_linear", dev, _lib.engram_linear, layout, x.data_ptr(), x_stride, wp, bp, rp, r_stride, M, out.data_ptr(),
+            o_stride, ws, ws_bytes)
     return out

@@ -17,30 +17,57 @@ namespace engram {
 namespace {
 
 constexpr int kPlanThreads = 256;
-constexpr int kTokensPerGroup = 1024;  // tokens of one workgroup: 4 per thread, coalesced
 
-// Inclusive sums of a and b over the workgroup's threads (64 bits: lengths near 2^30 times 4096
-// requests pass 32).  tmp: 2 x (kPlanThreads / 64) words, free again after the call.
-__device__ __forceinline__ void scan2(int64_t& a, int64_t& b, int64_t (*tmp)[kPlanThreads / kWave]) {
+// Sums saturate at 2^31 - 1 (lengths near 2^30 times 4096 requests pass 32 bits): sums of non-negative
+// values capped like this do not depend on their order, and nothing that fits (tokens, pages) reaches the cap.
+constexpr uint32_t kCapped = 0x7FFFFFFF;
+__device__ __forceinline__ uint32_t add(uint32_t a, uint32_t b) {
+  const uint32_t s = a + b;
+  return s < kCapped ? s : kCapped;
+}
+
+// Inclusive sum over the wave's lanes: within rows of 16 lanes, then row 0 into 1 and 2 into 3, then
+// lane 31 into the upper half.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v = add(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x111, 0xF, 0xF, false)));  // row_shr 1
+  v = add(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x112, 0xF, 0xF, false)));
+  v = add(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x114, 0xF, 0xF, false)));
+  v = add(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x118, 0xF, 0xF, false)));
+  v = add(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x142, 0xA, 0xF, false)));  // row_bcast 15
+  v = add(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x143, 0xC, 0xF, false)));  // row_bcast 31
+  return v;
+}
+
+// Sums of a and b over the threads before this one, and over all threads (total).  tmp: free again after
+// the call's last barrier.
+struct Sums {
+  uint32_t a, b, all_a, all_b;
+};
+__device__ __forceinline__ Sums scan2(uint32_t a, uint32_t b, uint32_t (*tmp)[2]) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    const int64_t pa = __shfl_up(a, o, kWave), pb = __shfl_up(b, o, kWave);
-    if (lane >= o) {
-      a += pa;
-      b += pb;
-    }
-  }
+  const uint32_t ia = wave_scan(a), ib = wave_scan(b);
   __syncthreads();
   if (lane == 63) {
-    tmp[0][wv] = a;
-    tmp[1][wv] = b;
+    tmp[wv][0] = ia;
+    tmp[wv][1] = ib;
   }
   __syncthreads();
-  for (int w = 0; w < wv; ++w) {
-    a += tmp[0][w];
-    b += tmp[1][w];
+  // the sums before this lane: shifted by one, not subtracted (a capped sum has no difference)
+  const uint32_t ua = uint32_t(__shfl_up(int(ia), 1, kWave)), ub = uint32_t(__shfl_up(int(ib), 1, kWave));
+  Sums s;
+  s.a = lane > 0 ? ua : 0u;  // (every lane takes part in the shuffle)
+  s.b = lane > 0 ? ub : 0u;
+  s.all_a = s.all_b = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / kWave; ++w) {
+    if (w < wv) {
+      s.a = add(s.a, tmp[w][0]);
+      s.b = add(s.b, tmp[w][1]);
+    }
+    s.all_a = add(s.all_a, tmp[w][0]);
+    s.all_b = add(s.all_b, tmp[w][1]);
   }
+  return s;
 }
 
 // First r with end[r] > i (end ascending, n entries; n if none).
@@ -58,18 +85,22 @@ __device__ __forceinline__ int first_above(const int32_t* end, int n, int i) {
 template <int ITEMS>
 __global__ __launch_bounds__(kPlanThreads) void k_batch_plan(PlanArgs a) {
   constexpr int kCap = kPlanThreads * ITEMS;
+  // the held lengths are looked up again below; for the most requests they no longer fit 64 KB of LDS
+  constexpr bool kKeep = ITEMS < 16;
   __shared__ int32_t back_end[kCap], tok_end[kCap], blk_end[kCap];  // inclusive sums
-  __shared__ int64_t tmp[2][kPlanThreads / kWave];
-  __shared__ int64_t total[2];
+  __shared__ int32_t length[kKeep ? kCap : 1];
+  __shared__ uint32_t tmp[kPlanThreads / kWave][2];
   const int tid = threadIdx.x;
   const int bs = a.block_size, cap = a.max_blocks * bs;
   const int r0 = tid * ITEMS;
   const bool lead = blockIdx.x == 0;
+  int free0 = a.free_count[0];
+  free0 = free0 < 0 ? 0 : (free0 > a.n_blocks ? a.n_blocks : free0);
 
   int held[ITEMS], have[ITEMS], want[ITEMS], stat[ITEMS];
-  int64_t back[ITEMS], tok[ITEMS];
+  uint32_t back[ITEMS], tok[ITEMS];  // this thread's sums up to each request
   bool gone[ITEMS];
-  int64_t sb = 0, st = 0;
+  uint32_t sb = 0, st = 0;
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k) {
     const int r = r0 + k;
@@ -80,94 +111,64 @@ __global__ __launch_bounds__(kPlanThreads) void k_batch_plan(PlanArgs a) {
     gone[k] = n < 0 && !bad;
     want[k] = bad || n < 0 ? 0 : n;
     stat[k] = bad ? 3 : 0;
-    sb += gone[k] ? have[k] : 0;
+    sb = add(sb, gone[k] ? have[k] : 0);
     back[k] = sb;
-    st += want[k];
+    st = add(st, want[k]);
     tok[k] = st;
+    if constexpr (kKeep) length[r] = held[k];
   }
-  {
-    int64_t eb = sb, et = st;
-    scan2(eb, et, tmp);
-    if (tid == kPlanThreads - 1) total[0] = eb;
-    eb -= sb;
-    et -= st;
-#pragma unroll
-    for (int k = 0; k < ITEMS; ++k) {
-      back[k] += eb;
-      tok[k] += et;
-      // past 2^31 nothing is looked up: a stack has fewer entries
-      back_end[r0 + k] = int32_t(back[k] < 0x7FFFFFFF ? back[k] : 0x7FFFFFFF);
-    }
-  }
-  __syncthreads();
-  int free0 = a.free_count[0];
-  free0 = free0 < 0 ? 0 : (free0 > a.n_blocks ? a.n_blocks : free0);
-  const int64_t all_back = total[0];
-  const int avail = int(all_back < a.n_blocks - free0 ? all_back + free0 : a.n_blocks);
+  const Sums first = scan2(sb, st, tmp);
+  const uint32_t all_back = first.all_a, room = uint32_t(a.n_blocks - free0);
+  const int avail = free0 + int(all_back < room ? all_back : room);
 
   // by tokens, then by pages
   int need[ITEMS];
-  int64_t blk[ITEMS], sn = 0;
+  uint32_t blk[ITEMS], sn = 0;
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k) {
-    if (want[k] > 0 && tok[k] > a.max_tokens) {
+    back_end[r0 + k] = int32_t(add(first.a, back[k]));
+    if (want[k] > 0 && add(first.b, tok[k]) > uint32_t(a.max_tokens)) {
       stat[k] = 1;
       want[k] = 0;
     }
     need[k] = want[k] > 0 ? (held[k] + want[k] + bs - 1) / bs - have[k] : 0;
+    sn = add(sn, need[k]);
+    blk[k] = sn;
+  }
+  const Sums asked = scan2(sn, 0u, tmp);
+  st = sn = 0;
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    if (need[k] > 0 && add(asked.a, blk[k]) > uint32_t(avail)) {
+      stat[k] = 2;
+      want[k] = 0;
+      need[k] = 0;
+    }
+    st += want[k];
+    tok[k] = st;
     sn += need[k];
     blk[k] = sn;
   }
-  {
-    int64_t en = sn, unused = 0;
-    scan2(en, unused, tmp);
-    en -= sn;
-    st = sn = 0;
+  const Sums given = scan2(st, sn, tmp);
 #pragma unroll
-    for (int k = 0; k < ITEMS; ++k) {
-      if (need[k] > 0 && blk[k] + en > avail) {
-        stat[k] = 2;
-        want[k] = 0;
-        need[k] = 0;
-      }
-      st += want[k];
-      tok[k] = st;
-      sn += need[k];
-      blk[k] = sn;
-    }
-  }
-  {
-    int64_t et = st, en = sn;
-    scan2(et, en, tmp);
-    if (tid == kPlanThreads - 1) {
-      total[0] = et;
-      total[1] = en;
-    }
-    et -= st;
-    en -= sn;
-#pragma unroll
-    for (int k = 0; k < ITEMS; ++k) {
-      const int r = r0 + k;
-      tok_end[r] = int32_t(tok[k] + et);
-      blk_end[r] = int32_t(blk[k] + en);
-      if (lead && r < a.R) {
-        a.token_start[r + 1] = int32_t(tok[k] + et);
-        a.start_pos[r] = held[k];
-        a.seq_lens[r] = gone[k] ? 0 : held[k] + want[k];
-        a.status[r] = stat[k];
-        if (stat[k] != 0 && a.err_count != nullptr) atomicAdd(a.err_count, 1);
-      }
+  for (int k = 0; k < ITEMS; ++k) {
+    const int r = r0 + k;
+    tok_end[r] = int32_t(given.a + tok[k]);
+    blk_end[r] = int32_t(given.b + blk[k]);
+    if (lead && r < a.R) {
+      a.token_start[r + 1] = int32_t(given.a + tok[k]);
+      a.start_pos[r] = held[k];
+      a.seq_lens[r] = gone[k] ? 0 : held[k] + want[k];
+      a.status[r] = stat[k];
+      if (stat[k] != 0 && a.err_count != nullptr) atomicAdd(a.err_count, 1);
     }
   }
   __syncthreads();
-  const int n_tok = int(total[0]), n_new = int(total[1]);
+  const int n_tok = int(given.all_a), n_new = int(given.all_b);
   if (lead && tid == 0) {
     a.token_start[0] = 0;
     a.free_left[0] = avail - n_new;
-    if (a.err_count != nullptr && all_back > a.n_blocks - free0) {
-      const int64_t dropped = all_back - (a.n_blocks - free0);
-      atomicAdd(a.err_count, int(dropped < 0x7FFFFFFF ? dropped : 0x7FFFFFFF));
-    }
+    if (a.err_count != nullptr && all_back > room) atomicAdd(a.err_count, int(all_back - room));
   }
 
   // entry j of the stack after the released pages came back: below free0 the caller's list, above
@@ -178,8 +179,9 @@ __global__ __launch_bounds__(kPlanThreads) void k_batch_plan(PlanArgs a) {
     return a.block_table[int64_t(r) * a.max_blocks + (j - before)];
   };
   auto stack = [&](int idx) { return idx < free0 ? a.free_list[idx] : released(idx - free0); };
+  auto length_of = [&](int r) { return kKeep ? length[kKeep ? r : 0] : a.cached_lens[r]; };
   auto pages_of = [&](int r) {  // pages the request holds already
-    return (a.cached_lens[r] + bs - 1) / bs;
+    return (length_of(r) + bs - 1) / bs;
   };
 
   const int step = int(gridDim.x) * kPlanThreads;
@@ -195,7 +197,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_batch_plan(PlanArgs a) {
     int pos = -1, req = -1;
     if (i < n_tok) {
       req = first_above(tok_end, a.R, int(i));
-      pos = a.cached_lens[req] + int(i) - (req > 0 ? tok_end[req - 1] : 0);
+      pos = length_of(req) + int(i) - (req > 0 ? tok_end[req - 1] : 0);
       const int b = pos / bs, old = pages_of(req);
       const int page = b < old ? a.block_table[int64_t(req) * a.max_blocks + b]
                                : stack(avail - 1 - ((req > 0 ? blk_end[req - 1] : 0) + b - old));
@@ -213,8 +215,10 @@ __global__ __launch_bounds__(kPlanThreads) void k_batch_plan(PlanArgs a) {
 
 hipError_t launch_batch_plan(const PlanArgs& a, hipStream_t stream) {
   if (a.R < 0 || a.R > kMaxRequests || a.max_tokens < 0) return hipErrorInvalidValue;
-  int64_t grid = (int64_t(a.max_tokens) + kTokensPerGroup - 1) / kTokensPerGroup;
-  grid = grid < 1 ? 1 : (grid > 1024 ? 1024 : grid);
+  // one token per thread: a token is a chain of reads (16,384 tokens of 512 requests: 14.6 us with four
+  // tokens per thread, 9.3 us with one; every workgroup's own sums cost less than the wait)
+  int64_t grid = (int64_t(a.max_tokens) + kPlanThreads - 1) / kPlanThreads;
+  grid = grid < 1 ? 1 : (grid > 4096 ? 4096 : grid);
   PlanArgs args = a;
   void* params[] = {&args};
   const void* fn = a.R <= kPlanThreads       ? reinterpret_cast<const void*>(&k_batch_plan<1>)

@@ -268,7 +268,7 @@ typedef enum { ENGRAM_STREAM_BF16 = 0, ENGRAM_STREAM_FP32 = 1 } engram_stream_fo
 typedef struct {
   int32_t block_size; /* >= 1 */
   int32_t max_blocks; /* >= 1; max_blocks * block_size <= 2^30 */
-  int64_t n_blocks;   /* 1 .. 2^31 - 1 */
+  int64_t n_blocks;   /* 1 .. 2^30 */
 } engram_page_layout;
 
 /* What engram_batch_plan writes, all device pointers, all required.  None may overlap an input. */

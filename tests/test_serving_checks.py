@@ -29,7 +29,7 @@ def bad_fields(make, check, changes):
 
 def test_layout_checks():
     bad_fields(lambda: eg.make_page_layout(16, 64, 1000), LIB.engram_page_layout_check,
-               [dict(block_size=0), dict(block_size=-4), dict(max_blocks=0), dict(n_blocks=0), dict(n_blocks=1 << 31),
+               [dict(block_size=0), dict(block_size=-4), dict(max_blocks=0), dict(n_blocks=0), dict(n_blocks=(1 << 30) + 1),
                 dict(block_size=1 << 20, max_blocks=1 << 11)])
     bad_fields(lambda: eg.make_norm_layout(4, 5120), LIB.engram_norm_layout_check,
                [dict(hc=0), dict(hc=65), dict(dim=0), dict(dim=12), dict(dim=65544), dict(y_streams=2), dict(stream_format=2),
