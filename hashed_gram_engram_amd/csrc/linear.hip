@@ -640,6 +640,111 @@ __global__ __launch_bounds__(512, 2) void k_linear_big(LinearArgs a) {
   epilogue<8, 4, GLU>(a, acc, lds + wv * kEpi, m0 + (wv & 3) * 64, int(n0) + (wv >> 2) * (GLU ? 64 : 128), lane);
 }
 
+// ---------------------------------------------------------------- up to 16 tokens
+// A tile of 16 tokens x 16 weight rows (32 gated) whose K is shared by the W waves of the workgroup: wave w
+// takes stages w, w + W, ...  A wave has a ring of ST slots of its own (its weight rows, then XR token rows;
+// with XR = 8 the fragments of tokens 8..15 read those of 0..7 and are dropped) and waits only for its own
+// copies, so the waves run free of each other until they add up their sums.
+template <int W, int ST, int XR, bool GLU>
+__global__ __launch_bounds__(W* kWave) void k_linear_few(LinearArgs a) {
+  constexpr int TN = GLU ? 2 : 1;
+  constexpr int kCopies = 2 * TN + XR / 8, kSlot = kCopies * 1024;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  static_assert(W * TN * 1024 <= W * ST * kSlot && epilogue_bytes<TN>() <= W * ST * kSlot, "sums and epilogue");
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, g = lane >> 4;
+  const int64_t n0 = int64_t(blockIdx.x) * 16;
+  const int S = a.K / kBK, count = (S - wv + W - 1) / W;  // stages, this wave's
+  const int turned = S > 0 ? int(blockIdx.x % unsigned(S)) : 0;
+  char* ring = lds + wv * ST * kSlot;
+  const char* base[kCopies];
+  uint32_t off[kCopies];
+#pragma unroll
+  for (int i = 0; i < kCopies; ++i) {
+    const int r = 8 * (i < 2 * TN ? i : i - 2 * TN), mine = r + (lane >> 3);
+    const uint32_t at = 16 * ((lane & 7) ^ swizzle(mine));
+    if (i < 2 * TN) {
+      const int64_t row = weight_row<GLU>(a, n0, r);
+      base[i] = reinterpret_cast<const char*>(a.w + row * a.K);
+      off[i] = uint32_t(weight_row<GLU>(a, n0, mine) - row) * uint32_t(a.K) * 2 + at;
+    } else {
+      const int64_t last = a.M - 1, first = r < last ? r : last, m = mine < last ? mine : last;
+      base[i] = reinterpret_cast<const char*>(a.x + first * a.x_stride);
+      off[i] = uint32_t(m - first) * uint32_t(a.x_stride) * 2 + at;
+    }
+  }
+  auto copy = [&](int i, int slot) {  // stages past the wave's last repeat it
+    int t = wv + W * (i < count ? i : count - 1) + turned;
+    t = t < S ? t : t - S;
+    const size_t at = size_t(t) * kRowB;
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c)
+      __builtin_amdgcn_global_load_lds((const void*)(base[c] + at + off[c]), (lds_ptr_t)(ring + slot * kSlot + c * 1024), 16,
+                                       0, 0);
+  };
+  f32x4 acc[TN][1];
+#pragma unroll
+  for (int i = 0; i < TN; ++i) acc[i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (count > 0) {
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) copy(i, i);
+    int slot = 0;
+    for (int i = 0; i < count; ++i) {
+      wait_copies<(ST - 2) * kCopies>();  // this stage is there
+      const char* p = ring + slot * kSlot;
+      u32x4 fw[2][TN], fx[2];
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int c = 16 * ((4 * hh + g) ^ swizzle(r16));
+#pragma unroll
+        for (int k = 0; k < TN; ++k) fw[hh][k] = *reinterpret_cast<const u32x4*>(p + (16 * k + r16) * kRowB + c);
+        const int t = r16 & (XR - 1);
+        fx[hh] = *reinterpret_cast<const u32x4*>(p + (16 * TN + t) * kRowB + 16 * ((4 * hh + g) ^ swizzle(t)));
+      }
+      // the slot of the stage before: its fragments went into the last pass's MFMAs
+      copy(i + ST - 1, slot == 0 ? ST - 1 : slot - 1);
+      wait_reads();
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+        for (int k = 0; k < TN; ++k) acc[k][0] = mfma16x16x32(fw[hh][k], fx[hh], acc[k][0]);
+      slot = slot + 1 == ST ? 0 : slot + 1;
+    }
+    wait_copies<0>();
+  }
+  if (wv == W - 1 && a.K % kBK != 0) tail<TN, 1, GLU>(a, acc, n0, 0, 0, lane);
+  __syncthreads();  // nobody copies into LDS any more
+  f32x4* sums = reinterpret_cast<f32x4*>(lds);
+#pragma unroll
+  for (int i = 0; i < TN; ++i) sums[(wv * TN + i) * kWave + lane] = acc[i][0];
+  __syncthreads();
+  if (wv != 0) return;
+#pragma unroll
+  for (int i = 0; i < TN; ++i) {
+    acc[i][0] = sums[i * kWave + lane];
+#pragma unroll
+    for (int v = 1; v < W; ++v) acc[i][0] += sums[(v * TN + i) * kWave + lane];
+  }
+  wave_lds_fence();
+  epilogue<TN, 1, GLU>(a, acc, lds, 0, int(n0), lane);
+}
+
+template <int W, int ST, int XR, bool GLU>
+hipError_t launch_few(const LinearArgs& a, hipStream_t stream) {
+  constexpr int kBytes = W * ST * ((GLU ? 4 : 2) + XR / 8) * 1024;
+  static_assert(kBytes <= 160 * 1024, "LDS");
+  const int64_t tiles = (int64_t(a.N) + 15) / 16;
+  if (tiles > 0x7FFFFFFF || a.M > XR) return hipErrorInvalidValue;
+  const void* fn = reinterpret_cast<const void*>(&k_linear_few<W, ST, XR, GLU>);
+  if constexpr (kBytes > 65536) {
+    const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    if (e != hipSuccess) return e;
+  }
+  LinearArgs args = a;
+  void* params[] = {&args};
+  return hipLaunchKernel(fn, dim3(unsigned(tiles)), dim3(W * kWave), params, kBytes, stream);
+}
+
 // Launches `fn` over `tiles` tiles times a.parts parts, then the kernel that joins the parts.
 hipError_t launch_parts(const LinearArgs& a, const void* fn, int bytes, int waves, const void* join, int64_t tiles,
                         hipStream_t stream) {
@@ -685,9 +790,13 @@ constexpr TileShape kTiles[2][15] = {
      {128, 128, 4, 4}, {128, 128, 4, 2}, {64, 256, 8, 4}, {64, 128, 4, 6}, {64, 64, 4, 4}, {32, 128, 4, 6},
      {32, 64, 4, 8}, {32, 32, 2, 8}, {16, 32, 1, 12}}};
 
+constexpr int kFew8 = 15, kFew16 = 16;  // k_linear_few for up to 8 and 16 tokens
+
 template <bool GLU>
 hipError_t launch_shape(int tile, const LinearArgs& a, hipStream_t stream) {
   switch (tile) {
+    case kFew8: return launch_few<4, 4, 8, GLU>(a, stream);
+    case kFew16: return launch_few<4, GLU ? 3 : 5, 16, GLU>(a, stream);
     case 0: return launch_big<GLU>(a, stream);
     case 1: return launch_tile<128, 256, 4, 2, 3, GLU>(a, stream);
     case 2: return launch_tile<256, 128, 4, 2, 3, GLU>(a, stream);
@@ -743,6 +852,15 @@ struct LinearChoice {
 };
 LinearChoice choose(int64_t M, int K, int N, bool glu, int cus) {
   LinearChoice best;
+  // Up to 16 tokens: the shared-K kernel (one token x 5120 x 5120: 11.0 us, the best tile and split of the
+  // others 12.8; x 4096 x 1024: 4.4 and 7.9; 16 tokens x 2048 x 8192: 7.7 and 8.3).  From 9 tokens on only
+  // while its tiles are at most two to a compute unit: it reads x once per 16 rows (16 tokens x 6144 x
+  // 25,600: 65.7 us, and 55.4 with tiles of 128 rows).
+  const int64_t few = (int64_t(N) + 15) / 16;
+  if (M <= 8 || (M <= 16 && few <= 2 * cus)) {
+    best.tile = M <= 8 ? kFew8 : kFew16;
+    return best;
+  }
   double least = 1e30;
   const int64_t rows = glu ? 2 * int64_t(N) : N;
   for (int i = 0; i < 15; ++i) {

@@ -23,7 +23,8 @@ def whole(g, *shape):
 
 SIZES = [(1, 64, 16), (1, 8, 1), (1, 5120, 5120), (2, 72, 33), (5, 1000, 257), (16, 128, 64), (17, 640, 100), (31, 4096, 48),
          (33, 200, 1001), (64, 1024, 512), (65, 264, 130), (100, 5120, 1030), (127, 64, 255), (128, 4096, 256), (129, 520, 384),
-         (200, 2048, 1280), (257, 1288, 513), (300, 8, 700), (512, 512, 2048), (777, 1032, 777), (1025, 256, 1281)]
+         (200, 2048, 1280), (257, 1288, 513), (300, 8, 700), (512, 512, 2048), (777, 1032, 777), (1025, 256, 1281),
+         (8, 4104, 47), (13, 3000, 130), (16, 4104, 47), (9, 264, 9001), (3, 56, 20000), (7, 192, 20001)]
 
 
 # shapes that take every tile, whole and split over K (plain, then gated), as engram_linear chooses them on
@@ -31,7 +32,7 @@ SIZES = [(1, 64, 16), (1, 8, 1), (1, 5120, 5120), (2, 72, 33), (5, 1000, 257), (
 TILES = [(2067, 256, 4991), (1803, 832, 3400), (822, 4912, 3006), (512, 4560, 5198), (1537, 312, 3597), (136, 5144, 3845),
          (1678, 120, 2371), (1887, 5352, 260), (822, 280, 5993), (161, 3840, 5879), (385, 64, 4707), (65, 4816, 5955),
          (1043, 64, 3868), (1594, 64, 2501), (163, 3536, 5707), (229, 416, 4108), (35, 4008, 5463), (202, 64, 4108),
-         (68, 3168, 2882), (2048, 4096, 4096), (1000, 10240, 5120)]
+         (68, 3168, 2882), (2048, 4096, 4096), (1000, 10240, 5120), (681, 3744, 36)]
 GATED_TILES = [(963, 248, 4830), (1561, 840, 1828), (331, 4936, 2714), (1163, 1032, 3214), (194, 4736, 4267), (391, 120, 4618),
                (146, 4336, 1833), (323, 280, 5664), (66, 4072, 5545), (925, 304, 3182), (173, 4016, 2770), (67, 4688, 2727),
                (385, 64, 4707), (258, 64, 5478), (180, 3296, 2738), (33, 2936, 4279), (71, 64, 4218), (73, 3392, 1381),
