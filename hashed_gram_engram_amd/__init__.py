@@ -26,6 +26,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 ENGRAM_OK = 0
 ENGRAM_E_TIMEOUT = -8
+ENGRAM_E_WORKSPACE = -5
 STATUS = {0: "ok", -1: "null pointer", -2: "layout", -3: "shape", -4: "alignment",
           -5: "workspace", -6: "hip", -7: "device", -8: "timeout"}
 
@@ -642,21 +643,34 @@ def make_page_layout(block_size: int, max_blocks: int, n_blocks: int) -> PageLay
 
 
 class BatchPlan:
-    """The buffers engram_batch_plan writes (engram_batch_plan_out in include/engram.h), kept by the
-    caller from step to step.  seq_lens and free_left are the next step's cached_lens and free_count:
-    use two plans in turn, or copy them (a call never writes what it reads)."""
+    """The buffers engram_batch_plan writes (engram_batch_plan_out in include/engram.h), made once by the
+    caller and kept from step to step.  They are read, and may be filled, through the attributes named
+    in FIELDS, but not replaced or resized.  seq_lens and free_left are the next step's cached_lens and
+    free_count: use two plans in turn, or copy them (a call never writes what it reads)."""
 
     FIELDS = ("token_start", "start_pos", "seq_lens", "status", "free_left", "slots", "positions", "requests", "live")
 
     def __init__(self, n_requests: int, max_tokens: int, device="cuda"):
-        def make(n, dtype=torch.int32):
-            return torch.zeros(n, dtype=dtype, device=device)
-        self.n_requests, self.max_tokens = n_requests, max_tokens
-        self.token_start, self.start_pos, self.seq_lens = make(n_requests + 1), make(n_requests), make(n_requests)
-        self.status, self.free_left = make(n_requests), make(1)
-        self.slots, self.positions = make(max_tokens, torch.int64), make(max_tokens)
-        self.requests, self.live = make(max_tokens), make(max_tokens, torch.uint8)
-        self.device = self.slots.device
+        sizes = (n_requests + 1, n_requests, n_requests, n_requests, 1, max_tokens, max_tokens, max_tokens, max_tokens)
+        types = [{"slots": torch.int64, "live": torch.uint8}.get(f, torch.int32) for f in self.FIELDS]
+        self._buffers = tuple(torch.zeros(n, dtype=t, device=device) for n, t in zip(sizes, types))
+        self._out = _PlanOut(*[t.data_ptr() for t in self._buffers])
+        self._index = self._buffers[0].get_device()
+        self._sizes = (n_requests, max_tokens)
+
+    n_requests = property(lambda self: self._sizes[0])
+    max_tokens = property(lambda self: self._sizes[1])
+    device = property(lambda self: self._buffers[0].device)
+
+
+for _i, _f in enumerate(BatchPlan.FIELDS):
+    setattr(BatchPlan, _f, property(lambda self, i=_i: self._buffers[i]))
+
+
+def _plan_on(plan: BatchPlan, device: int) -> BatchPlan:
+    if plan._index != device:
+        raise ValueError(f"plan is on {plan.device}, not with the other tensors")
+    return plan
 
 
 def engram_batch_plan(layout: PageLayout, new_lens: torch.Tensor, cached_lens: torch.Tensor, block_table: torch.Tensor,
@@ -665,24 +679,14 @@ def engram_batch_plan(layout: PageLayout, new_lens: torch.Tensor, cached_lens: t
     """Plans a step of ragged requests into `plan` (engram_batch_plan in include/engram.h): admits
     requests by tokens and pages, takes and gives back pages (block_table [R, max_blocks] and
     free_list [n_blocks] are updated in place), and lays out the admitted tokens."""
-    R, T, i32, dev = plan.n_requests, plan.max_tokens, torch.int32, free_list.get_device()
+    (R, T), i32, dev = plan._sizes, torch.int32, free_list.get_device()
     new = _tensor("new_lens", new_lens, (R,), i32, dev)
     held = _tensor("cached_lens", cached_lens, (R,), i32, dev)
     table = _tensor("block_table", block_table, (R, layout.max_blocks), i32, dev)
     pool = _tensor("free_list", free_list, (layout.n_blocks,), i32, dev)
     count = _tensor("free_count", free_count, (1,), i32, dev)
-    # the plan's buffers are attributes: they may have been replaced since it was made
-    out = _PlanOut(_tensor("plan.token_start", plan.token_start, (R + 1,), i32, dev),
-                   _tensor("plan.start_pos", plan.start_pos, (R,), i32, dev),
-                   _tensor("plan.seq_lens", plan.seq_lens, (R,), i32, dev),
-                   _tensor("plan.status", plan.status, (R,), i32, dev),
-                   _tensor("plan.free_left", plan.free_left, (1,), i32, dev),
-                   _tensor("plan.slots", plan.slots, (T,), torch.int64, dev),
-                   _tensor("plan.positions", plan.positions, (T,), i32, dev),
-                   _tensor("plan.requests", plan.requests, (T,), i32, dev),
-                   _tensor("plan.live", plan.live, (T,), torch.uint8, dev))
-    _launch("engram_batch_plan", dev, _lib.engram_batch_plan, layout, new, held, R, table, pool, count, T, out,
-            _counter(err_count, dev))
+    _launch("engram_batch_plan", dev, _lib.engram_batch_plan, layout, new, held, R, table, pool, count, T,
+            _plan_on(plan, dev)._out, _counter(err_count, dev))
     return plan
 
 
@@ -693,7 +697,8 @@ def engram_hash_ids_paged(layout: HashLayout, pages: PageLayout, token_map: torc
     """Row ids [n_layers, n_tokens, (max_ngram - 1) * n_heads] int64 of a plan's flat tokens input_ids
     [plan.max_tokens] (engram_hash_ids_paged in include/engram.h); history [n_blocks, block_size]
     int64, addressed through the plan and block_table, is read and updated in place."""
-    n, R, i64, i32, dev = plan.max_tokens, plan.n_requests, torch.int64, torch.int32, input_ids.get_device()
+    (R, n), i64, i32, dev = plan._sizes, torch.int64, torch.int32, input_ids.get_device()
+    at = _plan_on(plan, dev)._out
     layers, heads, orders = layout.n_layers, layout.n_heads, layout.max_ngram - 1
     tmap = _tensor("token_map", token_map, (layout.vocab,), i32 if token_map.dtype is i32 else torch.uint32, dev)
     mult = _tensor("multipliers", multipliers, (layers, orders + 1), i64, dev)
@@ -703,17 +708,15 @@ def engram_hash_ids_paged(layout: HashLayout, pages: PageLayout, token_map: torc
     mask = None
     if token_mask is not None:
         mask = _tensor("token_mask", token_mask, (n,), torch.bool if token_mask.dtype is torch.bool else torch.uint8, dev)
-    slots = _tensor("plan.slots", plan.slots, (n,), i64, dev)
-    pos = _tensor("plan.positions", plan.positions, (n,), i32, dev)
-    req = _tensor("plan.requests", plan.requests, (n,), i32, dev)
-    start = _tensor("plan.start_pos", plan.start_pos, (R,), i32, dev)
     table = _tensor("block_table", block_table, (R, pages.max_blocks), i32, dev)
     hist = _tensor("history", history, (pages.n_blocks, pages.block_size), i64, dev)
     if out is None:
-        out = torch.empty((layers, n, orders * heads), dtype=i64, device=input_ids.device)
-    to = _tensor("out", out, (layers, n, orders * heads), i64, dev)
-    _launch("engram_hash_ids_paged", dev, _lib.engram_hash_ids_paged, layout, pages, tmap, mult, prime, offs, ids, mask, n, slots,
-            pos, req, start, R, table, hist, to, _counter(err_count, dev))
+        out = input_ids.new_empty((layers, n, orders * heads))
+        to = out.data_ptr()
+    else:
+        to = _tensor("out", out, (layers, n, orders * heads), i64, dev)
+    _launch("engram_hash_ids_paged", dev, _lib.engram_hash_ids_paged, layout, pages, tmap, mult, prime, offs, ids, mask, n, at.slots,
+            at.positions, at.requests, at.start_pos, R, table, hist, to, _counter(err_count, dev))
     return out
 
 
@@ -765,7 +768,7 @@ def engram_residual_norm(layout: NormLayout, x: torch.Tensor, y: Optional[torch.
         raise ValueError("gate and out need y")
     if layout.pre_norm:
         if h is None:
-            h = torch.empty(full, dtype=bf16, device=x.device)
+            h = torch.empty_like(x, dtype=bf16)
             hp = h.data_ptr()
         else:
             hp = _tensor("h", h, full, bf16, dev)
@@ -812,18 +815,22 @@ def engram_linear(layout: LinearLayout, x: torch.Tensor, w: torch.Tensor, bias: 
         r_stride = _rows("residual", residual, lead, (N,), stream, dev)
         rp = residual.data_ptr()
     if out is None:
-        out, o_stride = torch.empty((*lead, N), dtype=stream, device=x.device), N
+        out, o_stride = x.new_empty((*lead, N), dtype=stream), N
     else:
         o_stride = _rows("out", out, lead, (N,), stream, dev)
-    need = _lib.engram_linear_workspace_bytes(layout, M) if workspace is None else 0
-    if need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     ws, ws_bytes = None, 0
     if workspace is not None:
         _contig("workspace", workspace)
         if workspace.get_device() != dev:
             raise ValueError(f"workspace is on {workspace.device}, not with the other tensors")
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _launch("engram_linear", dev, _lib.engram_linear, layout, x.data_ptr(), x_stride, wp, bp, rp, r_stride, M, out.data_ptr(),
-            o_stride, ws, ws_bytes)
+    args = (layout, x.data_ptr(), x_stride, wp, bp, rp, r_stride, M, out.data_ptr(), o_stride)
+    try:
+        _launch("engram_linear", dev, _lib.engram_linear, *args, ws, ws_bytes)
+    except EngramError as e:
+        if e.status != ENGRAM_E_WORKSPACE or workspace is not None:
+            raise
+        # the shape splits K (a call without a workspace is refused before anything is enqueued)
+        workspace = x.new_empty(engram_linear_workspace_bytes(layout, M), dtype=torch.uint8)
+        _launch("engram_linear", dev, _lib.engram_linear, *args, workspace.data_ptr(), workspace.numel())
     return out

@@ -8,9 +8,8 @@
 // v_mfma_f32_16x16x32_bf16 (weight rows as A, tokens as B: a lane then holds 4 consecutive output
 // features of one token).
 //
-// Gated: the weight has the N gate rows, then the N value rows.  A tile takes 16 rows of the gate, the
-// same 16 of the value, and so on, so a lane holds both factors of an output and the epilogue needs no
-// exchange.
+// Gated: the weight has the N gate rows, then the N value rows.  A block of 16 rows takes 8 rows of the
+// gate and the same 8 of the value, so both factors of an output meet in one wave's epilogue.
 //
 // Features past K (K is a multiple of 8) are copied from 16 zero bytes; weight rows past N and tokens
 // past M repeat the last one and are not stored.
@@ -26,7 +25,12 @@ namespace {
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 // ---------------------------------------------------------------- epilogue
-// act(z) of 8 values; one branch for all of them.
+// act(z) of 8 values; one branch for all of them.  exp is the hardware's 2^x of a rounded product (within
+// |z| 2^-23 of exp(z), relative, where the result is small against z) and 1 / v within one unit in the last
+// place: with the library's expf, erff and division the epilogue of an 8192 x 6144 x 25,600 product took
+// 140 us longer for GELU.  Phi(-|z|) is formula 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical
+// Functions (|error of erf| <= 1.5e-7).
+__device__ __forceinline__ float rcp(float v) { return __builtin_amdgcn_rcpf(v); }
 __device__ __forceinline__ void activate8(float (&z)[8], int act) {
   if (act == 0) return;
   if (act == 1) {
@@ -34,15 +38,20 @@ __device__ __forceinline__ void activate8(float (&z)[8], int act) {
     for (int e = 0; e < 8; ++e) z[e] = z[e] < 0.0f ? 0.0f : z[e];  // a NaN stays one
   } else if (act == 2) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) z[e] = 0.5f * z[e] * (1.0f + erff(z[e] * 0.70710678118654752f));
+    for (int e = 0; e < 8; ++e) {
+      const float x = fabsf(z[e]) * 0.70710678f, t = rcp(1.0f + 0.3275911f * x);
+      const float p = t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+      const float q = 0.5f * p * __expf(-x * x);  // Phi(-|z|)
+      z[e] *= z[e] > 0.0f ? 1.0f - q : q;
+    }
   } else if (act == 5) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) z[e] = 1.0f / (1.0f + expf(-z[e]));
+    for (int e = 0; e < 8; ++e) z[e] = rcp(1.0f + __expf(-z[e]));
   } else {
     // z / (1 + exp(-u)): u = z, or 2 sqrt(2 / pi) (z + 0.044715 z^3) since (1 + tanh v) / 2 = 1 / (1 + exp(-2 v))
     const float c1 = act == 3 ? 1.5957691216057308f : 1.0f, c3 = act == 3 ? 0.071354816272f : 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) z[e] = z[e] / (1.0f + expf(-z[e] * (c1 + c3 * z[e] * z[e])));
+    for (int e = 0; e < 8; ++e) z[e] *= rcp(1.0f + __expf(-z[e] * (c1 + c3 * z[e] * z[e])));
   }
 }
 
@@ -133,13 +142,13 @@ constexpr int epilogue_bytes() { return 16 * epilogue_row<TN>() * 4; }
 
 // A wave's part of the tile: TN x TM blocks of 16 weight rows x 16 tokens, block (i, j) holding rows
 // 16 i + 4 (l >> 4) + 0..3 of token 16 j + (l & 15).  16 tokens at a time pass through the wave's own
-// piece of LDS, so that a lane gets 8 consecutive output features of a token (with GLU: blocks 2 i of
-// the gate, 2 i + 1 of the value) and stores are whole row segments.
+// piece of LDS, so that a lane gets 8 consecutive output features of a token (with GLU: a block's 8 gate
+// rows and its 8 value rows) and stores are whole row segments.
 template <int TN, int TM, bool GLU>
 __device__ __forceinline__ void epilogue(const LinearArgs& a, const f32x4 (&acc)[TN][TM], char* lds, int64_t m0, int n0,
                                          int lane) {
   constexpr int kRow = epilogue_row<TN>();
-  constexpr int kLanes = (GLU ? TN / 2 : TN) * 2;  // of 8 output features each
+  constexpr int kLanes = GLU ? TN : 2 * TN;     // of 8 output features each
   constexpr bool kFixed = kWave % kLanes == 0;     // a lane's features are the same in every pass
   float* buf = reinterpret_cast<float*>(lds);
   const bool vec = vector_rows(a);
@@ -167,14 +176,14 @@ __device__ __forceinline__ void epilogue(const LinearArgs& a, const f32x4 (&acc)
       if (m >= a.M || n >= a.N) continue;
       if constexpr (!kFixed) biases(n);
       float z[8];
-      const float* p = buf + t * kRow + (GLU ? (c >> 4) * 32 + (c & 15) : c);
+      const float* p = buf + t * kRow + (GLU ? 2 * c : c);
       load8(p, z);
 #pragma unroll
       for (int k = 0; k < 8; ++k) z[k] += b[k];
       activate8(z, a.act);
       if constexpr (GLU) {
         float u[8];
-        load8(p + 16, u);
+        load8(p + 8, u);
 #pragma unroll
         for (int k = 0; k < 8; ++k) z[k] *= u[k] + bu[k];
       }
@@ -207,9 +216,9 @@ __device__ __forceinline__ void group_barrier() {
 template <bool GLU>
 __device__ __forceinline__ int64_t weight_row(const LinearArgs& a, int64_t n0, int r) {
   if constexpr (!GLU) return n0 + r < a.N ? n0 + r : int64_t(a.N) - 1;
-  int64_t n = n0 + (r >> 5) * 16 + (r & 15);
+  int64_t n = n0 + (r >> 4) * 8 + (r & 7);
   n = n < a.N ? n : int64_t(a.N) - 1;
-  return n + ((r >> 4) & 1) * int64_t(a.N);
+  return n + ((r >> 3) & 1) * int64_t(a.N);
 }
 
 // The tile of workgroup b of `tiles`: workgroups are dealt to the 8 XCDs round robin, so each XCD
@@ -320,7 +329,7 @@ __global__ __launch_bounds__(kWave) void k_linear_join(LinearArgs a) {
   // which part of the tile a wave holds: as in k_linear_big (the 256 x 256 tile) and k_linear
   constexpr bool kGroups = BM == 256 && BN == 256;
   const int wm = kGroups ? wv % WM : wv / WN, wn = kGroups ? wv / WM : wv % WN;
-  epilogue<TN, TM, GLU>(a, acc, lds, tb * BM + wm * TM * 16, int(cb * kOutCols) + wn * (GLU ? TN * 8 : TN * 16), lane);
+  epilogue<TN, TM, GLU>(a, acc, lds, tb * BM + wm * TM * 16, int(cb * kOutCols) + wn * TN * (GLU ? 8 : 16), lane);
 }
 
 // Orders one region of the K loop: R fragment reads, M MFMAs and C copies, the reads first and the
@@ -351,7 +360,7 @@ __global__ __launch_bounds__(WM* WN* kWave, BM / WM * BN / WN > 8192 ? 1 : 2) vo
   constexpr int kFirst = kCopies / 2;             // of these, issued in the second half of a stage
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
   constexpr int kOutCols = GLU ? BN / 2 : BN;
-  static_assert(kAll % kWaves == 0 && BN % 16 == 0 && (!GLU || TN % 2 == 0), "tile");
+  static_assert(kAll % kWaves == 0 && BN % 16 == 0, "tile");
   constexpr int kEpi = epilogue_bytes<TN>();
   static_assert(kEpi * kWaves <= ST * kSlot, "epilogue buffer");
   extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -461,7 +470,7 @@ __global__ __launch_bounds__(WM* WN* kWave, BM / WM * BN / WN > 8192 ? 1 : 2) vo
     return;
   }
   __syncthreads();  // the ring is free
-  epilogue<TN, TM, GLU>(a, acc, lds + wv * kEpi, m0 + wm * TM * 16, int(n0) + wn * (GLU ? TN * 8 : TN * 16), lane);
+  epilogue<TN, TM, GLU>(a, acc, lds + wv * kEpi, m0 + wm * TM * 16, int(n0) + wn * TN * (GLU ? 8 : 16), lane);
 }
 
 // ---------------------------------------------------------------- tiles of 256 x 256
@@ -637,23 +646,22 @@ __global__ __launch_bounds__(512, 2) void k_linear_big(LinearArgs a) {
     return;
   }
   constexpr int kEpi = epilogue_bytes<8>();
-  epilogue<8, 4, GLU>(a, acc, lds + wv * kEpi, m0 + (wv & 3) * 64, int(n0) + (wv >> 2) * (GLU ? 64 : 128), lane);
+  epilogue<8, 4, GLU>(a, acc, lds + wv * kEpi, m0 + (wv & 3) * 64, int(n0) + (wv >> 2) * 128 / (GLU ? 2 : 1), lane);
 }
 
 // ---------------------------------------------------------------- up to 16 tokens
-// A tile of 16 tokens x 16 weight rows (32 gated) whose K is shared by the W waves of the workgroup: wave w
+// A tile of 16 tokens x 16 weight rows whose K is shared by the W waves of the workgroup: wave w
 // takes stages w, w + W, ...  A wave has a ring of ST slots of its own (its weight rows, then XR token rows;
 // with XR = 8 the fragments of tokens 8..15 read those of 0..7 and are dropped) and waits only for its own
 // copies, so the waves run free of each other until they add up their sums.
 template <int W, int ST, int XR, bool GLU>
 __global__ __launch_bounds__(W* kWave) void k_linear_few(LinearArgs a) {
-  constexpr int TN = GLU ? 2 : 1;
-  constexpr int kCopies = 2 * TN + XR / 8, kSlot = kCopies * 1024;
+  constexpr int kCopies = 2 + XR / 8, kSlot = kCopies * 1024;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  static_assert(W * TN * 1024 <= W * ST * kSlot && epilogue_bytes<TN>() <= W * ST * kSlot, "sums and epilogue");
+  static_assert(W * 1024 <= W * ST * kSlot && epilogue_bytes<1>() <= W * ST * kSlot, "sums and epilogue");
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
-  const int64_t n0 = int64_t(blockIdx.x) * 16;
+  const int64_t n0 = int64_t(blockIdx.x) * (GLU ? 8 : 16);
   const int S = a.K / kBK, count = (S - wv + W - 1) / W;  // stages, this wave's
   const int turned = S > 0 ? int(blockIdx.x % unsigned(S)) : 0;
   char* ring = lds + wv * ST * kSlot;
@@ -661,9 +669,9 @@ __global__ __launch_bounds__(W* kWave) void k_linear_few(LinearArgs a) {
   uint32_t off[kCopies];
 #pragma unroll
   for (int i = 0; i < kCopies; ++i) {
-    const int r = 8 * (i < 2 * TN ? i : i - 2 * TN), mine = r + (lane >> 3);
+    const int r = 8 * (i < 2 ? i : i - 2), mine = r + (lane >> 3);
     const uint32_t at = 16 * ((lane & 7) ^ swizzle(mine));
-    if (i < 2 * TN) {
+    if (i < 2) {
       const int64_t row = weight_row<GLU>(a, n0, r);
       base[i] = reinterpret_cast<const char*>(a.w + row * a.K);
       off[i] = uint32_t(weight_row<GLU>(a, n0, mine) - row) * uint32_t(a.K) * 2 + at;
@@ -682,9 +690,7 @@ __global__ __launch_bounds__(W* kWave) void k_linear_few(LinearArgs a) {
       __builtin_amdgcn_global_load_lds((const void*)(base[c] + at + off[c]), (lds_ptr_t)(ring + slot * kSlot + c * 1024), 16,
                                        0, 0);
   };
-  f32x4 acc[TN][1];
-#pragma unroll
-  for (int i = 0; i < TN; ++i) acc[i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+  f32x4 acc[1][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}};
   if (count > 0) {
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i) copy(i, i);
@@ -692,48 +698,41 @@ __global__ __launch_bounds__(W* kWave) void k_linear_few(LinearArgs a) {
     for (int i = 0; i < count; ++i) {
       wait_copies<(ST - 2) * kCopies>();  // this stage is there
       const char* p = ring + slot * kSlot;
-      u32x4 fw[2][TN], fx[2];
+      u32x4 fw[2], fx[2];
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         const int c = 16 * ((4 * hh + g) ^ swizzle(r16));
-#pragma unroll
-        for (int k = 0; k < TN; ++k) fw[hh][k] = *reinterpret_cast<const u32x4*>(p + (16 * k + r16) * kRowB + c);
+        fw[hh] = *reinterpret_cast<const u32x4*>(p + r16 * kRowB + c);
         const int t = r16 & (XR - 1);
-        fx[hh] = *reinterpret_cast<const u32x4*>(p + (16 * TN + t) * kRowB + 16 * ((4 * hh + g) ^ swizzle(t)));
+        fx[hh] = *reinterpret_cast<const u32x4*>(p + (16 + t) * kRowB + 16 * ((4 * hh + g) ^ swizzle(t)));
       }
       // the slot of the stage before: its fragments went into the last pass's MFMAs
       copy(i + ST - 1, slot == 0 ? ST - 1 : slot - 1);
       wait_reads();
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-        for (int k = 0; k < TN; ++k) acc[k][0] = mfma16x16x32(fw[hh][k], fx[hh], acc[k][0]);
+      for (int hh = 0; hh < 2; ++hh) acc[0][0] = mfma16x16x32(fw[hh], fx[hh], acc[0][0]);
       slot = slot + 1 == ST ? 0 : slot + 1;
     }
     wait_copies<0>();
   }
-  if (wv == W - 1 && a.K % kBK != 0) tail<TN, 1, GLU>(a, acc, n0, 0, 0, lane);
+  if (wv == W - 1 && a.K % kBK != 0) tail<1, 1, GLU>(a, acc, n0, 0, 0, lane);
   __syncthreads();  // nobody copies into LDS any more
   f32x4* sums = reinterpret_cast<f32x4*>(lds);
-#pragma unroll
-  for (int i = 0; i < TN; ++i) sums[(wv * TN + i) * kWave + lane] = acc[i][0];
+  sums[wv * kWave + lane] = acc[0][0];
   __syncthreads();
   if (wv != 0) return;
+  acc[0][0] = sums[lane];
 #pragma unroll
-  for (int i = 0; i < TN; ++i) {
-    acc[i][0] = sums[i * kWave + lane];
-#pragma unroll
-    for (int v = 1; v < W; ++v) acc[i][0] += sums[(v * TN + i) * kWave + lane];
-  }
+  for (int v = 1; v < W; ++v) acc[0][0] += sums[v * kWave + lane];
   wave_lds_fence();
-  epilogue<TN, 1, GLU>(a, acc, lds, 0, int(n0), lane);
+  epilogue<1, 1, GLU>(a, acc, lds, 0, int(n0), lane);
 }
 
 template <int W, int ST, int XR, bool GLU>
 hipError_t launch_few(const LinearArgs& a, hipStream_t stream) {
-  constexpr int kBytes = W * ST * ((GLU ? 4 : 2) + XR / 8) * 1024;
+  constexpr int kBytes = W * ST * (2 + XR / 8) * 1024;
   static_assert(kBytes <= 160 * 1024, "LDS");
-  const int64_t tiles = (int64_t(a.N) + 15) / 16;
+  const int64_t tiles = ((GLU ? 2 : 1) * int64_t(a.N) + 15) / 16;
   if (tiles > 0x7FFFFFFF || a.M > XR) return hipErrorInvalidValue;
   const void* fn = reinterpret_cast<const void*>(&k_linear_few<W, ST, XR, GLU>);
   if constexpr (kBytes > 65536) {
@@ -777,31 +776,25 @@ hipError_t launch_tile(const LinearArgs& a, hipStream_t stream) {
 }
 
 // ---------------------------------------------------------------- choice of tile and split
-// Tiles: tokens x weight rows, waves, ring slots (0: k_linear_big).  The gated form needs an even number
-// of 16-row blocks per wave, hence other shapes here and there.
+// Tiles: tokens x weight rows, waves, ring slots (0: k_linear_big).
 struct TileShape {
   int bm, bn, waves, slots;
 };
-constexpr TileShape kTiles[2][15] = {
-    {{256, 256, 8, 0}, {128, 256, 8, 3}, {256, 128, 8, 3}, {160, 160, 4, 3}, {128, 160, 4, 4}, {192, 128, 4, 4},
-     {128, 128, 4, 4}, {128, 128, 4, 2}, {64, 256, 8, 4}, {64, 128, 4, 6}, {64, 64, 4, 4}, {32, 128, 4, 6},
-     {32, 64, 4, 8}, {32, 32, 2, 8}, {16, 16, 1, 12}},
-    {{256, 256, 8, 0}, {128, 256, 8, 3}, {256, 128, 8, 3}, {160, 128, 4, 4}, {128, 192, 4, 4}, {192, 128, 4, 4},
-     {128, 128, 4, 4}, {128, 128, 4, 2}, {64, 256, 8, 4}, {64, 128, 4, 6}, {64, 64, 4, 4}, {32, 128, 4, 6},
-     {32, 64, 4, 8}, {32, 32, 2, 8}, {16, 32, 1, 12}}};
-
+constexpr TileShape kTiles[15] = {{256, 256, 8, 0}, {128, 256, 8, 3}, {256, 128, 8, 3}, {160, 160, 4, 3}, {128, 160, 4, 4},
+                                  {192, 128, 4, 4}, {128, 128, 4, 4}, {128, 128, 4, 2}, {64, 256, 8, 4},  {64, 128, 4, 6},
+                                  {64, 64, 4, 4},   {32, 128, 4, 6},  {32, 64, 4, 8},   {32, 32, 2, 8},   {16, 16, 1, 12}};
 constexpr int kFew8 = 15, kFew16 = 16;  // k_linear_few for up to 8 and 16 tokens
 
 template <bool GLU>
 hipError_t launch_shape(int tile, const LinearArgs& a, hipStream_t stream) {
   switch (tile) {
     case kFew8: return launch_few<4, 4, 8, GLU>(a, stream);
-    case kFew16: return launch_few<4, GLU ? 3 : 5, 16, GLU>(a, stream);
+    case kFew16: return launch_few<4, 5, 16, GLU>(a, stream);
     case 0: return launch_big<GLU>(a, stream);
     case 1: return launch_tile<128, 256, 4, 2, 3, GLU>(a, stream);
     case 2: return launch_tile<256, 128, 4, 2, 3, GLU>(a, stream);
-    case 3: return launch_tile<160, GLU ? 128 : 160, 2, 2, GLU ? 4 : 3, GLU>(a, stream);
-    case 4: return launch_tile<128, GLU ? 192 : 160, 2, 2, 4, GLU>(a, stream);
+    case 3: return launch_tile<160, 160, 2, 2, 3, GLU>(a, stream);
+    case 4: return launch_tile<128, 160, 2, 2, 4, GLU>(a, stream);
     case 5: return launch_tile<192, 128, 2, 2, 4, GLU>(a, stream);
     case 6: return launch_tile<128, 128, 2, 2, 4, GLU>(a, stream);
     case 7: return launch_tile<128, 128, 2, 2, 2, GLU>(a, stream);
@@ -809,9 +802,9 @@ hipError_t launch_shape(int tile, const LinearArgs& a, hipStream_t stream) {
     case 9: return launch_tile<64, 128, 2, 2, 6, GLU>(a, stream);
     case 10: return launch_tile<64, 64, 2, 2, 4, GLU>(a, stream);
     case 11: return launch_tile<32, 128, 1, 4, 6, GLU>(a, stream);
-    case 12: return launch_tile<32, 64, GLU ? 2 : 1, GLU ? 2 : 4, 8, GLU>(a, stream);
-    case 13: return launch_tile<32, 32, GLU ? 2 : 1, GLU ? 1 : 2, 8, GLU>(a, stream);
-    case 14: return launch_tile<16, GLU ? 32 : 16, 1, 1, 12, GLU>(a, stream);
+    case 12: return launch_tile<32, 64, 1, 4, 8, GLU>(a, stream);
+    case 13: return launch_tile<32, 32, 1, 2, 8, GLU>(a, stream);
+    case 14: return launch_tile<16, 16, 1, 1, 12, GLU>(a, stream);
   }
   return hipErrorInvalidValue;
 }
@@ -852,19 +845,19 @@ struct LinearChoice {
 };
 LinearChoice choose(int64_t M, int K, int N, bool glu, int cus) {
   LinearChoice best;
+  const int64_t rows = glu ? 2 * int64_t(N) : N;
   // Up to 16 tokens: the shared-K kernel (one token x 5120 x 5120: 11.0 us, the best tile and split of the
   // others 12.8; x 4096 x 1024: 4.4 and 7.9; 16 tokens x 2048 x 8192: 7.7 and 8.3).  From 9 tokens on only
   // while its tiles are at most two to a compute unit: it reads x once per 16 rows (16 tokens x 6144 x
   // 25,600: 65.7 us, and 55.4 with tiles of 128 rows).
-  const int64_t few = (int64_t(N) + 15) / 16;
+  const int64_t few = (rows + 15) / 16;
   if (M <= 8 || (M <= 16 && few <= 2 * cus)) {
     best.tile = M <= 8 ? kFew8 : kFew16;
     return best;
   }
   double least = 1e30;
-  const int64_t rows = glu ? 2 * int64_t(N) : N;
   for (int i = 0; i < 15; ++i) {
-    const TileShape& t = kTiles[glu][i];
+    const TileShape& t = kTiles[i];
     const int64_t tiles = (M + t.bm - 1) / t.bm * ((rows + t.bn - 1) / t.bn);
     if (tiles > (int64_t(1) << 24)) continue;  // far below what a launch takes
     for (int parts : {1, 2, 3, 4, 6, 8}) {

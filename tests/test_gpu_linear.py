@@ -36,7 +36,8 @@ TILES = [(2067, 256, 4991), (1803, 832, 3400), (822, 4912, 3006), (512, 4560, 51
 GATED_TILES = [(963, 248, 4830), (1561, 840, 1828), (331, 4936, 2714), (1163, 1032, 3214), (194, 4736, 4267), (391, 120, 4618),
                (146, 4336, 1833), (323, 280, 5664), (66, 4072, 5545), (925, 304, 3182), (173, 4016, 2770), (67, 4688, 2727),
                (385, 64, 4707), (258, 64, 5478), (180, 3296, 2738), (33, 2936, 4279), (71, 64, 4218), (73, 3392, 1381),
-               (691, 3888, 17), (301, 5120, 10240)]
+               (691, 3888, 17), (301, 5120, 10240), (936, 240, 5235), (484, 832, 5870),
+               (222, 4424, 5244), (215, 4640, 5264), (136, 5136, 1831)]
 
 
 @pytest.mark.parametrize("M,K,N,glus", [(*s, (False, True)) for s in SIZES] + [(*s, (False,)) for s in TILES] +

@@ -169,9 +169,8 @@ def test_binding_refusals():
             eg.engram_batch_plan(pages, *(args | {k: v.long()}).values(), plan)
         with pytest.raises(ValueError, match=k):
             eg.engram_batch_plan(pages, *(args | {k: torch.zeros(7, dtype=i32)}).values(), plan)
-    plan.slots = plan.slots[:5]
-    with pytest.raises(ValueError, match="plan.slots"):
-        eg.engram_batch_plan(pages, *args.values(), plan)
+    with pytest.raises(AttributeError):
+        plan.slots = plan.slots[:5]
     plan, hl = eg.BatchPlan(3, 8, device="cpu"), eg.make_hash_layout(1, 3, 2, 2, 50, 8)
     args = dict(token_map=torch.zeros(50, dtype=i32), multipliers=torch.zeros((1, 3), dtype=torch.int64),
                 primes=torch.zeros((1, 2, 2), dtype=torch.int64), offsets=torch.zeros((1, 4), dtype=torch.int64),
