@@ -91,8 +91,8 @@ __device__ __forceinline__ void store8(const LinearArgs& a, int64_t m, int n, fl
         lo += *reinterpret_cast<const f32x4*>(res);
         hi += *reinterpret_cast<const f32x4*>(res + 4);
       }
-      *reinterpret_cast<f32x4*>(out) = lo;
-      *reinterpret_cast<f32x4*>(out + 4) = hi;
+      __builtin_nontemporal_store(lo, reinterpret_cast<f32x4*>(out));
+      __builtin_nontemporal_store(hi, reinterpret_cast<f32x4*>(out + 4));
       return;
     }
 #pragma unroll
@@ -111,8 +111,9 @@ __device__ __forceinline__ void store8(const LinearArgs& a, int64_t m, int n, fl
         v[2 * e + 1] += bf16_hi(w[e]);
       }
     }
-    *reinterpret_cast<u32x4*>(out) =
-        u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    __builtin_nontemporal_store(
+        u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])},
+        reinterpret_cast<u32x4*>(out));
     return;
   }
 #pragma unroll
@@ -302,34 +303,34 @@ __device__ __forceinline__ void store_partial(const LinearArgs& a, const f32x4 (
     for (int j = 0; j < TM; ++j) p[(i * TM + j) * kWave] = acc[i][j];
 }
 
-// Adds the parts of a wave's blocks in order and finishes them.  One wave per workgroup.
+// Adds the parts of 16 tokens of a wave's blocks in order and finishes them; one wave per workgroup (with
+// all of a wave's tokens in one, 1000 x 10,240 x 5120 in three parts took 28 us, and 19 us like this).
 template <int BM, int BN, int WM, int WN, bool GLU>
 __global__ __launch_bounds__(kWave) void k_linear_join(LinearArgs a) {
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16, kOutCols = GLU ? BN / 2 : BN;
   __shared__ __attribute__((aligned(16))) char lds[epilogue_bytes<TN>()];
   const int lane = threadIdx.x;
   const int64_t tbs = (a.M + BM - 1) / BM, cbs = (int64_t(a.N) + kOutCols - 1) / kOutCols, slots = tbs * cbs * WM * WN;
-  const int64_t at = blockIdx.x;
+  const int j = int(blockIdx.x % TM);
+  const int64_t at = blockIdx.x / TM;
   const int wv = int(at % (WM * WN));
   int64_t tb, cb;
   tile_of(at / (WM * WN), tbs, cbs, &tb, &cb);
-  const f32x4* p = reinterpret_cast<const f32x4*>(a.partials) + at * (TN * TM * kWave) + lane;
-  f32x4 acc[TN][TM];
-#pragma unroll
-  for (int i = 0; i < TN; ++i)
-#pragma unroll
-    for (int j = 0; j < TM; ++j) acc[i][j] = p[(i * TM + j) * kWave];
-  for (int part = 1; part < a.parts; ++part) {
-    p += slots * (TN * TM * kWave);
-#pragma unroll
-    for (int i = 0; i < TN; ++i)
-#pragma unroll
-      for (int j = 0; j < TM; ++j) acc[i][j] += p[(i * TM + j) * kWave];
-  }
   // which part of the tile a wave holds: as in k_linear_big (the 256 x 256 tile) and k_linear
   constexpr bool kGroups = BM == 256 && BN == 256;
   const int wm = kGroups ? wv % WM : wv / WN, wn = kGroups ? wv / WM : wv % WN;
-  epilogue<TN, TM, GLU>(a, acc, lds, tb * BM + wm * TM * 16, int(cb * kOutCols) + wn * TN * (GLU ? 8 : 16), lane);
+  const int64_t m0 = tb * BM + (wm * TM + j) * 16;
+  if (m0 >= a.M) return;
+  const f32x4* p = reinterpret_cast<const f32x4*>(a.partials) + at * (TN * TM * kWave) + j * kWave + lane;
+  f32x4 acc[TN][1];
+#pragma unroll
+  for (int i = 0; i < TN; ++i) acc[i][0] = p[i * TM * kWave];
+  for (int part = 1; part < a.parts; ++part) {
+    p += slots * (TN * TM * kWave);
+#pragma unroll
+    for (int i = 0; i < TN; ++i) acc[i][0] += p[i * TM * kWave];
+  }
+  epilogue<TN, 1, GLU>(a, acc, lds, m0, int(cb * kOutCols) + wn * TN * (GLU ? 8 : 16), lane);
 }
 
 // Orders one region of the K loop: R fragment reads, M MFMAs and C copies, the reads first and the
@@ -744,17 +745,19 @@ hipError_t launch_few(const LinearArgs& a, hipStream_t stream) {
   return hipLaunchKernel(fn, dim3(unsigned(tiles)), dim3(W * kWave), params, kBytes, stream);
 }
 
-// Launches `fn` over `tiles` tiles times a.parts parts, then the kernel that joins the parts.
-hipError_t launch_parts(const LinearArgs& a, const void* fn, int bytes, int waves, const void* join, int64_t tiles,
-                        hipStream_t stream) {
-  if (a.parts < 1 || tiles > 0x7FFFFFFF / a.parts || tiles * waves > 0x7FFFFFFF) return hipErrorInvalidValue;
+// Launches `fn` over `tiles` tiles times a.parts parts, then the kernel that joins the parts
+// (`joins` workgroups per tile: its waves times their blocks of 16 tokens).
+hipError_t launch_parts(const LinearArgs& a, const void* fn, int bytes, int waves, const void* join, int joins,
+                        int64_t tiles, hipStream_t stream) {
+  if (a.parts < 1 || tiles > 0x7FFFFFFF / a.parts || (a.parts > 1 && tiles * joins > 0x7FFFFFFF))
+    return hipErrorInvalidValue;
   hipError_t e = bytes > 65536 ? hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) : hipSuccess;
   if (e != hipSuccess) return e;
   LinearArgs args = a;
   void* params[] = {&args};
   e = hipLaunchKernel(fn, dim3(unsigned(tiles * a.parts)), dim3(waves * kWave), params, bytes, stream);
   if (e != hipSuccess || a.parts == 1) return e;
-  return hipLaunchKernel(join, dim3(unsigned(tiles * waves)), dim3(kWave), params, 0, stream);
+  return hipLaunchKernel(join, dim3(unsigned(tiles * joins)), dim3(kWave), params, 0, stream);
 }
 
 template <bool GLU>
@@ -762,7 +765,7 @@ hipError_t launch_big(const LinearArgs& a, hipStream_t stream) {
   constexpr int kOut = GLU ? kBig / 2 : kBig;
   const int64_t tiles = (a.M + kBig - 1) / kBig * ((int64_t(a.N) + kOut - 1) / kOut);
   return launch_parts(a, reinterpret_cast<const void*>(&k_linear_big<GLU>), kBigLds, 8,
-                      reinterpret_cast<const void*>(&k_linear_join<kBig, kBig, 4, 2, GLU>), tiles, stream);
+                      reinterpret_cast<const void*>(&k_linear_join<kBig, kBig, 4, 2, GLU>), 8 * 4, tiles, stream);
 }
 
 template <int BM, int BN, int WM, int WN, int ST, bool GLU>
@@ -772,7 +775,7 @@ hipError_t launch_tile(const LinearArgs& a, hipStream_t stream) {
   static_assert(kBytes <= 160 * 1024, "LDS");
   const int64_t tiles = (a.M + BM - 1) / BM * ((int64_t(a.N) + kOut - 1) / kOut);
   return launch_parts(a, reinterpret_cast<const void*>(&k_linear<BM, BN, WM, WN, ST, GLU>), kBytes, WM * WN,
-                      reinterpret_cast<const void*>(&k_linear_join<BM, BN, WM, WN, GLU>), tiles, stream);
+                      reinterpret_cast<const void*>(&k_linear_join<BM, BN, WM, WN, GLU>), WN * BM / 16, tiles, stream);
 }
 
 // ---------------------------------------------------------------- choice of tile and split
@@ -810,11 +813,11 @@ hipError_t launch_shape(int tile, const LinearArgs& a, hipStream_t stream) {
 }
 
 // Microseconds that a tile shape and a split take, as a model of what bounds them: per stage and
-// compute unit, the copies (68 KB per us into its LDS) or the MFMAs (8.4 TFLOP/s); per round of
-// workgroups a prologue and an epilogue; over all, the bytes at 5.7 TB/s; the parts written and read at
-// 6.4 TB/s and a second launch.  Fitted to 75 shapes, 1..8192 tokens, K 128..10240, N 72..25600, with every
-// tile and split timed: the choice is within 3% of the best one on average (15% at worst; the first rule,
-// by token count alone, was 60% above it).
+// compute unit the copies into its LDS (63 KB per us); per round of workgroups a prologue and an
+// epilogue; over all, the bytes at 4.85 TB/s; the parts written and read at 7.1 TB/s and a second
+// launch.  Fitted to 90 shapes, 10..8192 tokens, K 128..10240, N 72..25600, with every tile and split timed:
+// the choice takes 1.7% longer than the best one on average and 20% at worst (a first rule, by token
+// count alone, 60% on average).
 double model_us(const TileShape& t, int parts, int64_t M, int K, int64_t rows, int64_t N, int cus) {
   const double tiles = double((M + t.bm - 1) / t.bm) * double((rows + t.bn - 1) / t.bn);
   const int lds = t.slots == 0 ? kBigLds : t.slots * (t.bm + t.bn) * kRowB;
@@ -826,13 +829,12 @@ double model_us(const TileShape& t, int parts, int64_t M, int K, int64_t rows, i
   n = n < fit ? n : fit;
   double rounds = work / (cus * n);
   rounds = rounds < 4 ? ceil(rounds) : rounds + 0.5;
-  const double copies = n * (t.bm + t.bn) * kRowB / 1024 / 68.0, mfma = n * t.bm * t.bn * 128 / 8.4e6;
-  double stage = copies > mfma ? copies : mfma;
-  stage = stage > 0.08 ? stage : 0.08;
-  const double tile_us = 1.0 + rounds * (stages * stage + 2.8 + t.bm * t.bn * 1.85e-4);
-  const double mem_us = 1.0 + 2.0 * (double(M) * K + double(rows) * K + double(M) * N) / 5.7e6;
-  double us = tile_us > mem_us ? tile_us + 0.2 * mem_us : mem_us + 0.2 * tile_us;
-  if (parts > 1) us += 2.4 + parts * tiles * t.bm * t.bn * 8 / 6.4e6;
+  double stage = n * (t.bm + t.bn) * kRowB / 1024 / 63.0;
+  stage = stage > 0.13 ? stage : 0.13;
+  const double tile_us = 1.7 + rounds * (stages * stage + 2.1 + t.bm * t.bn * 1.55e-4);
+  const double mem_us = 1.7 + 2.0 * (double(M) * K + double(rows) * K + double(M) * N) / 4.85e6;
+  double us = tile_us > mem_us ? tile_us + 0.23 * mem_us : mem_us + 0.23 * tile_us;
+  if (parts > 1) us += 2.5 + parts * tiles * t.bm * t.bn * 8 / 7.1e6;
   return us;
 }
 
