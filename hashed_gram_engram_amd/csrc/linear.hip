@@ -784,7 +784,7 @@ struct TileShape {
   int bm, bn, waves, slots;
 };
 constexpr TileShape kTiles[15] = {{256, 256, 8, 0}, {128, 256, 8, 3}, {256, 128, 8, 3}, {160, 160, 4, 3}, {128, 160, 4, 4},
-                                  {192, 128, 4, 4}, {128, 128, 4, 4}, {128, 128, 4, 2}, {64, 256, 8, 4},  {64, 128, 4, 6},
+                                  {192, 128, 4, 4}, {128, 128, 4, 4}, {128, 128, 4, 2}, {64, 256, 8, 4},  {64, 128, 8, 6},
                                   {64, 64, 4, 4},   {32, 128, 4, 6},  {32, 64, 4, 8},   {32, 32, 2, 8},   {16, 16, 1, 12}};
 constexpr int kFew8 = 15, kFew16 = 16;  // k_linear_few for up to 8 and 16 tokens
 
@@ -802,7 +802,7 @@ hipError_t launch_shape(int tile, const LinearArgs& a, hipStream_t stream) {
     case 6: return launch_tile<128, 128, 2, 2, 4, GLU>(a, stream);
     case 7: return launch_tile<128, 128, 2, 2, 2, GLU>(a, stream);
     case 8: return launch_tile<64, 256, 2, 4, 4, GLU>(a, stream);
-    case 9: return launch_tile<64, 128, 2, 2, 6, GLU>(a, stream);
+    case 9: return launch_tile<64, 128, 2, 4, 6, GLU>(a, stream);
     case 10: return launch_tile<64, 64, 2, 2, 4, GLU>(a, stream);
     case 11: return launch_tile<32, 128, 1, 4, 6, GLU>(a, stream);
     case 12: return launch_tile<32, 64, 1, 4, 8, GLU>(a, stream);

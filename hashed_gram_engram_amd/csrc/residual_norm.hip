@@ -24,6 +24,13 @@ __device__ __forceinline__ void unpack8(u32x4 w, float (&v)[8]) {
 __device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
   return u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
 }
+// The bf16 bits that unpack8 took (a rounding would change a NaN's).
+__device__ __forceinline__ u32x4 bits8(const float (&v)[8]) {
+  u32x4 w;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = (__float_as_uint(v[2 * e]) >> 16) | (__float_as_uint(v[2 * e + 1]) & 0xFFFF0000u);
+  return w;
+}
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
 #pragma unroll
@@ -149,7 +156,8 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_residual_norm(NormArgs a)
         __builtin_nontemporal_store(f32x4{r[k][0], r[k][1], r[k][2], r[k][3]}, reinterpret_cast<f32x4*>(o));
         __builtin_nontemporal_store(f32x4{r[k][4], r[k][5], r[k][6], r[k][7]}, reinterpret_cast<f32x4*>(o + 4));
       } else {
-        __builtin_nontemporal_store(pack8(r[k]), reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + row * a.dim + 8 * v));
+        const u32x4 w = open ? pack8(r[k]) : bits8(r[k]);
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + row * a.dim + 8 * v));
       }
     }
   }
@@ -199,8 +207,6 @@ hipError_t launch_threads(const NormArgs& a, hipStream_t stream) {
   if (nv <= 3) return launch_norm<T, 3>(a, stream);
   if (nv <= 4) return launch_norm<T, 4>(a, stream);
   if (nv <= 5) return launch_norm<T, 5>(a, stream);
-  if constexpr (T == 1024)
-    if (nv <= 8) return launch_norm<T, 8>(a, stream);
   return hipErrorInvalidValue;
 }
 

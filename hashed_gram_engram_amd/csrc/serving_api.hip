@@ -31,7 +31,7 @@ engram_status engram_page_layout_check(const engram_page_layout* l) {
 
 engram_status engram_norm_layout_check(const engram_norm_layout* l) {
   if (l == nullptr) return ENGRAM_E_NULL;
-  if (l->hc < 1 || l->hc > 64 || l->dim < 8 || l->dim % 8 != 0 || l->dim > 65536) return ENGRAM_E_LAYOUT;
+  if (l->hc < 1 || l->hc > 64 || l->dim < 8 || l->dim % 8 != 0 || l->dim > 40960) return ENGRAM_E_LAYOUT;
   if (l->y_streams != 1 && l->y_streams != l->hc) return ENGRAM_E_LAYOUT;
   if (l->stream_format != ENGRAM_STREAM_BF16 && l->stream_format != ENGRAM_STREAM_FP32) return ENGRAM_E_LAYOUT;
   if (l->gate < ENGRAM_GATE_NONE || l->gate > ENGRAM_GATE_FEATURE) return ENGRAM_E_LAYOUT;

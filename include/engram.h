@@ -340,7 +340,7 @@ typedef enum { ENGRAM_GATE_NONE = 0, ENGRAM_GATE_TOKEN = 1, ENGRAM_GATE_FEATURE 
 
 typedef struct {
   int32_t hc;            /* residual streams, 1 .. 64                                          */
-  int32_t dim;           /* features, a multiple of 8, at most 65536                           */
+  int32_t dim;           /* features, a multiple of 8, at most 40960                           */
   int32_t y_streams;     /* hc, or 1: one block output shared by every stream                  */
   int32_t stream_format; /* engram_stream_format of x and out                                  */
   int32_t gate;          /* engram_gate_kind                                                   */

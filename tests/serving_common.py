@@ -92,7 +92,7 @@ def hash_ref(h, ids, mask, plan, block_size, table, history):
 
 def norm_ref(x, y, gate, kind, post_w, pre_w, mask, alpha, beta, post_eps, pre_eps, post_norm=True):
     """(out, h, bound of out, bound of h) in 64 bits, from tensors on any device.  Bounds: fp32 sums of
-    squares of positive terms, at most 64 in a thread, 6 levels of a tree over a wave and 16 waves one
+    squares of positive terms, at most 40 in a thread, 6 levels of a tree over a wave and 16 waves one
     after the other, are within 90 u, the root halves that; with the division, root, weight, gate (exp
     within 4 u) and scale a term of n is within 64 u; then two products, a sum and the output's rounding."""
     x64 = x.double().cpu()

@@ -32,7 +32,7 @@ def test_layout_checks():
                [dict(block_size=0), dict(block_size=-4), dict(max_blocks=0), dict(n_blocks=0), dict(n_blocks=(1 << 30) + 1),
                 dict(block_size=1 << 20, max_blocks=1 << 11)])
     bad_fields(lambda: eg.make_norm_layout(4, 5120), LIB.engram_norm_layout_check,
-               [dict(hc=0), dict(hc=65), dict(dim=0), dict(dim=12), dict(dim=65544), dict(y_streams=2), dict(stream_format=2),
+               [dict(hc=0), dict(hc=65), dict(dim=0), dict(dim=12), dict(dim=40968), dict(y_streams=2), dict(stream_format=2),
                 dict(gate=3), dict(gate=-1), dict(post_norm=2), dict(pre_norm=-1), dict(alpha=float("inf")),
                 dict(beta=float("nan")), dict(post_eps=-1.0), dict(pre_eps=float("inf"))])
     bad_fields(lambda: eg.make_linear_layout(5120, 777), LIB.engram_linear_layout_check,
