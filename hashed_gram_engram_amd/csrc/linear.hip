@@ -224,8 +224,8 @@ __device__ __forceinline__ int64_t weight_row(const LinearArgs& a, int64_t n0, i
 
 // The tile of workgroup b of `tiles`: workgroups are dealt to the 8 XCDs round robin, so each XCD
 // takes a run of consecutive tiles, token blocks fastest: a weight panel is read by one XCD, once.
-__device__ __forceinline__ int64_t xcd_tile(int64_t b, int64_t tiles) {
-  const int64_t q = tiles >> 3, rem = tiles & 7, x = b & 7;
+__device__ __forceinline__ uint32_t xcd_tile(uint32_t b, uint32_t tiles) {
+  const uint32_t q = tiles >> 3, rem = tiles & 7, x = b & 7;
   return x * q + (x < rem ? x : rem) + (b >> 3);
 }
 
@@ -238,31 +238,32 @@ __device__ __forceinline__ int swizzle(int r) { return (r >> 1) & 7; }
 
 // Tiles in order: groups of 8 token blocks, and in a group token blocks fastest, so that the tiles that
 // run on an XCD at one time share token panels as well as weight panels in its L2.
-__device__ __forceinline__ void tile_of(int64_t tile, int64_t tbs, int64_t cbs, int64_t* tb, int64_t* cb) {
-  constexpr int64_t kGroup = 8;
-  const int64_t g = tile / (kGroup * cbs), in = tile - g * kGroup * cbs;
-  const int64_t size = tbs - g * kGroup < kGroup ? tbs - g * kGroup : kGroup;
-  *tb = g * kGroup + in % size;
+// (Tiles are counted in 32 bits: a 64-bit division is some 100 instructions before the first copy.)
+__device__ __forceinline__ void tile_of(uint32_t tile, uint32_t tbs, uint32_t cbs, uint32_t* tb, uint32_t* cb) {
+  constexpr uint32_t kGroup = 8;
+  const uint32_t g = tbs <= kGroup ? 0 : tile / (kGroup * cbs), in = tile - g * kGroup * cbs;
+  const uint32_t size = tbs - g * kGroup < kGroup ? tbs - g * kGroup : kGroup;
   *cb = in / size;
+  *tb = g * kGroup + in - *cb * size;
 }
 
 // What a workgroup computes: a tile, and of its K the whole stages [first, first + stages) and, in the
 // last part, the features past the last whole stage.  Split over K, part 0 of every tile comes first:
 // the workgroups of an XCD then share panels as without a split.
 struct Share {
-  int64_t tile, tb, cb;
+  uint32_t tile, tb, cb;
   int part, first, stages;
   bool tail;
 };
-__device__ __forceinline__ Share share_of(const LinearArgs& a, int64_t tbs, int64_t cbs) {
+__device__ __forceinline__ Share share_of(const LinearArgs& a, uint32_t tbs, uint32_t cbs) {
   Share s;
-  const int64_t tiles = tbs * cbs, at = xcd_tile(blockIdx.x, gridDim.x);
-  s.part = int(at / tiles);
+  const uint32_t tiles = tbs * cbs, at = xcd_tile(blockIdx.x, gridDim.x);
+  const int S = a.K / kBK;
+  s.part = a.parts > 1 ? int(at / tiles) : 0;
   s.tile = at - s.part * tiles;
   tile_of(s.tile, tbs, cbs, &s.tb, &s.cb);
-  const int S = a.K / kBK;
-  s.first = int(int64_t(S) * s.part / a.parts);
-  s.stages = int(int64_t(S) * (s.part + 1) / a.parts) - s.first;
+  s.first = a.parts > 1 ? S * s.part / a.parts : 0;  // (S < 2^14)
+  s.stages = a.parts > 1 ? S * (s.part + 1) / a.parts - s.first : S;
   s.tail = s.part == a.parts - 1 && a.K % kBK != 0;
   return s;
 }
@@ -310,18 +311,19 @@ __global__ __launch_bounds__(kWave) void k_linear_join(LinearArgs a) {
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16, kOutCols = GLU ? BN / 2 : BN;
   __shared__ __attribute__((aligned(16))) char lds[epilogue_bytes<TN>()];
   const int lane = threadIdx.x;
-  const int64_t tbs = (a.M + BM - 1) / BM, cbs = (int64_t(a.N) + kOutCols - 1) / kOutCols, slots = tbs * cbs * WM * WN;
+  const uint32_t tbs = uint32_t((a.M + BM - 1) / BM), cbs = uint32_t((a.N + kOutCols - 1) / kOutCols);
+  const int64_t slots = int64_t(tbs) * cbs * WM * WN;
   const int j = int(blockIdx.x % TM);
-  const int64_t at = blockIdx.x / TM;
+  const uint32_t at = blockIdx.x / TM;
   const int wv = int(at % (WM * WN));
-  int64_t tb, cb;
+  uint32_t tb, cb;
   tile_of(at / (WM * WN), tbs, cbs, &tb, &cb);
   // which part of the tile a wave holds: as in k_linear_big (the 256 x 256 tile) and k_linear
   constexpr bool kGroups = BM == 256 && BN == 256;
   const int wm = kGroups ? wv % WM : wv / WN, wn = kGroups ? wv / WM : wv % WN;
-  const int64_t m0 = tb * BM + (wm * TM + j) * 16;
+  const int64_t m0 = int64_t(tb) * BM + (wm * TM + j) * 16;
   if (m0 >= a.M) return;
-  const f32x4* p = reinterpret_cast<const f32x4*>(a.partials) + at * (TN * TM * kWave) + j * kWave + lane;
+  const f32x4* p = reinterpret_cast<const f32x4*>(a.partials) + int64_t(at) * (TN * TM * kWave) + j * kWave + lane;
   f32x4 acc[TN][1];
 #pragma unroll
   for (int i = 0; i < TN; ++i) acc[i][0] = p[i * TM * kWave];
@@ -367,12 +369,12 @@ __global__ __launch_bounds__(WM* WN* kWave, BM / WM * BN / WN > 8192 ? 1 : 2) vo
   extern __shared__ __attribute__((aligned(16))) char lds[];
 
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t tbs = (a.M + BM - 1) / BM, cbs = (int64_t(a.N) + kOutCols - 1) / kOutCols;
+  const uint32_t tbs = uint32_t((a.M + BM - 1) / BM), cbs = uint32_t((a.N + kOutCols - 1) / kOutCols);
   const Share sh = share_of(a, tbs, cbs);
-  const int64_t m0 = sh.tb * BM, n0 = sh.cb * kOutCols;
+  const int64_t m0 = int64_t(sh.tb) * BM, n0 = int64_t(sh.cb) * kOutCols;
   const int S = sh.stages;
 
-  const int turned = S > 0 ? int(sh.cb % S) : 0;
+  const int turned = S > 0 ? int(sh.cb % uint32_t(S)) : 0;
 
   // lane l of copy q fills bytes 16 l of 1 KB: row 8 q + l / 8, position l % 8.  Its 8 rows start at
   // a wave-uniform address; the lane's part is a 32-bit offset.
@@ -467,7 +469,7 @@ __global__ __launch_bounds__(WM* WN* kWave, BM / WM * BN / WN > 8192 ? 1 : 2) vo
     tail<TN, TM, GLU>(a, acc, n0, wn * TN * 16, m0 + wm * TM * 16, lane);
   }
   if (a.parts > 1) {
-    store_partial<TN, TM>(a, acc, (sh.part * tbs * cbs + sh.tile) * kWaves + wv, lane);
+    store_partial<TN, TM>(a, acc, (int64_t(sh.part) * tbs * cbs + sh.tile) * kWaves + wv, lane);
     return;
   }
   __syncthreads();  // the ring is free
@@ -610,9 +612,9 @@ __global__ __launch_bounds__(512, 2) void k_linear_big(LinearArgs a) {
   constexpr int kOut = GLU ? kBig / 2 : kBig;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t tbs = (a.M + kBig - 1) / kBig, cbs = (int64_t(a.N) + kOut - 1) / kOut;
+  const uint32_t tbs = uint32_t((a.M + kBig - 1) / kBig), cbs = uint32_t((a.N + kOut - 1) / kOut);
   const Share sh = share_of(a, tbs, cbs);
-  const int64_t m0 = sh.tb * kBig, n0 = sh.cb * kOut;
+  const int64_t m0 = int64_t(sh.tb) * kBig, n0 = int64_t(sh.cb) * kOut;
   BigPipe p;
   p.wv = wv;
 #pragma unroll
@@ -637,13 +639,13 @@ __global__ __launch_bounds__(512, 2) void k_linear_big(LinearArgs a) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   if (sh.stages > 0) {
-    const int turned = int(sh.cb % sh.stages);
+    const int turned = int(sh.cb % uint32_t(sh.stages));
     if (wv < 4) big_loop<0>(acc, p, lds, sh.first, sh.stages, turned);
     else big_loop<1>(acc, p, lds, sh.first, sh.stages, turned);
   }
   if (sh.tail) tail<8, 4, GLU>(a, acc, n0, (wv >> 2) * 128, m0 + (wv & 3) * 64, lane);
   if (a.parts > 1) {
-    store_partial<8, 4>(a, acc, (sh.part * tbs * cbs + sh.tile) * 8 + wv, lane);
+    store_partial<8, 4>(a, acc, (int64_t(sh.part) * tbs * cbs + sh.tile) * 8 + wv, lane);
     return;
   }
   constexpr int kEpi = epilogue_bytes<8>();

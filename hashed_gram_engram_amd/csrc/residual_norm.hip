@@ -64,12 +64,12 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_residual_norm(NormArgs a)
   constexpr int kRows = kThreads / T;  // rows of a workgroup
   __shared__ float tmp[kThreads / kWave];
   const int lane = threadIdx.x % T;
-  const int64_t rows = a.M * a.hc;
-  const int64_t row_raw = int64_t(blockIdx.x) * kRows + threadIdx.x / T;
+  // (rows are fewer than 2^31: 32-bit divisions)
+  const uint32_t rows = uint32_t(a.M * a.hc), row_raw = blockIdx.x * uint32_t(kRows) + threadIdx.x / T;
   const bool in = row_raw < rows;
   const int64_t row = in ? row_raw : rows - 1;  // rows past the last repeat it and store nothing
-  const int64_t m = row / a.hc;
-  const int s = int(row - m * a.hc);
+  const int64_t m = uint32_t(row) / uint32_t(a.hc);
+  const int s = int(uint32_t(row) - uint32_t(m) * uint32_t(a.hc));
   const int ys = a.y_streams == 1 ? 0 : s;
   const int nvec = a.dim >> 3;
   const bool has_y = a.y != nullptr;
