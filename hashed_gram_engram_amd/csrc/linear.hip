@@ -335,24 +335,6 @@ __global__ __launch_bounds__(kWave) void k_linear_join(LinearArgs a) {
   epilogue<TN, 1, GLU>(a, acc, lds, m0, int(cb * kOutCols) + wn * TN * (GLU ? 8 : 16), lane);
 }
 
-// Orders one region of the K loop: R fragment reads, M MFMAs and C copies, the reads first and the
-// copies spread out, each behind an MFMA.  A copy instruction occupies a CU's address unit for 16
-// cycles and an MFMA its matrix unit for 16: a burst of either stalls the wave that the other needs.
-template <int R, int M, int C>
-__device__ __forceinline__ void interleave() {
-  constexpr int kMfma = 0x8, kVmem = 0x20, kRead = 0x100;
-  // the reads over the first three quarters of the MFMAs, the copies over all of them
-#pragma unroll
-  for (int i = 0; i < M; ++i) {
-    const int r0 = min(R, i * R * 4 / (3 * M)), r1 = min(R, (i + 1) * R * 4 / (3 * M));
-    const int c0 = i * C / M, c1 = (i + 1) * C / M;
-    if (r1 > r0) __builtin_amdgcn_sched_group_barrier(kRead, 1, 0);
-    if (r1 > r0 + 1) __builtin_amdgcn_sched_group_barrier(kRead, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
-    if (c1 > c0) __builtin_amdgcn_sched_group_barrier(kVmem, 1, 0);
-  }
-}
-
 template <int BM, int BN, int WM, int WN, int ST, bool GLU>
 __global__ __launch_bounds__(WM* WN* kWave, BM / WM * BN / WN > 8192 ? 1 : 2) void k_linear(LinearArgs a) {
   constexpr int kWaves = WM * WN;
@@ -419,18 +401,29 @@ __global__ __launch_bounds__(WM* WN* kWave, BM / WM * BN / WN > 8192 ? 1 : 2) vo
     u32x4 w[TN], x[TM];
   };
   const int w_off = (wn * TN * 16 + r16) * kRowB, x_off = (BN + wm * TM * 16 + r16) * kRowB;
-  auto read = [&](Frags& f, int slot, int hh) {
-    const char* b = lds + slot * kSlot + 16 * ((4 * hh + g) ^ swizzle(r16));
-#pragma unroll
-    for (int i = 0; i < TN; ++i) f.w[i] = *reinterpret_cast<const u32x4*>(b + w_off + i * 16 * kRowB);
-#pragma unroll
-    for (int j = 0; j < TM; ++j) f.x[j] = *reinterpret_cast<const u32x4*>(b + x_off + j * 16 * kRowB);
+  // fragment q of a half stage: weight rows, then tokens
+  auto read = [&](Frags& f, const char* b, int q) {
+    if (q < TN) f.w[q] = *reinterpret_cast<const u32x4*>(b + w_off + q * 16 * kRowB);
+    else f.x[q - TN] = *reinterpret_cast<const u32x4*>(b + x_off + (q - TN) * 16 * kRowB);
   };
-  auto multiply = [&](const Frags& f) {
+  auto half_of = [&](int slot, int hh) { return lds + slot * kSlot + 16 * ((4 * hh + g) ^ swizzle(r16)); };
+  // Multiplies one half stage, in this order: the reads of the next one's fragments over the first three
+  // quarters of the MFMAs, copies i0 .. i1 - 1 of stage t over all of them.  A copy instruction occupies
+  // the CU's address unit for 16 cycles, an MFMA its matrix unit for 16: a burst of either stalls the wave
+  // that the other needs.
+  auto half = [&](const Frags& now, Frags& next, const char* from, int t, int slot, int i0, int i1) {
+    constexpr int R = TN + TM, M = TN * TM;
+    const int C = i1 - i0;
 #pragma unroll
-    for (int i = 0; i < TN; ++i)
+    for (int m = 0; m < M; ++m) {
+      const int r0 = m * R * 4 / (3 * M), r1 = (m + 1) * R * 4 / (3 * M);
 #pragma unroll
-      for (int j = 0; j < TM; ++j) acc[i][j] = mfma16x16x32(f.w[i], f.x[j], acc[i][j]);
+      for (int q = r0; q < (m == M - 1 ? R : r1); ++q)
+        if (q < R) read(next, from, q);
+      acc[m / TM][m % TM] = mfma16x16x32(now.w[m / TM], now.x[m % TM], acc[m / TM][m % TM]);
+      __builtin_amdgcn_sched_barrier(0);
+      copy(t, slot, i0 + m * C / M, i0 + (m + 1) * C / M);
+    }
   };
   if (S > 0) {
 #pragma unroll
@@ -438,28 +431,23 @@ __global__ __launch_bounds__(WM* WN* kWave, BM / WM * BN / WN > 8192 ? 1 : 2) vo
     copy(ST - 1, ST - 1, 0, kFirst);
     wait_copies<(ST - 2) * kCopies + kFirst>();
     group_barrier();
-    Frags f[2];
-    read(f[0], 0, 0);
+    Frags f0, f1;
+#pragma unroll
+    for (int q = 0; q < TN + TM; ++q) read(f0, half_of(0, 0), q);
     int slot = 0, before = ST - 1;
     for (int t = 0; t < S; ++t) {
       const int next = slot + 1 == ST ? 0 : slot + 1;
       wait_reads();
       // first half; the rest of stage t - 1 + ST goes into stage t - 1's slot
-      read(f[1], slot, 1);
-      multiply(f[0]);
-      copy(t - 1 + ST, before, kFirst, kCopies);
-      interleave<TN + TM, TN * TM, kCopies - kFirst>();
+      half(f0, f1, half_of(slot, 1), t - 1 + ST, before, kFirst, kCopies);
       // Stage t + 1 is in LDS for everyone once only the copies of stages t + 2 .. t + ST - 1 are in
       // flight, and nobody reads stage t's slot any more once every wave has its last fragments.
       wait_copies<(ST - 2) * kCopies>();
       wait_reads();
       group_barrier();
-      // second half; stage t + ST starts into stage t's slot
-      read(f[0], next, 0);  // (past the last stage: a repeat, not used)
-      multiply(f[1]);
-      copy(t + ST, slot, 0, kFirst);
-      interleave<TN + TM, TN * TM, kFirst>();
-      __builtin_amdgcn_sched_barrier(0);
+      // second half; stage t + ST starts into stage t's slot (past the last stage the fragments read are
+      // a repeat's, not used)
+      half(f1, f0, half_of(next, 0), t + ST, slot, 0, kFirst);
       before = slot;
       slot = next;
     }
@@ -785,7 +773,7 @@ hipError_t launch_tile(const LinearArgs& a, hipStream_t stream) {
 struct TileShape {
   int bm, bn, waves, slots;
 };
-constexpr TileShape kTiles[15] = {{256, 256, 8, 0}, {128, 256, 8, 3}, {256, 128, 8, 3}, {160, 160, 4, 3}, {128, 160, 4, 4},
+constexpr TileShape kTiles[15] = {{256, 256, 8, 0}, {128, 256, 8, 3}, {256, 128, 8, 3}, {160, 160, 4, 4}, {128, 160, 4, 4},
                                   {192, 128, 4, 4}, {128, 128, 4, 4}, {128, 128, 4, 2}, {64, 256, 8, 4},  {64, 128, 8, 6},
                                   {64, 64, 4, 4},   {32, 128, 4, 6},  {32, 64, 4, 8},   {32, 32, 2, 8},   {16, 16, 1, 12}};
 constexpr int kFew8 = 15, kFew16 = 16;  // k_linear_few for up to 8 and 16 tokens
@@ -798,7 +786,7 @@ hipError_t launch_shape(int tile, const LinearArgs& a, hipStream_t stream) {
     case 0: return launch_big<GLU>(a, stream);
     case 1: return launch_tile<128, 256, 4, 2, 3, GLU>(a, stream);
     case 2: return launch_tile<256, 128, 4, 2, 3, GLU>(a, stream);
-    case 3: return launch_tile<160, 160, 2, 2, 3, GLU>(a, stream);
+    case 3: return launch_tile<160, 160, 2, 2, 4, GLU>(a, stream);
     case 4: return launch_tile<128, 160, 2, 2, 4, GLU>(a, stream);
     case 5: return launch_tile<192, 128, 2, 2, 4, GLU>(a, stream);
     case 6: return launch_tile<128, 128, 2, 2, 4, GLU>(a, stream);
@@ -815,9 +803,9 @@ hipError_t launch_shape(int tile, const LinearArgs& a, hipStream_t stream) {
 }
 
 // Microseconds that a tile shape and a split take, as a model of what bounds them: per stage and
-// compute unit the copies into its LDS (63 KB per us); per round of workgroups a prologue and an
-// epilogue; over all, the bytes at 4.85 TB/s; the parts written and read at 7.1 TB/s and a second
-// launch.  Fitted to 90 shapes, 10..8192 tokens, K 128..10240, N 72..25600, with every tile and split timed:
+// compute unit the copies into its LDS (66 KB per us) or the MFMAs (8 TFLOP/s); per round of workgroups a
+// prologue and an epilogue; over all, the bytes (7.3 TB/s, of which 43% of the shorter of the two times
+// does not overlap); the parts written and read at 5.5 TB/s and a second launch.  Fitted to 90 shapes, 10..8192 tokens, K 128..10240, N 72..25600, with every tile and split timed:
 // the choice takes 1.7% longer than the best one on average and 20% at worst (a first rule, by token
 // count alone, 60% on average).
 double model_us(const TileShape& t, int parts, int64_t M, int K, int64_t rows, int64_t N, int cus) {
@@ -831,12 +819,13 @@ double model_us(const TileShape& t, int parts, int64_t M, int K, int64_t rows, i
   n = n < fit ? n : fit;
   double rounds = work / (cus * n);
   rounds = rounds < 4 ? ceil(rounds) : rounds + 0.5;
-  double stage = n * (t.bm + t.bn) * kRowB / 1024 / 63.0;
-  stage = stage > 0.13 ? stage : 0.13;
-  const double tile_us = 1.7 + rounds * (stages * stage + 2.1 + t.bm * t.bn * 1.55e-4);
-  const double mem_us = 1.7 + 2.0 * (double(M) * K + double(rows) * K + double(M) * N) / 4.85e6;
-  double us = tile_us > mem_us ? tile_us + 0.23 * mem_us : mem_us + 0.23 * tile_us;
-  if (parts > 1) us += 2.5 + parts * tiles * t.bm * t.bn * 8 / 7.1e6;
+  const double copies = n * (t.bm + t.bn) * kRowB / 1024 / 66.0, mfma = n * t.bm * t.bn * 128 / 8.0e6;
+  double stage = copies > mfma ? copies : mfma;
+  stage = stage > 0.1 ? stage : 0.1;
+  const double tile_us = 0.9 + rounds * (stages * stage + 2.9 + t.bm * t.bn * 1.24e-4);
+  const double mem_us = 0.9 + 2.0 * (double(M) * K + double(rows) * K + double(M) * N) / 7.3e6;
+  double us = tile_us > mem_us ? tile_us + 0.43 * mem_us : mem_us + 0.43 * tile_us;
+  if (parts > 1) us += 2.2 + parts * tiles * t.bm * t.bn * 8 / 5.5e6;
   return us;
 }
 

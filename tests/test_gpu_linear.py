@@ -32,13 +32,13 @@ SIZES = [(1, 64, 16), (1, 8, 1), (1, 5120, 5120), (2, 72, 33), (5, 1000, 257), (
 TILES = [(2067, 256, 4991), (1803, 832, 3400), (822, 4912, 3006), (512, 4560, 5198), (1537, 312, 3597), (136, 5144, 3845),
          (1678, 120, 2371), (1887, 5352, 260), (822, 280, 5993), (161, 3840, 5879), (385, 64, 4707), (65, 4816, 5955),
          (1043, 64, 3868), (1594, 64, 2501), (163, 3536, 5707), (229, 416, 4108), (35, 4008, 5463), (202, 64, 4108),
-         (68, 3168, 2882), (2048, 4096, 4096), (1000, 10240, 5120), (681, 3744, 36), (166, 2936, 5874)]
+         (68, 3168, 2882), (2048, 4096, 4096), (1000, 10240, 5120), (681, 3744, 36), (166, 2936, 5874), (267, 3480, 3808)]
 GATED_TILES = [(963, 248, 4830), (1561, 840, 1828), (331, 4936, 2714), (1163, 1032, 3214), (194, 4736, 4267), (391, 120, 4618),
                (146, 4336, 1833), (323, 280, 5664), (66, 4072, 5545), (925, 304, 3182), (173, 4016, 2770), (67, 4688, 2727),
                (385, 64, 4707), (258, 64, 5478), (180, 3296, 2738), (33, 2936, 4279), (71, 64, 4218), (73, 3392, 1381),
                (691, 3888, 17), (301, 5120, 10240), (936, 240, 5235), (484, 832, 5870),
                (222, 4424, 5244), (215, 4640, 5264), (136, 5136, 1831), (2038, 5552, 1544),
-               (69, 4152, 2767), (162, 2832, 2780), (1369, 3008, 17), (17, 2232, 260)]
+               (69, 4152, 2767), (162, 2832, 2780), (1369, 3008, 17), (17, 2232, 260), (263, 3416, 1890)]
 
 
 @pytest.mark.parametrize("M,K,N,glus", [(*s, (False, True)) for s in SIZES] + [(*s, (False,)) for s in TILES] +
