@@ -1,18 +1,27 @@
 // Matrix product with bias, activation (plain or gated) and residual: out = residual + act(x w^T + bias).
 //
-// A workgroup computes a tile of BM tokens x BN weight rows over all of K, in stages of 64 features.
-// A stage holds BN weight rows, then BM token rows, of 128 bytes each in LDS, 16-byte chunk c of row r
-// at position c ^ (r & 7) (conflict-free for the fragment reads); ST slots form a ring that global ->
-// LDS copies of 16 bytes per lane fill ST - 1 stages ahead, one workgroup barrier per stage.  The
-// waves share the tile as WM x WN parts; a wave multiplies its part as blocks of
-// v_mfma_f32_16x16x32_bf16 (weight rows as A, tokens as B: a lane then holds 4 consecutive output
-// features of one token).
+// Three kernels, by a modelled choice (choose() below):
+//  k_linear      a tile of BM tokens x BN weight rows by 1..8 waves, for most shapes;
+//  k_linear_big  256 x 256 by two groups of waves that take turns at the matrix units, for large ones;
+//  k_linear_few  16 x 16 with K shared by the waves of a workgroup, for up to 16 tokens.
+// K is taken in stages of 64 features, copied global -> LDS (16 bytes per lane, rows of 128 bytes) into a
+// ring of slots; a wave multiplies blocks of v_mfma_f32_16x16x32_bf16 with weight rows as A and tokens as
+// B, so that a lane holds 4 consecutive weight rows of one token.  Where there are few tiles K is split
+// over workgroups: they leave fp32 blocks in the caller's workspace and k_linear_join adds them in order.
 //
 // Gated: the weight has the N gate rows, then the N value rows.  A block of 16 rows takes 8 rows of the
 // gate and the same 8 of the value, so both factors of an output meet in one wave's epilogue.
 //
-// Features past K (K is a multiple of 8) are copied from 16 zero bytes; weight rows past N and tokens
-// past M repeat the last one and are not stored.
+// Edges: weight rows past N and tokens past M repeat the last one and are not stored; the features past the
+// last whole stage (K is a multiple of 8) are read straight into fragments, zeros past K.
+//
+// What bounds it.  Up to 64 tokens, the weight's bytes: 1 token x 6144 x 25,600 takes 54 us (5.8 TB/s), 64
+// tokens 63 us.  That needs every column of tiles to start at another stage of K: rows are 2 K bytes apart,
+// so workgroups in step ask the same memory channel (64 tokens: 81 us without, 66 us with).  A few hundred
+// tokens: the copies, 12-16 TB/s out of the L2s and about 66 KB per us into a CU, hence the largest tile
+// that still fills the device (301 x 5120 x 20,480: 77 us with 160 x 160, 97 us with 128 x 128).  Thousands:
+// the matrix units at the clock that they leave (1.85 GHz; busy 68% of it): 8192 x 6144 x 25,600 1.84-1.91 ms,
+// 1.35-1.40 PFLOP/s.
 #include <math.h>
 
 #include "common.h"
@@ -335,8 +344,13 @@ __global__ __launch_bounds__(kWave) void k_linear_join(LinearArgs a) {
   epilogue<TN, 1, GLU>(a, acc, lds, m0, int(cb * kOutCols) + wn * TN * (GLU ? 8 : 16), lane);
 }
 
+// ---------------------------------------------------------------- tiles of BM x BN
+// The waves share the tile as WM x WN parts of TM x TN blocks.  A stage of the ring (ST slots) holds BN weight
+// rows, then BM token rows.  While a wave multiplies one half of a stage (32 features) it reads the next
+// half's fragments; one barrier per stage, between its halves, hands the slot on.  (The wait counts hold
+// only if nothing else is in flight: a spilled register would break them; none of these kernels has one.)
 template <int BM, int BN, int WM, int WN, int ST, bool GLU>
-__global__ __launch_bounds__(WM* WN* kWave, BM / WM * BN / WN > 8192 ? 1 : 2) void k_linear(LinearArgs a) {
+__global__ __launch_bounds__(WM* WN* kWave, 2) void k_linear(LinearArgs a) {
   constexpr int kWaves = WM * WN;
   constexpr int kRowsT = BM + BN;                 // rows of a stage: the weight's, then the tokens'
   constexpr int kSlot = kRowsT * kRowB;
@@ -355,7 +369,7 @@ __global__ __launch_bounds__(WM* WN* kWave, BM / WM * BN / WN > 8192 ? 1 : 2) vo
   const Share sh = share_of(a, tbs, cbs);
   const int64_t m0 = int64_t(sh.tb) * BM, n0 = int64_t(sh.cb) * kOutCols;
   const int S = sh.stages;
-
+  // the stages are taken from this one on, and round (see above: memory channels)
   const int turned = S > 0 ? int(sh.cb % uint32_t(S)) : 0;
 
   // lane l of copy q fills bytes 16 l of 1 KB: row 8 q + l / 8, position l % 8.  Its 8 rows start at
