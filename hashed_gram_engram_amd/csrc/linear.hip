@@ -20,8 +20,8 @@
 // so workgroups in step ask the same memory channel (64 tokens: 81 us without, 66 us with).  A few hundred
 // tokens: the copies, 12-16 TB/s out of the L2s and about 66 KB per us into a CU, hence the largest tile
 // that still fills the device (301 x 5120 x 20,480: 77 us with 160 x 160, 97 us with 128 x 128).  Thousands:
-// the matrix units at the clock that they leave (1.85 GHz; busy 68% of it): 8192 x 6144 x 25,600 1.84-1.91 ms,
-// 1.35-1.40 PFLOP/s.
+// the matrix units (busy 68% of the cycles, at 1.8-1.9 GHz): 8192 x 6144 x 25,600 without activation
+// 1.84-1.91 ms, 1.35-1.40 PFLOP/s; with GELU 1.93-2.0 ms.
 #include <math.h>
 
 #include "common.h"
