@@ -257,8 +257,8 @@ engram_status engram_hash_ids(const engram_hash_layout* layout, const uint32_t* 
  * A serving step of ragged requests: engram_batch_plan (where each request's tokens live),
  * engram_hash_ids_paged (their row ids), engram_forward, then the block around it:
  * engram_residual_norm (closes one block and opens the next) and engram_linear (a projection with
- * bias, activation and residual).  The conventions above hold; none of them needs a workspace,
- * none keeps state, and calls that write different buffers may overlap in time. */
+ * bias, activation and residual).  The conventions above hold; only engram_linear needs a workspace
+ * (for some shapes), none keeps state, and calls that write different buffers may overlap in time. */
 
 /* Storage of a residual stream (x, out of engram_residual_norm; residual, out of engram_linear). */
 typedef enum { ENGRAM_STREAM_BF16 = 0, ENGRAM_STREAM_FP32 = 1 } engram_stream_format;
