@@ -831,6 +831,8 @@ def engram_linear(layout: LinearLayout, x: torch.Tensor, w: torch.Tensor, bias: 
         if e.status != ENGRAM_E_WORKSPACE or workspace is not None:
             raise
         # the shape splits K (a call without a workspace is refused before anything is enqueued)
-        workspace = x.new_empty(engram_linear_workspace_bytes(layout, M), dtype=torch.uint8)
+        with torch.cuda.device(dev):
+            need = engram_linear_workspace_bytes(layout, M)
+        workspace = x.new_empty(need, dtype=torch.uint8)
         _launch("engram_linear", dev, _lib.engram_linear, *args, workspace.data_ptr(), workspace.numel())
     return out

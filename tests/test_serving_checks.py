@@ -194,3 +194,38 @@ def test_scalar_plan_by_hand():
     # one page too few: the last request is refused, its table untouched
     plan, t, f, errors = plan_ref(2, 2, 8, [2, -1, 3], [1, 1, 0], table, np.array([3, 5, 9, 9, 9, 9, 9, 9]), 1, 6)
     assert plan["status"] == [0, 0, 2] and plan["free_left"] == [1] and t[2].tolist() == [0, 0] and errors == 1
+
+
+def test_linear_sizes_its_workspace_on_the_tensors_device(monkeypatch):
+    """A call refused for want of a workspace asks for the size with the tensors' device current: the size
+    follows that device's compute units, not those of the device that happens to be current."""
+    current, asked, given = [0], [], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    def size(layout, M):
+        asked.append(current[0])
+        return 64
+
+    def launch(where, device, fn, *args):
+        given.append(args[-1])
+        if args[-1] == 0:
+            raise eg.EngramError(where, eg.ENGRAM_E_WORKSPACE)
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(eg, "engram_linear_workspace_bytes", size)
+    monkeypatch.setattr(eg, "_launch", launch)
+    monkeypatch.setattr(eg, "_rows", lambda name, t, lead, row, dtype, device: row[0])
+    monkeypatch.setattr(eg, "_tensor", lambda name, t, shape, dtype, device: t.data_ptr())
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 1)
+    x, w = torch.zeros(2, 8, dtype=torch.bfloat16), torch.zeros(4, 8, dtype=torch.bfloat16)
+    eg.engram_linear(eg.make_linear_layout(8, 4), x, w)
+    assert asked == [1] and given == [0, 64] and current == [0]
