@@ -363,6 +363,7 @@ typedef struct {
  *        not looked at; NULL = all open
  *   out  [B, T, hc, dim] in x's format; may be x
  *   h    [B, T, hc, dim] bf16; NULL without pre_norm
+ * Apart from out = x, out and h must not overlap an input or each other.
  * Per (token, stream s), fp32 throughout, rounded once on output:
  *   n = y * rsqrt(mean(y^2) + post_eps) * post_weight,  r = alpha * x + beta * gate * n (closed: x),
  *   out = r,  h = r * rsqrt(mean(r^2) + pre_eps) * pre_weight  (of r before its rounding). */
