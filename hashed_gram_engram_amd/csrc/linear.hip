@@ -53,14 +53,16 @@ __device__ __forceinline__ void activate8(float (&z)[8], int act) {
       const float q = 0.5f * p * __expf(-x * x);  // Phi(-|z|)
       z[e] *= z[e] > 0.0f ? 1.0f - q : q;
     }
-  } else if (act == 5) {
+  } else if (act == 3) {
+    // (1 + tanh v) / 2 = 1 / (1 + exp(-2 v)) with 2 v = 2 sqrt(2 / pi) (z + 0.044715 z^3)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] *= rcp(1.0f + __expf(-z[e] * (1.5957691216057308f + 0.071354816272f * z[e] * z[e])));
+  } else if (act == 4) {  // (tanh-GELU's expression with no cubic term would make 0 times an infinite z a NaN)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] *= rcp(1.0f + __expf(-z[e]));
+  } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) z[e] = rcp(1.0f + __expf(-z[e]));
-  } else {
-    // z / (1 + exp(-u)): u = z, or 2 sqrt(2 / pi) (z + 0.044715 z^3) since (1 + tanh v) / 2 = 1 / (1 + exp(-2 v))
-    const float c1 = act == 3 ? 1.5957691216057308f : 1.0f, c3 = act == 3 ? 0.071354816272f : 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) z[e] *= rcp(1.0f + __expf(-z[e] * (c1 + c3 * z[e] * z[e])));
   }
 }
 
