@@ -57,6 +57,14 @@ __device__ __forceinline__ float row_sum(float v, float* tmp) {
   return v;
 }
 
+// 1 / sqrt(m) of a mean square.  The hardware's root takes a denormal for 0 (rows below 1e-19 with an epsilon
+// of 0 came out infinite), so a small m is scaled by 2^60 first.
+__device__ __forceinline__ float rstd_of(float m) {
+  const bool small = m < 0x1p-100f;
+  const float r = __frsqrt_rn(small ? m * 0x1p60f : m);
+  return small ? r * 0x1p30f : r;
+}
+
 // T threads per row, NV vectors of 8 features per thread (dim <= T * NV * 8), FP32 streams or bf16.
 template <int T, int NV, bool FP32>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void k_residual_norm(NormArgs a) {
@@ -120,7 +128,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_residual_norm(NormArgs a)
       for (int e = 0; e < 8; ++e) q += y[e] * y[e];
     }
     q = row_sum<T>(q, tmp);
-    scale *= __frsqrt_rn(q / float(a.dim) + a.post_eps);
+    scale *= rstd_of(q / float(a.dim) + a.post_eps);
   }
   if (open) {
 #pragma unroll
@@ -168,7 +176,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_residual_norm(NormArgs a)
 #pragma unroll
       for (int e = 0; e < 8; ++e) q += r[k][e] * r[k][e];
     q = row_sum<T>(q, tmp);
-    const float rstd = __frsqrt_rn(q / float(a.dim) + a.pre_eps);
+    const float rstd = rstd_of(q / float(a.dim) + a.pre_eps);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int v = lane + k * T;
