@@ -1,6 +1,6 @@
 // Matrix product with bias, activation (plain or gated) and residual: out = residual + act(x w^T + bias).
 //
-// Three kernels, by a modelled choice (choose() below):
+// Three kernels, by a modelled choice (choose() in linear_choice.h):
 //  k_linear      a tile of BM tokens x BN weight rows by 1..8 waves, for most shapes;
 //  k_linear_big  256 x 256 by two groups of waves that take turns at the matrix units, for large ones;
 //  k_linear_few  16 x 16 with K shared by the waves of a workgroup, for up to 16 tokens.
@@ -22,9 +22,8 @@
 // that still fills the device (301 x 5120 x 20,480: 77 us with 160 x 160, 97 us with 128 x 128).  Thousands:
 // the matrix units (busy 68% of the cycles, at 1.8-1.9 GHz): 8192 x 6144 x 25,600 without activation
 // 1.84-1.91 ms, 1.35-1.40 PFLOP/s; with GELU 1.91-2.0 ms.
-#include <math.h>
-
 #include "common.h"
+#include "linear_choice.h"
 #include "serving.h"
 
 namespace engram {
@@ -239,9 +238,6 @@ __device__ __forceinline__ uint32_t xcd_tile(uint32_t b, uint32_t tiles) {
   const uint32_t q = tiles >> 3, rem = tiles & 7, x = b & 7;
   return x * q + (x < rem ? x : rem) + (b >> 3);
 }
-
-constexpr int kBK = 64;         // features of a stage
-constexpr int kRowB = kBK * 2;  // bytes of a row of a stage
 
 // 16-byte chunk c of row r of a stage lies at position c ^ swizzle(r): the 16 rows of a fragment read
 // cover all 64 banks once.
@@ -494,9 +490,7 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_linear(LinearArgs a) {
 // J + 1 is then there for its first reader (group 0, phase 4 J + 3).  Copies past the last stage
 // repeat it, so that the counts hold.  (The 64 copies of a stage take the CU's memory path about 1600
 // cycles, its 4 phases of MFMAs 2048: copies in one phase would make that phase three times as long.)
-constexpr int kBig = 256;
-constexpr int kOpB = kBig * kRowB;  // one operand of one stage
-constexpr int kBigLds = 5 * kOpB;   // weight slots 0..2, token slots 3, 4
+constexpr int kOpB = kBig * kRowB;  // one operand of one stage: weight slots 0..2, token slots 3, 4 of kBigLds
 typedef f32x4 BigAcc[8][4];
 
 struct BigPipe {
@@ -784,16 +778,7 @@ hipError_t launch_tile(const LinearArgs& a, hipStream_t stream) {
                       reinterpret_cast<const void*>(&k_linear_join<BM, BN, WM, WN, GLU>), WN * BM / 16, tiles, stream);
 }
 
-// ---------------------------------------------------------------- choice of tile and split
-// Tiles: tokens x weight rows, waves, ring slots (0: k_linear_big).
-struct TileShape {
-  int bm, bn, waves, slots;
-};
-constexpr TileShape kTiles[15] = {{256, 256, 8, 0}, {128, 256, 8, 3}, {256, 128, 8, 3}, {160, 160, 4, 4}, {128, 160, 4, 4},
-                                  {192, 128, 4, 4}, {128, 128, 4, 4}, {128, 128, 4, 2}, {64, 256, 8, 4},  {64, 128, 8, 6},
-                                  {64, 64, 4, 4},   {32, 128, 4, 6},  {32, 64, 4, 8},   {32, 32, 2, 8},   {16, 16, 1, 12}};
-constexpr int kFew8 = 15, kFew16 = 16;  // k_linear_few for up to 8 and 16 tokens
-
+// ---------------------------------------------------------------- launch of the chosen tile (linear_choice.h)
 template <bool GLU>
 hipError_t launch_shape(int tile, const LinearArgs& a, hipStream_t stream) {
   switch (tile) {
@@ -816,73 +801,6 @@ hipError_t launch_shape(int tile, const LinearArgs& a, hipStream_t stream) {
     case 14: return launch_tile<16, 16, 1, 1, 12, GLU>(a, stream);
   }
   return hipErrorInvalidValue;
-}
-
-// Microseconds that a tile shape and a split take, as a model of what bounds them: per stage and
-// compute unit the copies into its LDS (66 KB per us) or the MFMAs (8 TFLOP/s); per round of workgroups a
-// prologue and an epilogue; over all, the bytes (7.3 TB/s, of which 43% of the shorter of the two times
-// does not overlap); the parts written and read at 5.5 TB/s and a second launch.  Fitted to 90 shapes, 10..8192 tokens, K 128..10240, N 72..25600, with every tile and split timed:
-// the choice takes 1.7% longer than the best one on average and 20% at worst (a first rule, by token
-// count alone, 60% on average).
-double model_us(const TileShape& t, int parts, int64_t M, int K, int64_t rows, int64_t N, int cus) {
-  const double tiles = double((M + t.bm - 1) / t.bm) * double((rows + t.bn - 1) / t.bn);
-  const int lds = t.slots == 0 ? kBigLds : t.slots * (t.bm + t.bn) * kRowB;
-  int fit = 160 * 1024 / lds;  // workgroups of a compute unit
-  const int by_waves = t.waves >= 4 ? 8 / t.waves : 8;
-  fit = fit < by_waves ? fit : by_waves;
-  const double work = tiles * parts, stages = K / 64.0 / parts;
-  double n = ceil(work / cus);
-  n = n < fit ? n : fit;
-  double rounds = work / (cus * n);
-  rounds = rounds < 4 ? ceil(rounds) : rounds + 0.5;
-  const double copies = n * (t.bm + t.bn) * kRowB / 1024 / 66.0, mfma = n * t.bm * t.bn * 128 / 8.0e6;
-  double stage = copies > mfma ? copies : mfma;
-  stage = stage > 0.1 ? stage : 0.1;
-  const double tile_us = 0.9 + rounds * (stages * stage + 2.9 + t.bm * t.bn * 1.24e-4);
-  const double mem_us = 0.9 + 2.0 * (double(M) * K + double(rows) * K + double(M) * N) / 7.3e6;
-  double us = tile_us > mem_us ? tile_us + 0.43 * mem_us : mem_us + 0.43 * tile_us;
-  if (parts > 1) us += 2.2 + parts * tiles * t.bm * t.bn * 8 / 5.5e6;
-  return us;
-}
-
-constexpr int64_t kMostPartBytes = int64_t(512) << 20;
-
-// The tile, the parts and the bytes of their workspace.
-struct LinearChoice {
-  int tile = 0, parts = 1;
-  int64_t bytes = 0;
-};
-LinearChoice choose(int64_t M, int K, int N, bool glu, int cus) {
-  LinearChoice best;
-  const int64_t rows = glu ? 2 * int64_t(N) : N;
-  // Up to 16 tokens: the shared-K kernel (one token x 5120 x 5120: 11.0 us, the best tile and split of the
-  // others 12.8; x 4096 x 1024: 4.4 and 7.9; 16 tokens x 2048 x 8192: 7.7 and 8.3).  From 9 tokens on only
-  // while its tiles are at most two to a compute unit: it reads x once per 16 rows (16 tokens x 6144 x
-  // 25,600: 65.7 us, and 55.4 with tiles of 128 rows).
-  const int64_t few = (rows + 15) / 16;
-  if (M <= 8 || (M <= 16 && few <= 2 * cus)) {
-    best.tile = M <= 8 ? kFew8 : kFew16;
-    return best;
-  }
-  double least = 1e30;
-  for (int i = 0; i < 15; ++i) {
-    const TileShape& t = kTiles[i];
-    const int64_t tiles = (M + t.bm - 1) / t.bm * ((rows + t.bn - 1) / t.bn);
-    if (tiles > (int64_t(1) << 24)) continue;  // far below what a launch takes
-    for (int parts : {1, 2, 3, 4, 6, 8}) {
-      const int64_t bytes = parts > 1 ? tiles * parts * t.bm * t.bn * 4 : 0;
-      // split only while the parts fill the device at most about three times and are not too short
-      if (parts > 1 && (tiles * parts > 3 * cus || K / 64 / parts < 4 || bytes > kMostPartBytes)) break;
-      const double us = model_us(t, parts, M, K, rows, N, cus);
-      if (us < least) {
-        least = us;
-        best.tile = i;
-        best.parts = parts;
-        best.bytes = bytes;
-      }
-    }
-  }
-  return best;
 }
 
 }  // namespace
