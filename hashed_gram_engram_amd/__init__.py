@@ -103,6 +103,8 @@ _lib.engram_residual_norm.argtypes = [ctypes.POINTER(NormLayout), _vp, _vp, _i64
 _lib.engram_linear.argtypes = [ctypes.POINTER(LinearLayout), _vp, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _sz, _vp]
 _lib.engram_linear_workspace_bytes.argtypes = [ctypes.POINTER(LinearLayout), _i64]
 _lib.engram_linear_workspace_bytes.restype = _sz
+_lib.engram_linear_workspace_bytes_up_to.argtypes = [ctypes.POINTER(LinearLayout), _i64]
+_lib.engram_linear_workspace_bytes_up_to.restype = _sz
 _lib.engram_page_layout_check.argtypes = [ctypes.POINTER(PageLayout)]
 _lib.engram_norm_layout_check.argtypes = [ctypes.POINTER(NormLayout)]
 _lib.engram_linear_layout_check.argtypes = [ctypes.POINTER(LinearLayout)]
@@ -119,7 +121,8 @@ EXPORTED = ["engram_layout_check", "engram_param_counts", "engram_forward_worksp
             "engram_gather_dequant", "engram_kv_proj", "engram_gate_apply", "engram_forward",
             "engram_hash_ids", "engram_status_str", "engram_forward_check", "engram_set_spin_budget",
             "engram_forward_noalloc", "engram_batch_plan", "engram_hash_ids_paged", "engram_residual_norm",
-            "engram_linear", "engram_linear_workspace_bytes", "engram_page_layout_check", "engram_norm_layout_check", "engram_linear_layout_check"]
+            "engram_linear", "engram_linear_workspace_bytes", "engram_linear_workspace_bytes_up_to",
+            "engram_page_layout_check", "engram_norm_layout_check", "engram_linear_layout_check"]
 
 
 SCALE_FP32, SCALE_E8M0 = 0, 1  # engram_scale_format
@@ -789,7 +792,13 @@ def make_linear_layout(in_features: int, out_features: int, activation: int = AC
 
 
 def engram_linear_workspace_bytes(layout: LinearLayout, M: int) -> int:
+    """For exactly M rows on the current device; fewer rows may need more."""
     return int(_lib.engram_linear_workspace_bytes(ctypes.byref(layout), M))
+
+
+def engram_linear_workspace_bytes_up_to(layout: LinearLayout, M: int) -> int:
+    """Enough for every call of 1 .. M rows on the current device: one buffer for steps of different lengths."""
+    return int(_lib.engram_linear_workspace_bytes_up_to(ctypes.byref(layout), M))
 
 
 def engram_linear(layout: LinearLayout, x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -797,9 +806,10 @@ def engram_linear(layout: LinearLayout, x: torch.Tensor, w: torch.Tensor, bias: 
                   workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """out [..., N] = residual + act(x [..., K] @ w^T + bias), or with the layout's glu
     residual + act(gate) * value from a weight of 2 N rows (engram_linear in include/engram.h).  x,
-    residual and out may be slices of wider rows; out may be the residual.  Without a workspace
-    (engram_linear_workspace_bytes) the call takes one from torch's allocator where it needs one: calls
-    on other streams, and captured graphs, then have their own."""
+    residual and out may be slices of wider rows; out may be the residual.  Without a workspace the call
+    takes one from torch's allocator where it needs one: calls on other streams, and captured graphs, then
+    have their own.  A workspace that is given must hold engram_linear_workspace_bytes of this many rows; one
+    kept for steps of different lengths is sized by engram_linear_workspace_bytes_up_to."""
     K, N, dev, bf16 = layout.in_features, layout.out_features, x.get_device(), torch.bfloat16
     if x.dim() < 1:
         raise ValueError("x has no dimensions")

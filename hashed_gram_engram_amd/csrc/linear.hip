@@ -809,6 +809,10 @@ int64_t linear_workspace_bytes(int64_t M, int K, int N, bool glu, int cus) {
   return M > 0 ? choose(M, K, N, glu, cus).bytes : 0;
 }
 
+int64_t linear_workspace_bytes_up_to(int64_t M, int K, int N, bool glu, int cus) {
+  return most_bytes_up_to(M, K, N, glu, cus);
+}
+
 hipError_t launch_linear(const LinearArgs& a, int cus, hipStream_t stream) {
   if (a.M <= 0) return hipSuccess;
   const LinearChoice c = choose(a.M, a.K, a.N, a.glu != 0, cus);

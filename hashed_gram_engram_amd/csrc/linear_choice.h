@@ -89,4 +89,23 @@ inline LinearChoice choose(int64_t M, int K, int N, bool glu, int cus) {
   return best;
 }
 
+// The most workspace bytes of any call of at most M rows.  (Fewer rows may need more than M: they have fewer tiles
+// and are split.)  Row counts with more tiles than the split's limit above need none, so at most 384 x 256 are
+// looked at, 0.5 us each.
+inline int64_t most_bytes_up_to(int64_t M, int K, int N, bool glu, int cus) {
+  const int64_t rows = glu ? 2 * int64_t(N) : N;
+  int64_t last = 0, most = 0;
+  if (K / 64 >= 8)
+    for (const TileShape& t : kTiles) {
+      const int64_t split = 3 * cus / 2 / ((rows + t.bn - 1) / t.bn) * t.bm;
+      last = split > last ? split : last;
+    }
+  last = M < last ? M : last;
+  for (int64_t m = 1; m <= last; ++m) {
+    const int64_t bytes = choose(m, K, N, glu, cus).bytes;
+    most = bytes > most ? bytes : most;
+  }
+  return most;
+}
+
 }  // namespace engram

@@ -82,6 +82,7 @@ struct LinearArgs {
 // Bytes of `partials` (16-byte aligned) that launch_linear needs on a device of `cus` compute units; 0
 // where it does not split K.
 int64_t linear_workspace_bytes(int64_t M, int K, int N, bool glu, int cus);
+int64_t linear_workspace_bytes_up_to(int64_t M, int K, int N, bool glu, int cus);  // the most for 1 .. M rows
 hipError_t launch_linear(const LinearArgs& a, int cus, hipStream_t stream);  // (sets a.parts itself)
 
 }  // namespace engram

@@ -212,6 +212,13 @@ size_t engram_linear_workspace_bytes(const engram_linear_layout* l, int64_t M) {
   return size_t(linear_workspace_bytes(M, l->in_features, l->out_features, l->glu != 0, cus));
 }
 
+size_t engram_linear_workspace_bytes_up_to(const engram_linear_layout* l, int64_t M) {
+  if (engram_linear_layout_check(l) != ENGRAM_OK || M <= 0 || M > 0x7FFFFFFF) return 0;
+  DeviceInfo di;
+  const int cus = device_info(&di) == ENGRAM_OK ? di.cus : 256;
+  return size_t(linear_workspace_bytes_up_to(M, l->in_features, l->out_features, l->glu != 0, cus));
+}
+
 engram_status engram_linear(const engram_linear_layout* l, const uint16_t* x, int64_t x_stride, const uint16_t* w,
                             const float* bias, const void* residual, int64_t residual_stride, int64_t M, void* out,
                             int64_t out_stride, void* workspace, size_t workspace_bytes, engram_stream_t stream) {

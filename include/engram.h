@@ -412,6 +412,11 @@ engram_status engram_linear(const engram_linear_layout* layout, const uint16_t* 
  * graphs) must use different workspaces. */
 size_t engram_linear_workspace_bytes(const engram_linear_layout* layout, int64_t M);
 
+/* Bytes that are enough for every call of 1 .. M rows: the size of one buffer for steps of different lengths.
+ * (The size above is for exactly M rows and does not grow with M: 5120 -> 5120 takes 3.9 MB for 64 rows, 21 MB for
+ * 512 and none for 8192, and a call whose workspace is too small is refused.)  Host work of up to some 50 ms. */
+size_t engram_linear_workspace_bytes_up_to(const engram_linear_layout* layout, int64_t M);
+
 /* Host-only checks of the layouts above; no device work. */
 engram_status engram_page_layout_check(const engram_page_layout* layout);
 engram_status engram_norm_layout_check(const engram_norm_layout* layout);
