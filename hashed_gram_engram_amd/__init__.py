@@ -573,6 +573,8 @@ ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU, ACT_SIGMOID = range(6)  #
 
 # the HIP stream handle of a device's current stream (torch.cuda.current_stream, without the object)
 _raw_stream = torch._C._cuda_getCurrentRawStream
+# the current device (torch.cuda.current_device, without its check that the GPU is initialised: tensors on one exist)
+_current_device = torch._C._cuda_getDevice
 
 
 def _launch(where: str, device: int, fn, *args) -> None:
@@ -580,7 +582,7 @@ def _launch(where: str, device: int, fn, *args) -> None:
     device current for the call.  device: the tensors' index, -1 for host memory."""
     if device < 0:
         raise ValueError("tensors must be on a GPU, got cpu")
-    if device == torch.cuda.current_device():
+    if device == _current_device():
         st = fn(*args, _raw_stream(device))
     else:
         with torch.cuda.device(device):
@@ -629,6 +631,11 @@ def _rows(name: str, t: torch.Tensor, lead: tuple, row: tuple, dtype, device: in
             raise ValueError(f"{name}: the rows must be evenly spaced")
         want *= lead[d]
     return size if stride is None else stride
+
+
+def _refuse_grad(where: str, **tensors) -> None:
+    name = next(k for k, t in tensors.items() if t is not None and t.requires_grad)
+    raise ValueError(f"{name} requires grad, and {where} has no backward pass: call it under torch.no_grad()")
 
 
 def _counter(err_count: Optional[torch.Tensor], device: int):
@@ -739,7 +746,12 @@ def engram_residual_norm(layout: NormLayout, x: torch.Tensor, y: Optional[torch.
     """Closes a block and opens the next (engram_residual_norm in include/engram.h): returns
     (out, h) with out = alpha * x + beta * gate * norm(y) and h = norm(out).  x [B, T, hc, dim]
     contiguous; y and a gate per feature [B, T, y_streams, dim] may be slices of wider rows; out may
-    be x.  Without y, h = norm(x) and out is x; without pre_norm, h is None."""
+    be x.  Without y, h = norm(x) and out is x; without pre_norm, h is None.  Forward only: with autograd on, a
+    tensor that requires grad is refused."""
+    if (x.requires_grad or (y is not None and y.requires_grad) or (gate is not None and gate.requires_grad) or
+            (post_weight is not None and post_weight.requires_grad) or (pre_weight is not None and pre_weight.requires_grad) or
+            (out is not None and out.requires_grad) or (h is not None and h.requires_grad)) and torch.is_grad_enabled():
+        _refuse_grad("engram_residual_norm", x=x, y=y, gate=gate, post_weight=post_weight, pre_weight=pre_weight, out=out, h=h)
     if x.dim() != 4:
         raise ValueError(f"x has shape {tuple(x.shape)}, expected [B, T, hc, dim]")
     B, T, hc, dim = x.shape
@@ -809,7 +821,11 @@ def engram_linear(layout: LinearLayout, x: torch.Tensor, w: torch.Tensor, bias: 
     residual and out may be slices of wider rows; out may be the residual.  Without a workspace the call
     takes one from torch's allocator where it needs one: calls on other streams, and captured graphs, then
     have their own.  A workspace that is given must hold engram_linear_workspace_bytes of this many rows; one
-    kept for steps of different lengths is sized by engram_linear_workspace_bytes_up_to."""
+    kept for steps of different lengths is sized by engram_linear_workspace_bytes_up_to.
+    Forward only: with autograd on, a tensor that requires grad is refused."""
+    if (x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad) or
+            (residual is not None and residual.requires_grad) or (out is not None and out.requires_grad)) and torch.is_grad_enabled():
+        _refuse_grad("engram_linear", x=x, w=w, bias=bias, residual=residual, out=out)
     K, N, dev, bf16 = layout.in_features, layout.out_features, x.get_device(), torch.bfloat16
     if x.dim() < 1:
         raise ValueError("x has no dimensions")
