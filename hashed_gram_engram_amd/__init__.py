@@ -571,6 +571,8 @@ GATE_NONE, GATE_TOKEN, GATE_FEATURE = 0, 1, 2      # engram_gate_kind
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU, ACT_SIGMOID = range(6)  # engram_activation
 
 
+_U32 = getattr(torch, "uint32", torch.int32)  # (torch versions without unsigned types hold such maps as int32)
+
 # the HIP stream handle of a device's current stream (torch.cuda.current_stream, without the object)
 _raw_stream = torch._C._cuda_getCurrentRawStream
 # the current device (torch.cuda.current_device, without its check that the GPU is initialised: tensors on one exist)
@@ -710,7 +712,7 @@ def engram_hash_ids_paged(layout: HashLayout, pages: PageLayout, token_map: torc
     (R, n), i64, i32, dev = plan._sizes, torch.int64, torch.int32, input_ids.get_device()
     at = _plan_on(plan, dev)._out
     layers, heads, orders = layout.n_layers, layout.n_heads, layout.max_ngram - 1
-    tmap = _tensor("token_map", token_map, (layout.vocab,), i32 if token_map.dtype is i32 else torch.uint32, dev)
+    tmap = _tensor("token_map", token_map, (layout.vocab,), i32 if token_map.dtype is i32 else _U32, dev)
     mult = _tensor("multipliers", multipliers, (layers, orders + 1), i64, dev)
     prime = _tensor("primes", primes, (layers, orders, heads), i64, dev)
     offs = _tensor("offsets", offsets, (layers, orders * heads), i64, dev)
