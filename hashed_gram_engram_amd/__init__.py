@@ -563,7 +563,8 @@ def _check_forward_args(layout: EngramLayout, x, hash_ids, token_mask, table, sc
 # ----------------------------------------------------------------------------------------
 # The serving operators around the forward: a plan of ragged requests, their row ids, the norms
 # around a block, a projection with its epilogue.  They launch on the current stream of their
-# tensors' device.
+# tensors' device.  As in the forward, a bf16 tensor may be given as its int16 view; bf16 outputs that
+# a call makes then have x's type.
 # ----------------------------------------------------------------------------------------
 
 STREAM_BF16, STREAM_FP32 = 0, 1                    # engram_stream_format
@@ -593,11 +594,17 @@ def _launch(where: str, device: int, fn, *args) -> None:
         raise EngramError(where, st)
 
 
+def _type(name: str, t: torch.Tensor, dtype) -> None:
+    if t.dtype not in (_BF16 if dtype is torch.bfloat16 else (dtype,)):
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+
+
 def _tensor(name: str, t: torch.Tensor, shape: tuple, dtype, device: int) -> int:
-    """The address of a contiguous tensor of this shape and dtype on the device."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
-        if t.dtype != dtype:
-            raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    """The address of a contiguous tensor of this shape and dtype (for bf16 also its int16 view) on the
+    device."""
+    if t.dtype is not dtype:
+        _type(name, t, dtype)
+    if t.shape != shape or not t.is_contiguous() or t.get_device() != device:
         if t.shape != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if not t.is_contiguous():
@@ -610,7 +617,7 @@ def _rows(name: str, t: torch.Tensor, lead: tuple, row: tuple, dtype, device: in
     """The stride in elements between the rows of a tensor [*lead, *row] of this dtype whose rows are
     contiguous and evenly spaced."""
     if t.dtype is not dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+        _type(name, t, dtype)
     if t.shape != lead + row:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {lead + row}")
     if t.get_device() != device:
@@ -785,7 +792,7 @@ def engram_residual_norm(layout: NormLayout, x: torch.Tensor, y: Optional[torch.
         raise ValueError("gate and out need y")
     if layout.pre_norm:
         if h is None:
-            h = torch.empty_like(x, dtype=bf16)
+            h = torch.empty_like(x, dtype=x.dtype if stream is bf16 else bf16)
             hp = h.data_ptr()
         else:
             hp = _tensor("h", h, full, bf16, dev)
@@ -843,7 +850,7 @@ def engram_linear(layout: LinearLayout, x: torch.Tensor, w: torch.Tensor, bias: 
         r_stride = _rows("residual", residual, lead, (N,), stream, dev)
         rp = residual.data_ptr()
     if out is None:
-        out, o_stride = x.new_empty((*lead, N), dtype=stream), N
+        out, o_stride = x.new_empty((*lead, N), dtype=x.dtype if stream is bf16 else stream), N
     else:
         o_stride = _rows("out", out, lead, (N,), stream, dev)
     ws, ws_bytes = None, 0

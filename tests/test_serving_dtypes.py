@@ -23,3 +23,29 @@ def test_token_maps_without_unsigned_types(monkeypatch):
         hash_call(torch.zeros(50, dtype=I64))
     with pytest.raises(ValueError, match="must be on a GPU"):
         hash_call(torch.zeros(50, dtype=I32))
+
+
+def test_int16_views_of_bf16_are_taken():
+    bf, i16 = torch.bfloat16, torch.int16
+    lin = dict(x=torch.zeros((3, 64), dtype=bf), w=torch.zeros((40, 64), dtype=bf), residual=torch.zeros((3, 40), dtype=bf),
+               out=torch.zeros((3, 80), dtype=bf)[:, :40])
+    four = torch.zeros((1, 3, 2, 64), dtype=bf)
+    norm = dict(x=four, y=four, gate=four, out=four, h=four)
+    cases = ((eg.engram_linear, eg.make_linear_layout(64, 40), lin),
+             (eg.engram_residual_norm, eg.make_norm_layout(2, 64, gate=eg.GATE_FEATURE), norm))
+    for call, layout, args in cases:
+        for some in [[k] for k in args] + [list(args)]:
+            with pytest.raises(ValueError, match="must be on a GPU"):
+                call(layout, **(args | {k: args[k].view(i16) for k in some}))
+            for wrong in (torch.float16, torch.int32, torch.uint8):
+                with pytest.raises(TypeError, match=f"{some[0]} has dtype"):
+                    call(layout, **(args | {some[0]: args[some[0]].to(wrong)}))
+
+
+def test_int16_is_not_taken_for_other_types():
+    x, w = torch.zeros((3, 64), dtype=torch.bfloat16), torch.zeros((40, 64), dtype=torch.bfloat16)
+    with pytest.raises(TypeError, match="bias has dtype"):
+        eg.engram_linear(eg.make_linear_layout(64, 40), x, w, bias=torch.zeros(40, dtype=torch.int16))
+    with pytest.raises(TypeError, match="residual has dtype"):
+        eg.engram_linear(eg.make_linear_layout(64, 40, stream_format=eg.STREAM_FP32), x, w,
+                         residual=torch.zeros((3, 40), dtype=torch.int16))
