@@ -21,7 +21,8 @@
 // tokens: the copies, 12-16 TB/s out of the L2s and about 66 KB per us into a CU, hence the largest tile
 // that still fills the device (301 x 5120 x 20,480: 77 us with 160 x 160, 97 us with 128 x 128).  Thousands:
 // the matrix units (busy 68% of the cycles, at 1.8-1.9 GHz): 8192 x 6144 x 25,600 without activation
-// 1.84-1.91 ms, 1.35-1.40 PFLOP/s; with GELU 1.91-2.0 ms.
+// 1.82-1.91 ms, 1.35-1.42 PFLOP/s; with GELU 1.86-2.0 ms.  Short K: the first copies and the epilogue of a tile, which
+// overlap nothing where one workgroup fills a CU (6192 x 616 x 23,984: 277 us; its output alone takes 62 us).
 #include "common.h"
 #include "linear_choice.h"
 #include "serving.h"

@@ -22,12 +22,14 @@ constexpr TileShape kTiles[15] = {{256, 256, 8, 0}, {128, 256, 8, 3}, {256, 128,
                                   {64, 64, 4, 4},   {32, 128, 4, 6},  {32, 64, 4, 8},   {32, 32, 2, 8},   {16, 16, 1, 12}};
 constexpr int kFew8 = 15, kFew16 = 16;  // k_linear_few for up to 8 and 16 tokens
 
-// Microseconds that a tile shape and a split take, as a model of what bounds them: per stage and
-// compute unit the copies into its LDS (66 KB per us) or the MFMAs (8 TFLOP/s); per round of workgroups a
-// prologue and an epilogue; over all, the bytes (7.3 TB/s, of which 43% of the shorter of the two times
-// does not overlap); the parts written and read at 5.5 TB/s and a second launch.  Fitted to 90 shapes, 10..8192 tokens, K 128..10240, N 72..25600, with every tile and split timed:
-// the choice takes 1.7% longer than the best one on average and 20% at worst (a first rule, by token
-// count alone, 60% on average).
+// Microseconds that a tile shape and a split take, as a model: per stage and compute unit the copies into its
+// LDS (66 KB per us) or the MFMAs (8 TFLOP/s); per round of workgroups a prologue and an epilogue; over all, the
+// bytes (at 7.3 TB/s, of which 43% of the shorter of the two times does not overlap); the parts written and read at
+// 5.5 TB/s and a second launch.  The rates are fitted numbers, not the card's (a copy reaches 4.8 TB/s): fitted to
+// 90 plain shapes, 10..8192 tokens, K 128..10240, N 72..25600, without the tiles of fewer than 64 tokens where there
+// are more than 64.  Timed since with every tile and split, on those and 40 gated shapes: the choice takes 1.8% longer
+// than the best one on average, more than 10% for 9 of the 130, and 23% at worst (2012 x 128 x 1032: 8.5 us, 6.9 with
+// 64 x 256).  Where the 256 x 256 tile runs it takes 0.91-1.23 times what the model says, 1.11 on average.
 inline double model_us(const TileShape& t, int parts, int64_t M, int K, int64_t rows, int64_t N, int cus) {
   const double tiles = double((M + t.bm - 1) / t.bm) * double((rows + t.bn - 1) / t.bn);
   const int lds = t.slots == 0 ? kBigLds : t.slots * (t.bm + t.bn) * kRowB;

@@ -1,5 +1,5 @@
 // C ABI of the serving operators: synchronous argument checks, then one launch on the caller's
-// stream.  No device memory is allocated here.
+// stream (two for a product that splits K).  No device memory is allocated here.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <string.h>
