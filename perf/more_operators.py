@@ -334,6 +334,11 @@ def work(case):
             "flops": pairs * H * 2 * (2 * c["hd"] + c["dr"])}
 
 
+def _power(e):
+    """2^e in 64 bits, exactly (pow may be off in its last bit, which moves ties)."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
 def _exact_rows(c, rows):
     """The latents that cache rows stand for, in 64 bits, from their bits."""
     dc = c["dc"]
@@ -341,8 +346,8 @@ def _exact_rows(c, rows):
         return rows.double()
     b = rows[:, :dc].long()
     e, m = (b >> 3) & 15, (b & 7).double()
-    mag = torch.where(e > 0, (8 + m) * 2.0 ** (e.double() - 10), m * 2.0 ** -9)
-    mag = torch.where(b >= 128, -mag, mag) * torch.repeat_interleave(2.0 ** (rows[:, dc: dc + dc // 32].double() - 127), 32, dim=1)
+    mag = torch.where(e > 0, (8 + m) * _power(e - 10), m * 2.0 ** -9)
+    mag = torch.where(b >= 128, -mag, mag) * torch.repeat_interleave(_power(rows[:, dc: dc + dc // 32].long() - 127), 32, dim=1)
     return torch.cat([mag, rows[:, dc + 16:].contiguous().view(torch.bfloat16).double()], 1)
 
 
@@ -361,12 +366,11 @@ def exact(case, seed):
                 c = x[:, : s["dc"]]
                 if s["fp8"]:
                     blocks = c.reshape(n, -1, 32)
-                    one = torch.ones((), dtype=torch.float64, device=DEV)
                     m, e = torch.frexp(blocks.abs().amax(-1, keepdim=True).clamp(min=1e-30) / 448)
-                    step = torch.ldexp(one, e - (m == 0.5).int())  # the power of two not below the quotient
+                    step = _power(e - (m == 0.5).int())  # the power of two not below the quotient
                     y = blocks / step
                     # e4m3: four significant bits, none below 2^-9
-                    ulp = torch.ldexp(one, torch.frexp(y.abs().clamp(min=2.0 ** -6))[1] - 4)
+                    ulp = _power(torch.frexp(y.abs().clamp(min=2.0 ** -6))[1] - 4)
                     c = (torch.round(y / ulp) * ulp * step).reshape(n, -1)
                 both = torch.cat([old, torch.cat([c, x[:, s["dc"]:]], 1)])
                 latents.append(both[:, : s["dc"]])
