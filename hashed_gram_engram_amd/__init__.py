@@ -65,6 +65,12 @@ class LinearLayout(ctypes.Structure):
                 ("glu", ctypes.c_int32), ("stream_format", ctypes.c_int32)]
 
 
+class LatentLayout(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int32), ("latent_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("cache_format", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
 class EngramError(RuntimeError):
     def __init__(self, where: str, status: int):
         msg = _lib.engram_status_str(status).decode()
@@ -108,6 +114,24 @@ _lib.engram_linear_workspace_bytes_up_to.restype = _sz
 _lib.engram_page_layout_check.argtypes = [ctypes.POINTER(PageLayout)]
 _lib.engram_norm_layout_check.argtypes = [ctypes.POINTER(NormLayout)]
 _lib.engram_linear_layout_check.argtypes = [ctypes.POINTER(LinearLayout)]
+_LL = ctypes.POINTER(LatentLayout)
+_lib.engram_latent_layout_check.argtypes = [_LL]
+_lib.engram_latent_row_bytes.argtypes = [_LL]
+_lib.engram_latent_write.argtypes = [_LL, ctypes.POINTER(PageLayout), _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp]
+_lib.engram_latent_read.argtypes = [_LL, ctypes.POINTER(PageLayout), _vp, _vp, _vp, _i64, _vp, _i64, _i32, _i64, _vp, _vp, _vp, _vp,
+                                    _vp]
+_lib.engram_latent_attention.argtypes = [_LL, ctypes.POINTER(PageLayout), _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _i32, _vp, _i64,
+                                         _vp, _vp, _sz, _vp, _vp]
+_lib.engram_latent_attention_expanded.argtypes = [_LL, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i32, _vp,
+                                                  _i64, _vp, _vp, _sz, _vp]
+_lib.engram_latent_attention_workspace_bytes.argtypes = [_LL]
+_lib.engram_latent_attention_expanded_workspace_bytes.argtypes = [_LL, _i64, _i64, _i64]
+for _f in (_lib.engram_latent_row_bytes, _lib.engram_latent_attention_workspace_bytes,
+           _lib.engram_latent_attention_expanded_workspace_bytes):
+    _f.restype = _sz
+for _f in (_lib.engram_latent_layout_check, _lib.engram_latent_write, _lib.engram_latent_read, _lib.engram_latent_attention,
+           _lib.engram_latent_attention_expanded):
+    _f.restype = ctypes.c_int
 for _f in (_lib.engram_batch_plan, _lib.engram_hash_ids_paged, _lib.engram_residual_norm, _lib.engram_linear,
            _lib.engram_page_layout_check, _lib.engram_norm_layout_check, _lib.engram_linear_layout_check):
     _f.restype = ctypes.c_int
@@ -122,7 +146,10 @@ EXPORTED = ["engram_layout_check", "engram_param_counts", "engram_forward_worksp
             "engram_hash_ids", "engram_status_str", "engram_forward_check", "engram_set_spin_budget",
             "engram_forward_noalloc", "engram_batch_plan", "engram_hash_ids_paged", "engram_residual_norm",
             "engram_linear", "engram_linear_workspace_bytes", "engram_linear_workspace_bytes_up_to",
-            "engram_page_layout_check", "engram_norm_layout_check", "engram_linear_layout_check"]
+            "engram_page_layout_check", "engram_norm_layout_check", "engram_linear_layout_check",
+            "engram_latent_layout_check", "engram_latent_row_bytes", "engram_latent_write", "engram_latent_read",
+            "engram_latent_attention", "engram_latent_attention_workspace_bytes", "engram_latent_attention_expanded",
+            "engram_latent_attention_expanded_workspace_bytes"]
 
 
 SCALE_FP32, SCALE_E8M0 = 0, 1  # engram_scale_format
@@ -870,4 +897,186 @@ def engram_linear(layout: LinearLayout, x: torch.Tensor, w: torch.Tensor, bias: 
             need = engram_linear_workspace_bytes(layout, M)
         workspace = x.new_empty(need, dtype=torch.uint8)
         _launch("engram_linear", dev, _lib.engram_linear, *args, workspace.data_ptr(), workspace.numel())
+    return out
+
+
+# ----------------------------------------------------------------------------------------
+# The latent cache and the attention that reads it (include/engram.h, "The latent cache").  The plan's
+# fields say where the step's tokens are.  Forward only: with autograd on, tensors that require grad are
+# refused.
+# ----------------------------------------------------------------------------------------
+
+CACHE_BF16, CACHE_MXFP8 = 0, 1  # engram_cache_format
+
+
+def make_latent_layout(heads: int, latent_dim: int, rope_dim: int, head_dim: int = 128, scale: Optional[float] = None,
+                       window: int = 0, cache_format: int = CACHE_BF16) -> LatentLayout:
+    """Layout of the latent operators; scale: of the scores, (head_dim + rope_dim) ** -0.5 by default."""
+    if scale is None:
+        scale = (head_dim + rope_dim) ** -0.5
+    return LatentLayout(heads, latent_dim, rope_dim, head_dim, cache_format, window, scale)
+
+
+def engram_latent_layout_check(layout: LatentLayout) -> int:
+    return _lib.engram_latent_layout_check(ctypes.byref(layout))
+
+
+def engram_latent_row_bytes(layout: LatentLayout) -> int:
+    """Bytes of a cache row; 0 for a layout that engram_latent_layout_check refuses."""
+    return int(_lib.engram_latent_row_bytes(ctypes.byref(layout)))
+
+
+def make_latent_cache(layout: LatentLayout, pages: PageLayout, device="cuda") -> torch.Tensor:
+    """A cache of zeros: [n_blocks, block_size, latent_dim + rope_dim] bf16, or for MXFP8 the rows' bytes
+    [n_blocks, block_size, engram_latent_row_bytes] uint8."""
+    return torch.zeros(_cache_shape(layout, pages), dtype=_cache_type(layout), device=device)
+
+
+def _cache_type(layout: LatentLayout):
+    return torch.uint8 if layout.cache_format == CACHE_MXFP8 else torch.bfloat16
+
+
+def _cache_shape(layout: LatentLayout, pages: PageLayout) -> tuple:
+    row = layout.latent_dim + layout.rope_dim
+    if layout.cache_format == CACHE_MXFP8:
+        row += 16 + layout.rope_dim
+    return (pages.n_blocks, pages.block_size, row)
+
+
+def _no_grad(where: str, **tensors) -> None:
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors.values()):
+        _refuse_grad(where, **tensors)
+
+
+def engram_latent_write(layout: LatentLayout, pages: PageLayout, latent: torch.Tensor, rope: torch.Tensor, plan: BatchPlan,
+                        cache: torch.Tensor, err_count: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Writes the rows of a plan's tokens into the cache (engram_latent_write in include/engram.h): latent
+    [plan.max_tokens, latent_dim] and rope [plan.max_tokens, rope_dim] bf16 may be slices of wider rows.  Returns the
+    cache, which is updated in place."""
+    _no_grad("engram_latent_write", latent=latent, rope=rope, cache=cache)
+    n, dev, bf16 = plan._sizes[1], cache.get_device(), torch.bfloat16
+    at = _plan_on(plan, dev)._out
+    ls = _rows("latent", latent, (n,), (layout.latent_dim,), bf16, dev)
+    rs = _rows("rope", rope, (n,), (layout.rope_dim,), bf16, dev)
+    to = _tensor("cache", cache, _cache_shape(layout, pages), _cache_type(layout), dev)
+    _launch("engram_latent_write", dev, _lib.engram_latent_write, layout, pages, latent.data_ptr(), ls, rope.data_ptr(), rs, at.slots,
+            n, to, _counter(err_count, dev))
+    return cache
+
+
+def engram_latent_read(layout: LatentLayout, pages: PageLayout, cache: torch.Tensor, plan: BatchPlan, block_table: torch.Tensor,
+                       max_rows: int, min_tokens: int = 1, latent: Optional[torch.Tensor] = None,
+                       rope: Optional[torch.Tensor] = None, row_start: Optional[torch.Tensor] = None,
+                       err_count: Optional[torch.Tensor] = None):
+    """Reads the rows of a plan's requests with at least min_tokens new tokens back (engram_latent_read in
+    include/engram.h): returns (latent [max_rows, latent_dim], rope [max_rows, rope_dim], row_start [R + 1] int32).
+    Rows behind the last are left as they were (in tensors that the call makes: not set)."""
+    _no_grad("engram_latent_read", cache=cache, latent=latent, rope=rope)
+    (R, n), dev, bf16, i32 = plan._sizes, cache.get_device(), torch.bfloat16, torch.int32
+    at = _plan_on(plan, dev)._out
+    src = _tensor("cache", cache, _cache_shape(layout, pages), _cache_type(layout), dev)
+    table = _tensor("block_table", block_table, (R, pages.max_blocks), i32, dev)
+    if latent is None:
+        latent = cache.new_empty((max_rows, layout.latent_dim), dtype=bf16)
+    if rope is None:
+        rope = cache.new_empty((max_rows, layout.rope_dim), dtype=bf16)
+    if row_start is None:
+        row_start = cache.new_empty((R + 1,), dtype=i32)
+    _launch("engram_latent_read", dev, _lib.engram_latent_read, layout, pages, src, at.token_start, at.start_pos, R, table, n,
+            min_tokens, max_rows, _tensor("row_start", row_start, (R + 1,), i32, dev),
+            _tensor("latent", latent, (max_rows, layout.latent_dim), bf16, dev),
+            _tensor("rope", rope, (max_rows, layout.rope_dim), bf16, dev), _counter(err_count, dev))
+    return latent, rope, row_start
+
+
+def engram_latent_attention_workspace_bytes(layout: LatentLayout) -> int:
+    """For any call of this layout on the current device."""
+    return int(_lib.engram_latent_attention_workspace_bytes(ctypes.byref(layout)))
+
+
+def engram_latent_attention_expanded_workspace_bytes(layout: LatentLayout, R: int, n_tokens: int, n_rows: int) -> int:
+    """For n_tokens tokens of R requests over n_rows rows on the current device."""
+    return int(_lib.engram_latent_attention_expanded_workspace_bytes(ctypes.byref(layout), R, n_tokens, n_rows))
+
+
+def _attention_out(q: torch.Tensor, out: Optional[torch.Tensor], n: int, row: tuple, dev: int):
+    """(out, its stride)."""
+    if out is None:
+        return q.new_empty((n, *row)), row[0] * row[1]
+    return out, _rows("out", out, (n,), row, torch.bfloat16, dev)
+
+
+def _given(workspace: torch.Tensor, dev: int):
+    _contig("workspace", workspace)
+    if workspace.get_device() != dev:
+        raise ValueError(f"workspace is on {workspace.device}, not with the other tensors")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def engram_latent_attention(layout: LatentLayout, pages: PageLayout, q: torch.Tensor, cache: torch.Tensor, plan: BatchPlan,
+                            block_table: torch.Tensor, max_tokens: int = 0, out: Optional[torch.Tensor] = None,
+                            lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                            err_count: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Absorbed attention of a plan's tokens over the cache's pages (engram_latent_attention in include/engram.h):
+    out [plan.max_tokens, heads, latent_dim] bf16 of q [plan.max_tokens, heads, latent_dim + rope_dim] bf16, for
+    requests with at most max_tokens new tokens (0: all).  q and out may be slices of wider rows.  Rows of other
+    tokens are left as they were (in an out that the call makes: not set).  lse [plan.max_tokens, heads] fp32 is
+    filled where it is given.  Without a workspace the call takes one from torch's allocator: calls on other streams, and
+    captured graphs, then have their own."""
+    _no_grad("engram_latent_attention", q=q, cache=cache, out=out, lse=lse)
+    (R, n), dev, H, D = plan._sizes, cache.get_device(), layout.heads, layout.latent_dim
+    at = _plan_on(plan, dev)._out
+    src = _tensor("cache", cache, _cache_shape(layout, pages), _cache_type(layout), dev)
+    qs = _rows("q", q, (n,), (H, D + layout.rope_dim), torch.bfloat16, dev)
+    table = _tensor("block_table", block_table, (R, pages.max_blocks), torch.int32, dev)
+    out, os_ = _attention_out(q, out, n, (H, D), dev)
+    lp = None if lse is None else _tensor("lse", lse, (n, H), torch.float32, dev)
+    if workspace is None:
+        workspace = q.new_empty(_on_device(dev, engram_latent_attention_workspace_bytes, layout), dtype=torch.uint8)
+    ws, ws_bytes = _given(workspace, dev)
+    _launch("engram_latent_attention", dev, _lib.engram_latent_attention, layout, pages, q.data_ptr(), qs, src, at.token_start,
+            at.start_pos, R, table, n, max_tokens, out.data_ptr(), os_, lp, ws, ws_bytes, _counter(err_count, dev))
+    return out
+
+
+def _on_device(dev: int, fn, *args):
+    if dev < 0:
+        raise ValueError("tensors must be on a GPU, got cpu")
+    if dev == _current_device():
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
+def engram_latent_attention_expanded(layout: LatentLayout, q: torch.Tensor, kv: torch.Tensor, rope: torch.Tensor,
+                                     row_start: torch.Tensor, plan: BatchPlan, min_tokens: int = 1,
+                                     out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Expanded attention of a plan's tokens (engram_latent_attention_expanded in include/engram.h): out
+    [plan.max_tokens, heads, head_dim] bf16 of q [plan.max_tokens, heads, head_dim + rope_dim], kv [n_rows, heads,
+    2 * head_dim] (of each head the key part, then the value), rope [n_rows, rope_dim] and row_start [R + 1] as
+    engram_latent_read gives it, for requests with at least min_tokens new tokens.  q, kv, rope and out may be slices of
+    wider rows; rows of other tokens, lse and workspace as in engram_latent_attention."""
+    _no_grad("engram_latent_attention_expanded", q=q, kv=kv, rope=rope, out=out, lse=lse)
+    (R, n), dev, H, D, bf16 = plan._sizes, q.get_device(), layout.heads, layout.head_dim, torch.bfloat16
+    at = _plan_on(plan, dev)._out
+    if kv.dim() != 3:
+        raise ValueError(f"kv has shape {tuple(kv.shape)}, expected [n_rows, {H}, {2 * D}]")
+    rows = kv.shape[0]
+    qs = _rows("q", q, (n,), (H, D + layout.rope_dim), bf16, dev)
+    ks = _rows("kv", kv, (rows,), (H, 2 * D), bf16, dev)
+    rs = _rows("rope", rope, (rows,), (layout.rope_dim,), bf16, dev)
+    first = _tensor("row_start", row_start, (R + 1,), torch.int32, dev)
+    out, os_ = _attention_out(q, out, n, (H, D), dev)
+    lp = None if lse is None else _tensor("lse", lse, (n, H), torch.float32, dev)
+    ws, ws_bytes = None, 0
+    if workspace is None:
+        need = _on_device(dev, engram_latent_attention_expanded_workspace_bytes, layout, R, n, rows)
+        if need > 0:
+            workspace = q.new_empty(need, dtype=torch.uint8)
+    if workspace is not None:
+        ws, ws_bytes = _given(workspace, dev)
+    _launch("engram_latent_attention_expanded", dev, _lib.engram_latent_attention_expanded, layout, q.data_ptr(), qs, kv.data_ptr(),
+            ks, rope.data_ptr(), rs, first, rows, at.token_start, at.start_pos, R, n, min_tokens, out.data_ptr(), os_, lp, ws,
+            ws_bytes)
     return out

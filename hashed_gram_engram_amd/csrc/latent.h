@@ -1,0 +1,83 @@
+// Kernel argument blocks and launchers of the latent cache and its attention (host side).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace engram {
+
+// A step's requests in a plan's pages.
+struct LatentRequests {
+  const int32_t* token_start;  // [R + 1]
+  const int32_t* start_pos;    // [R]
+  const int32_t* block_table;  // [R, max_blocks]
+  int R, n_tokens;
+  int block_size, max_blocks, n_blocks;
+  int min_tokens, max_tokens;  // requests with so many new tokens take part
+  int window;                  // 0: none
+};
+
+// Bytes of a cache row.
+constexpr int latent_row_bytes(int latent_dim, int rope_dim, bool fp8) {
+  return fp8 ? latent_dim + 16 + 2 * rope_dim : 2 * (latent_dim + rope_dim);
+}
+
+struct LatentWriteArgs {
+  const uint16_t* latent;
+  const uint16_t* rope;
+  const int64_t* slots;
+  uint8_t* cache;
+  int32_t* err_count;
+  int64_t latent_stride, rope_stride, n_slots;
+  int n_tokens, latent_dim, rope_dim, fp8;
+};
+hipError_t launch_latent_write(const LatentWriteArgs& a, hipStream_t stream);
+
+struct LatentReadArgs {
+  LatentRequests rq;
+  const uint8_t* cache;
+  int32_t* row_start;
+  uint16_t* latent;
+  uint16_t* rope;
+  int32_t* err_count;
+  int64_t max_rows;
+  int latent_dim, rope_dim, fp8;
+};
+hipError_t launch_latent_read(const LatentReadArgs& a, int cus, hipStream_t stream);
+
+struct AbsorbedArgs {
+  LatentRequests rq;
+  const uint16_t* q;
+  const uint8_t* cache;
+  uint16_t* out;
+  float* lse;
+  int32_t* err_count;
+  int64_t q_stride, out_stride;
+  float scale_log2;  // of the scores, times log2 e
+  int heads, latent_dim, rope_dim, fp8;
+  char* workspace;
+};
+int64_t absorbed_workspace_bytes(int latent_dim, int cus);
+hipError_t launch_latent_absorbed(const AbsorbedArgs& a, int cus, hipStream_t stream);
+
+struct ExpandedArgs {
+  LatentRequests rq;  // (no pages)
+  const uint16_t* q;
+  const uint16_t* kv;
+  const uint16_t* rope;
+  const int32_t* row_start;  // [R + 1]
+  uint16_t* out;
+  float* lse;
+  int64_t q_stride, kv_stride, rope_stride, out_stride;
+  int n_rows;
+  float scale_log2;
+  int heads, head_dim, rope_dim;
+  float* workspace;
+  // set by the launcher: tiles of the grid, and the parts that a tile's keys are shared out in
+  int tiles, parts;
+};
+int64_t expanded_workspace_bytes(int64_t R, int64_t n_tokens, int64_t n_rows, int heads, int head_dim, int cus);
+hipError_t launch_latent_expanded(ExpandedArgs a, int cus, hipStream_t stream);
+
+}  // namespace engram

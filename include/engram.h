@@ -417,7 +417,118 @@ size_t engram_linear_workspace_bytes(const engram_linear_layout* layout, int64_t
  * 512 and none for 8192, and a call whose workspace is too small is refused.)  Host work of up to some 50 ms. */
 size_t engram_linear_workspace_bytes_up_to(const engram_linear_layout* layout, int64_t M);
 
+/* ---- The latent cache and the attention that reads it ------------------------------------------
+ * Attention whose keys and values come from one latent vector a token (latent_dim features) and one key
+ * part that carries its position (rope_dim features), shared by all heads.  A step writes the rows of its
+ * tokens into the plan's pages (engram_latent_write), then each of its requests attends to what it holds:
+ *  - absorbed (engram_latent_attention): queries that have been multiplied into the latent space read the
+ *    pages directly; for decoding and short parts of prompts;
+ *  - expanded (engram_latent_read, engram_linear, engram_latent_attention_expanded): the rows are read back,
+ *    multiplied into keys and values of each head, and attended to; for prompts.
+ * min_tokens and max_tokens divide the requests of one step between the two by their new tokens.
+ * token_start, start_pos, slots are a plan's (engram_batch_plan_out); the new tokens of request r are flat
+ * tokens token_start[r] .. token_start[r + 1] - 1, at positions start_pos[r] .. .  Whatever these arrays
+ * hold, no access leaves the tensors: token ranges are cut to n_tokens, positions to max_blocks * block_size.
+ * The ranges of different requests must not overlap (a plan's do not).  At most 4096 requests.
+ * The conventions above hold; calls that write different buffers may overlap in time. */
+
+/* A cache row (one slot of a page), engram_latent_row_bytes() bytes.
+ * BF16: latent_dim, then rope_dim bf16.  MXFP8: latent_dim e4m3fn codes; 16 bytes, the first
+ * latent_dim / 32 of them E8M0 scales, one per 32 features; rope_dim bf16.  A feature is
+ * e4m3(code) * 2^(scale - 127), which bf16 holds exactly wherever engram_latent_write made it. */
+typedef enum { ENGRAM_CACHE_BF16 = 0, ENGRAM_CACHE_MXFP8 = 1 } engram_cache_format;
+
+typedef struct {
+  int32_t heads;        /* query heads, 1 .. 1024                                                   */
+  int32_t latent_dim;   /* 128, 256 or 512                                                          */
+  int32_t rope_dim;     /* 32 or 64                                                                 */
+  int32_t head_dim;     /* expanded form: features of a head's own key part and of its value, 64 or 128 */
+  int32_t cache_format; /* engram_cache_format                                                      */
+  int32_t window;       /* 0: a token sees every position up to its own; w > 0: the last w of them  */
+  float scale;          /* of the scores; finite                                                    */
+} engram_latent_layout;
+
+/* Bytes of a cache row (0 on an invalid layout).  A cache is [n_blocks, block_size, row bytes]. */
+size_t engram_latent_row_bytes(const engram_latent_layout* layout);
+
+/* Writes the rows of a step's tokens:
+ *   latent [n_tokens, latent_dim], rope [n_tokens, rope_dim] bf16, their own strides from token to token
+ *          (multiples of 8; e.g. both slices of a projection's rows)
+ *   slots  [n_tokens] int64: row of the cache; a negative one (behind a plan's last token) is passed over,
+ *          one past the pool too and adds 1 to *err_count.  Two tokens must not share a slot (a plan's do
+ *          not): its row then holds parts of either.
+ *   cache  [n_blocks, block_size, row bytes] in/out
+ * MXFP8: the scale of a block of 32 features is the least power of two, 2^-127 at least, that brings its finite
+ * magnitudes within 448 (a block of zeros takes 2^-127); codes are rounded to nearest even (with the scale 2^120 to
+ * 240 at most: the next code stands for 2^128, which bf16 has not); a feature that is not finite becomes a
+ * NaN code.  The rope part keeps its bits, as BF16 rows do. */
+engram_status engram_latent_write(const engram_latent_layout* layout, const engram_page_layout* pages,
+                                  const uint16_t* latent, int64_t latent_stride, const uint16_t* rope,
+                                  int64_t rope_stride, const int64_t* slots, int64_t n_tokens, void* cache,
+                                  int32_t* err_count, engram_stream_t stream);
+
+/* Reads the rows of a step's requests back, one request after the other, positions ascending: of each
+ * request with at least min_tokens (>= 1) new tokens, positions 0 (with a window: the first that its first
+ * new token sees) .. its last new token's.
+ *   row_start [R + 1] int32 out: first row of each request; [R] = all rows
+ *   latent [max_rows, latent_dim], rope [max_rows, rope_dim] bf16 out; rows behind the last stay as they are
+ * The first request whose rows would pass max_rows, and every later one, gets none and adds 1 to
+ * *err_count.  A position whose page is outside [0, n_blocks) reads as zeros and adds 1. */
+engram_status engram_latent_read(const engram_latent_layout* layout, const engram_page_layout* pages,
+                                 const void* cache, const int32_t* token_start, const int32_t* start_pos,
+                                 int64_t R, const int32_t* block_table, int64_t n_tokens, int32_t min_tokens,
+                                 int64_t max_rows, int32_t* row_start, uint16_t* latent, uint16_t* rope,
+                                 int32_t* err_count, engram_stream_t stream);
+
+/* Absorbed attention over the pages, for each request with 1 .. max_tokens new tokens (max_tokens 0: any):
+ *   q   [n_tokens, heads, latent_dim + rope_dim] bf16, q_stride elements from token to token (a multiple of 8,
+ *       heads contiguous)
+ *   out [n_tokens, heads, latent_dim] bf16, out_stride elements from token to token (a multiple of 8)
+ *   lse [n_tokens, heads] fp32 out, or NULL: the natural logarithm of the softmax's sum
+ * For the token at position p: s_j = scale * q . row_j over the positions j <= p (window: j > p - window),
+ * out = sum_j softmax(s)_j latent_j.  Positions that are masked, past the request or on a page outside
+ * [0, n_blocks) take no part, whatever they hold (a bad page among the visible ones makes *err_count
+ * grow); where none is left out is 0 and lse -infinity.  Scores, softmax and sums are fp32, the weights
+ * are rounded to bf16 for the second product, out once.  Rows of other tokens stay as they are. */
+engram_status engram_latent_attention(const engram_latent_layout* layout, const engram_page_layout* pages,
+                                      const uint16_t* q, int64_t q_stride, const void* cache,
+                                      const int32_t* token_start, const int32_t* start_pos, int64_t R,
+                                      const int32_t* block_table, int64_t n_tokens, int32_t max_tokens,
+                                      uint16_t* out, int64_t out_stride, float* lse, void* workspace,
+                                      size_t workspace_bytes, int32_t* err_count, engram_stream_t stream);
+
+/* Bytes of workspace engram_latent_attention needs on the current device for any call of this layout: room for the
+ * parts of requests whose positions are shared between workgroups.  It does not depend on the lengths.
+ * Its contents need no clearing and mean nothing after the call; calls that overlap in time (other
+ * streams, captured graphs) must use different workspaces. */
+size_t engram_latent_attention_workspace_bytes(const engram_latent_layout* layout);
+
+/* Expanded attention, for each request with at least min_tokens (>= 1) new tokens:
+ *   q    [n_tokens, heads, head_dim + rope_dim] bf16, q_stride from token to token (a multiple of 8)
+ *   kv   [n_rows, heads, 2 * head_dim] bf16, kv_stride from row to row (a multiple of 8): of each head the
+ *        key part, then the value
+ *   rope [n_rows, rope_dim] bf16, rope_stride from row to row (a multiple of 8): the key part all heads share
+ *   row_start [R + 1] int32: rows row_start[r] .. row_start[r + 1] - 1 are the last positions of request r, the
+ *        last of them its last new token's (as engram_latent_read lays them out); cut to n_rows
+ *   out  [n_tokens, heads, head_dim] bf16, out_stride (a multiple of 8); lse as above
+ * s_j = scale * q . (key part of row j and head, rope_j) over the request's rows at positions j <= p
+ * (window: j > p - window), out = sum_j softmax(s)_j value_j; empty rows, masked rows, precision and other
+ * tokens as above. */
+engram_status engram_latent_attention_expanded(const engram_latent_layout* layout, const uint16_t* q,
+                                               int64_t q_stride, const uint16_t* kv, int64_t kv_stride,
+                                               const uint16_t* rope, int64_t rope_stride,
+                                               const int32_t* row_start, int64_t n_rows,
+                                               const int32_t* token_start, const int32_t* start_pos, int64_t R,
+                                               int64_t n_tokens, int32_t min_tokens, uint16_t* out,
+                                               int64_t out_stride, float* lse, void* workspace,
+                                               size_t workspace_bytes, engram_stream_t stream);
+
+/* The same for engram_latent_attention_expanded with n_tokens tokens of R requests over n_rows rows. */
+size_t engram_latent_attention_expanded_workspace_bytes(const engram_latent_layout* layout, int64_t R,
+                                                        int64_t n_tokens, int64_t n_rows);
+
 /* Host-only checks of the layouts above; no device work. */
+engram_status engram_latent_layout_check(const engram_latent_layout* layout);
 engram_status engram_page_layout_check(const engram_page_layout* layout);
 engram_status engram_norm_layout_check(const engram_norm_layout* layout);
 engram_status engram_linear_layout_check(const engram_linear_layout* layout);
