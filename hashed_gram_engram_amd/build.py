@@ -23,7 +23,8 @@ COMMON = ["--offload-arch=" + ARCH, "-O3", "-fPIC", "-std=c++17",
 
 ENGRAM_SRC = ["engram_api.hip", "gather_gate.hip", "hash.hip", "stream.hip", "tiled.hip",
               "serving_api.hip", "batch_plan.hip", "hash_paged.hip", "residual_norm.hip", "linear.hip",
-              "latent_api.hip", "latent_cache.hip", "latent_absorbed.hip", "latent_expanded.hip"]
+              "latent_api.hip", "latent_cache.hip", "latent_absorbed.hip", "latent_absorbed_rows.hip",
+              "latent_expanded.hip"]
 LIB_ENGRAM = os.path.join(HERE, "libengram.so")
 LIB_SYNTH = os.path.join(ROOT, "synth", "libsynth_fill.so")
 LIB_ORACLE = os.path.join(ROOT, "oracle", "liboracle.so")

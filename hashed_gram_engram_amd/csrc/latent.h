@@ -16,6 +16,19 @@ struct LatentRequests {
   int block_size, max_blocks, n_blocks;
   int min_tokens, max_tokens;  // requests with so many new tokens take part
   int window;                  // 0: none
+  uint32_t page_mul, page_shift;  // of page_of
+  // pos / block_size of a position below 2^30: page_mul = ceil(2^(30 + s) / block_size) with s the bits of block_size - 1, so
+  // that page_mul block_size - 2^(30 + s) < 2^s and the quotient is off by less than 1 / block_size
+  __host__ __device__ int page_of(int pos) const { return int((uint64_t(uint32_t(pos)) * page_mul) >> page_shift); }
+  void set_pages(int block, int blocks, int64_t pool) {
+    block_size = block;
+    max_blocks = blocks;
+    n_blocks = int(pool);
+    int s = 0;
+    while ((int64_t(1) << s) < block) ++s;
+    page_mul = uint32_t(((uint64_t(1) << (30 + s)) + block - 1) / block);
+    page_shift = 30 + s;
+  }
 };
 
 // Bytes of a cache row.
@@ -54,11 +67,13 @@ struct AbsorbedArgs {
   float* lse;
   int32_t* err_count;
   int64_t q_stride, out_stride;
-  float scale_log2;  // of the scores, times log2 e
+  float scale_log2;  // magnitude of the scores' scale, times log2 e, above zero (a masked score is -infinity times it)
+  uint32_t q_sign;   // 0x80008000: queries are negated (a negative scale)
   int heads, latent_dim, rope_dim, fp8;
   char* workspace;
 };
 int64_t absorbed_workspace_bytes(int latent_dim, int cus);
+hipError_t launch_absorbed_rows(const AbsorbedArgs& a, int G, bool wide, hipStream_t stream);  // 64 rows and more a request
 hipError_t launch_latent_absorbed(const AbsorbedArgs& a, int cus, hipStream_t stream);
 
 struct ExpandedArgs {
@@ -72,6 +87,7 @@ struct ExpandedArgs {
   int64_t q_stride, kv_stride, rope_stride, out_stride;
   int n_rows;
   float scale_log2;
+  uint32_t q_sign;
   int heads, head_dim, rope_dim;
   float* workspace;
   // set by the launcher: tiles of the grid, and the parts that a tile's keys are shared out in

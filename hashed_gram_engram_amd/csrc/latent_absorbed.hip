@@ -19,43 +19,15 @@
 // Rows that take no part (outside the tile's positions, on a bad page) are zeros in LDS and their scores
 // -infinity.  Where the tokens of a tile see different positions, a value that is not finite must not reach those that do
 // not see it (0 times infinity): such stages are looked through and, if they hold one, added by plain_values.
-#include "latent_common.h"
-#include "serving.h"
+#include <stdlib.h>
+#include "latent_units.h"
 
 namespace engram {
 
 namespace {
 
-typedef __attribute__((address_space(3))) void* lds_ptr_t;
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) s16x4* lds_s16x4_t;
-
 constexpr int kThreads = 256;
-constexpr int kTB = 64;           // positions per stage
-constexpr float kGrow = 8.0f;     // the reference maximum moves when it is passed by more (log2)
-constexpr float kInf = __builtin_inff();
-
-__device__ __forceinline__ void wait_lds_barrier() {
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-}
-__device__ __forceinline__ void wait_all_barrier() {
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-}
-
-// 16-byte chunk c of row r lies at position c ^ swizzle(r): 16 rows' reads of one chunk cover all 64 banks once
-// (rows start at even multiples of 128 bytes or odd ones by turns), and so do 8 rows' transposed
-// reads of a pair of chunks.
-__device__ __forceinline__ int swizzle(int r) { return (r & 6) | ((r >> 3) & 1); }
-
-// What a workgroup leaves in the workspace, for the join.
-struct Part {
-  int32_t first, row0, rows;  // flat token, first row and number of rows of the request; rows 0: no part
-  int32_t last;               // the part that ends its tile
-};
+constexpr int kTB = 64;  // positions per stage
 
 template <int DC, int MB>
 struct Shape {
@@ -72,16 +44,6 @@ struct Shape {
   static constexpr int kAlive = kSlots + 4 * kTB * 8;
   static constexpr int kMisc = kAlive + 4 * 8;
   static constexpr int kBytes = kMisc + 64;
-  // per workgroup in the workspace: two parts of accumulators, maxima and sums, and their descriptions
-  static constexpr int64_t kAccB = int64_t(M) * DC * 4, kMLB = M * 8;
-};
-
-struct Tile {
-  Span s;
-  int r, row0, rows;    // first row of the tile, rows of the request
-  int lo, hi;           // positions that any of its rows sees
-  int p_min, p_max;     // positions of its first and last row's tokens
-  int base;             // position of unit 0 (the request's first)
 };
 
 template <int DC, int MB, bool FP8>
@@ -98,90 +60,31 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
   float* smax = reinterpret_cast<float*>(lds + S::kMax);
   int64_t* misc = reinterpret_cast<int64_t*>(lds + S::kMisc);
 
-  // ---- this workgroup's units
-  auto shape_of = [&](const Span& s, int* tiles, int* stages) {
-    *tiles = (s.tokens * a.heads + S::M - 1) / S::M;
-    *stages = (s.hi - s.lo + kTB - 1) / kTB;
-  };
-  const int G = gridDim.x;
-  int w = blockIdx.x;
-  Part* parts = reinterpret_cast<Part*>(a.workspace);
-  float* ml = reinterpret_cast<float*>(a.workspace + int64_t(G) * 2 * sizeof(Part));
-  f32x4* accs = reinterpret_cast<f32x4*>(a.workspace + int64_t(G) * 2 * (sizeof(Part) + S::kMLB));
-  int64_t u, u1;
-  int r;
-  int64_t rem;
-  {
-    const int items = (a.rq.R + kThreads - 1) / kThreads, r0 = tid * items;
-    int64_t mine = 0, total;
-    for (int k = r0; k < r0 + items && k < a.rq.R; ++k) {
-      int tiles, stages;
-      shape_of(span_of(a.rq, k), &tiles, &stages);
-      mine += int64_t(tiles) * stages;
-    }
-    const int64_t before = block_scan64<kThreads>(mine, misc + 2, &total);
-    // where every workgroup has work, an XCD takes neighbours (they share tiles' rows); else all XCDs take some
-    const int n = total < G ? int(total) : G;
-    if (n == G && (G & 7) == 0) w = (w & 7) * (G >> 3) + (w >> 3);
-    if (tid == 0) {
-      parts[2 * w].rows = 0;
-      parts[2 * w + 1].rows = 0;
-    }
-    if (w >= n) return;
-    u = total / n * w + total % n * w / n;  // (so each of the n has a unit at least, and a tile's parts are neighbours)
-    u1 = total / n * (w + 1) + total % n * (w + 1) / n;
-    if (u >= before && u < before + mine) {
-      int64_t at = before;
-      for (int k = r0; k < r0 + items && k < a.rq.R; ++k) {
-        int tiles, stages;
-        shape_of(span_of(a.rq, k), &tiles, &stages);
-        const int64_t n = int64_t(tiles) * stages;
-        if (u < at + n) {
-          misc[0] = k;
-          misc[1] = u - at;
-          break;
-        }
-        at += n;
-      }
-    }
-    __syncthreads();
-    r = __builtin_amdgcn_readfirstlane(int(misc[0]));
-    rem = misc[1];
-    rem = (int64_t(__builtin_amdgcn_readfirstlane(int(rem >> 32))) << 32) | uint32_t(__builtin_amdgcn_readfirstlane(int(rem)));
-  }
+  const PartSpace space = part_space(a.workspace, gridDim.x, S::M);
+  // A chunk's place differs from row to row in the low three bits of its number only, so the reads of a stage take
+  // two (keys) and four (values) addresses and constants.  (Rows start at multiples of 128 bytes.)
+  const int key_at = (tg * S::kTBQ * 16 + i16) * S::kRowB + (g ^ latent_swizzle(i16)) * 16;
+  const int vrow = 4 * g + (i16 >> 2);
+  const int value_at = vrow * S::kRowB + ((wv * (DC / 32) + ((i16 & 3) >> 1)) ^ latent_swizzle(vrow)) * 16 + (i16 & 1) * 8;
+  Units un;
+  if (!my_units<kThreads, S::M, kTB>(a.rq, a.heads, space.parts, misc, &un)) return;
 
-  while (u < u1) {
-    // ---- the next segment: stages [c0, c0 + n) of one tile
-    Tile t;
-    t.r = r;
-    t.s = span_of(a.rq, r);
-    int tiles, stages;
-    shape_of(t.s, &tiles, &stages);
-    const int64_t units = int64_t(tiles) * stages;
-    const int tile = int(rem / stages), c0 = int(rem - int64_t(tile) * stages);
-    const int n = int(u1 - u < stages - c0 ? u1 - u : stages - c0);
-    t.row0 = tile * S::M;
-    t.rows = t.s.tokens * a.heads;
-    const int last_row = t.row0 + S::M < t.rows ? t.row0 + S::M - 1 : t.rows - 1;
-    t.p_min = t.s.pos + t.row0 / a.heads;
-    t.p_max = t.s.pos + last_row / a.heads;
-    t.base = t.s.lo;
-    t.lo = a.rq.window > 0 && t.p_min + 1 > a.rq.window ? t.p_min + 1 - a.rq.window : 0;
-    t.hi = t.p_max + 1;
+  while (un.u < un.u1) {
+    const Segment t = segment_of<S::M, kTB>(a.rq, a.heads, un);
+    const int c0 = t.c0, n = t.n;
 
     // ---- queries: fragments in registers, and the position of each row's token (-1: no row)
     u32x4 qf[S::kMBQ][S::kKB + 2];
     int qpos[S::kMBQ];
 #pragma unroll
     for (int mb = 0; mb < S::kMBQ; ++mb) {
-      const int row = t.row0 + (rh * S::kMBQ + mb) * 16 + i16;
-      const bool on = row < t.rows;
-      const int tok = on ? row / a.heads : 0, head = on ? row - tok * a.heads : 0;
-      qpos[mb] = on ? t.s.pos + tok : -1;
+      const int row = t.row0 + (rh * S::kMBQ + mb) * 16 + i16, at = row < t.rows ? row : t.rows - 1;  // (rows past the last repeat it)
+      const int tok = at / a.heads, head = at - tok * a.heads;
+      qpos[mb] = row < t.rows ? t.s.pos + tok : -1;
       const uint16_t* src = a.q + (t.s.first + tok) * a.q_stride + int64_t(head) * (DC + a.rope_dim) + 8 * g;
 #pragma unroll
       for (int kb = 0; kb < S::kKB + 2; ++kb)
-        qf[mb][kb] = on && kb < S::kKB + rkb ? *reinterpret_cast<const u32x4*>(src + 32 * kb) : u32x4{0u, 0u, 0u, 0u};
+        qf[mb][kb] = *reinterpret_cast<const u32x4*>(src + 32 * (kb < S::kKB + rkb ? kb : 0)) ^ a.q_sign;
     }
     f32x4 acc[S::kFB][MB];
     float m_run[MB], l_own[S::kMBQ];
@@ -198,8 +101,8 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
     auto find_slot = [&](int c) -> int64_t {  // (wave 0) slot of the lane's row of stage c
       const int pos = t.base + c * kTB + lane;
       if (c >= c0 + n || pos < t.lo || pos >= t.hi) return -1;
-      const int64_t slot = slot_of(a.rq, r, pos);
-      if (slot < 0 && tile == 0 && a.err_count != nullptr) atomicAdd(a.err_count, 1);
+      const int64_t slot = slot_of(a.rq, un.r, pos);
+      if (slot < 0 && t.tile == 0 && a.err_count != nullptr) atomicAdd(a.err_count, 1);
       return slot;
     };
     auto put_slot = [&](int c, int64_t slot) {
@@ -233,7 +136,7 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
       const uint64_t on = alive[c & 3];
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
-        const int row = tid / kNP + k * (kThreads / kNP), sw = swizzle(row);
+        const int row = tid / kNP + k * (kThreads / kNP), sw = latent_swizzle(row);
         u32x4 o0, o1;
         latent16(code[k], scale[k], o0, o1);
         if (!((on >> row) & 1)) o0 = o1 = u32x4{0u, 0u, 0u, 0u};
@@ -245,7 +148,7 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
       for (int k = 0; k < 2; ++k) {
         const int rp = 4 * rkb, id = tid + k * kThreads, row = id / rp;
         if (k < rkb)
-          *reinterpret_cast<u32x4*>(buf + row * S::kRowB + ((DC / 8 + id % rp) ^ swizzle(row)) * 16) =
+          *reinterpret_cast<u32x4*>(buf + row * S::kRowB + ((DC / 8 + id % rp) ^ latent_swizzle(row)) * 16) =
               (on >> row) & 1 ? rope[k] : u32x4{0u, 0u, 0u, 0u};
       }
     };
@@ -255,7 +158,7 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
 #pragma unroll
       for (int k = 0; k < S::kChunks / 4; ++k) {
         const int id = (k * 4 + wv) * 64 + lane, row = id / S::kChunks;
-        int ch = (id - row * S::kChunks) ^ swizzle(row);
+        int ch = (id - row * S::kChunks) ^ latent_swizzle(row);
         ch = ch < DC / 8 + 4 * rkb ? ch : 0;  // (a place that is not read)
         const int64_t slot = sl[row];
         __builtin_amdgcn_global_load_lds((const void*)(a.cache + (slot < 0 ? 0 : slot) * row_b + ch * 16),
@@ -307,15 +210,26 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
       for (int tb = 0; tb < S::kTBQ; ++tb)
 #pragma unroll
         for (int mb = 0; mb < S::kMBQ; ++mb) s[tb][mb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      const int sw = swizzle(i16);
+      {
+        const char* kp[2] = {buf + key_at, buf + (key_at ^ 64)};
+        auto key = [&](int kb, int tb) { return *reinterpret_cast<const u32x4*>(kp[kb & 1] + tb * 16 * S::kRowB + (kb >> 1) * 128); };
+        constexpr int kDeep = 4;
+        u32x4 kf[kDeep][S::kTBQ];
 #pragma unroll
-      for (int kb = 0; kb < S::kKB + 2; ++kb) {
-        if (kb == S::kKB + 1 && rkb == 1) continue;
+        for (int kb = 0; kb < kDeep - 1; ++kb)
 #pragma unroll
-        for (int tb = 0; tb < S::kTBQ; ++tb) {
-          const u32x4 k = *reinterpret_cast<const u32x4*>(buf + ((tg * S::kTBQ + tb) * 16 + i16) * S::kRowB + ((kb * 4 + g) ^ sw) * 16);
+          for (int tb = 0; tb < S::kTBQ; ++tb) kf[kb][tb] = key(kb, tb);
 #pragma unroll
-          for (int mb = 0; mb < S::kMBQ; ++mb) s[tb][mb] = mfma16x16x32(k, qf[mb][kb], s[tb][mb]);
+        for (int kb = 0; kb < S::kKB + 2; ++kb) {
+          if (kb + kDeep - 1 < S::kKB + 2)
+#pragma unroll
+            for (int tb = 0; tb < S::kTBQ; ++tb) kf[(kb + kDeep - 1) % kDeep][tb] = key(kb + kDeep - 1, tb);
+          if (kb == S::kKB + 1 && rkb == 1) continue;
+#pragma unroll
+          for (int tb = 0; tb < S::kTBQ; ++tb)
+#pragma unroll
+            for (int mb = 0; mb < S::kMBQ; ++mb) s[tb][mb] = mfma16x16x32(kf[kb % kDeep][tb], qf[mb][kb], s[tb][mb]);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
       const uint64_t on = alive[c & 3];
@@ -342,8 +256,7 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
         for (int tb = 0; tb < S::kTBQ; ++tb)
 #pragma unroll
           for (int e = 0; e < 4; ++e) m = fmaxf(m, s[tb][mb][e]);
-        m = fmaxf(m, __shfl_xor(m, 16, kWave));
-        m = fmaxf(m, __shfl_xor(m, 32, kWave));
+        m = quad_max(m);
         if (g == 0) smax[tg * S::M + (rh * S::kMBQ + mb) * 16 + i16] = m;
       }
       if (wv == 0) put_slot(c + 2, slot2);
@@ -400,73 +313,82 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
         if (j + 1 < n) store_stage(c + 1, next);
         if (j + 2 < n) load_stage(c + 2);
       }
-      bool odd = false;  // a value that is not finite, where rows see different positions
-      if (differ) {
-        for (int k = tid; k < kTB * DC / 8; k += kThreads) {
-          const int row = k / (DC / 8), ch = k % (DC / 8);
-          const u32x4 v = *reinterpret_cast<const u32x4*>(buf + row * S::kRowB + (ch ^ swizzle(row)) * 16);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) odd |= (v[e] & 0x7F80u) == 0x7F80u || (v[e] & 0x7F800000u) == 0x7F800000u;
-        }
-        if (tid == 0) misc[0] = 0;
-        wait_lds_barrier();
-        if (odd) misc[0] = 1;
-      }
       wait_lds_barrier();
-      if (differ) odd = misc[0] != 0;
 
-      // ---- values
-      if (__builtin_expect(!odd, 1)) {
-#pragma unroll
-        for (int ks = 0; ks < kTB / 32; ++ks) {
-          u32x4 p[MB];
-#pragma unroll
-          for (int mb = 0; mb < MB; ++mb) {
-            const int row = mb * 16 + i16;
-            p[mb] = *reinterpret_cast<const u32x4*>(lds + S::kP + row * kTB * 2 + ((ks * 4 + g) ^ ((row >> 1) & 7)) * 16);
-          }
-          const int vrow = 4 * g + (i16 >> 2), vsw = swizzle(vrow);
-#pragma unroll
-          for (int fb = 0; fb < S::kFB; ++fb) {
-            const int ch = (wv * (DC / 4) + fb * 16) / 8 + ((i16 & 3) >> 1);
-            char* at = buf + (ks * 32 + vrow) * S::kRowB + (ch ^ vsw) * 16 + (i16 & 1) * 8;
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)at);
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(at + 16 * S::kRowB));
-            const u32x2 l2 = __builtin_bit_cast(u32x2, lo), h2 = __builtin_bit_cast(u32x2, hi);
-            const u32x4 v = {l2.x, l2.y, h2.x, h2.y};
-#pragma unroll
-            for (int mb = 0; mb < MB; ++mb) acc[fb][mb] = mfma16x16x32(v, p[mb], acc[fb][mb]);
-          }
-        }
-      } else {
-        // plain_values: each weight times its row, only where the query sees it
+      // ---- values that are not finite, where the tile's tokens see different positions: added row by row where they are
+      // seen, and zeros for the product
+      if (differ) {
 #pragma unroll 1
-        for (int row = 0; row < kTB; ++row) {
-          const int pos = j0 + row;
-          const int off = ((row >> 5) * 4 + ((row >> 2) & 3)) * 16, in = ((row >> 4) & 1) * 8 + (row & 3) * 2;
+        for (int half = 0; half < 2; ++half) {
+          uint32_t odd = 0;
+#pragma unroll 1
+          for (int k = tid; k < 32 * DC / 8; k += kThreads) {
+            const int row = k / (DC / 8);
+            if (any_not_finite(*reinterpret_cast<const u32x4*>(buf + (half * 32 + row) * S::kRowB + k % (DC / 8) * 16))) odd |= 1u << row;
+          }
+          odd = any_rows(odd, misc);
+          if (__builtin_expect(odd == 0, 1)) continue;
+#pragma unroll 1
+          for (uint32_t left = odd; left != 0; left &= left - 1) {
+            const int in = __builtin_ctz(left), row = half * 32 + in, pos = j0 + row;
 #pragma unroll
-          for (int mb = 0; mb < MB; ++mb) {
-            const int q = t.row0 + mb * 16 + i16, qp = q < t.rows ? t.s.pos + q / a.heads : -1;
-            if (!((on >> row) & 1) || pos > qp || (a.rq.window > 0 && pos <= qp - a.rq.window)) continue;
-            const float p = bf16_lo(*reinterpret_cast<const uint16_t*>(lds + S::kP + (mb * 16 + i16) * kTB * 2 +
-                                                                        (off ^ ((((mb * 16 + i16) >> 1) & 7) * 16)) + in));
+            for (int mb = 0; mb < MB; ++mb) {
+              const int m = mb * 16 + i16, q = t.row0 + m, qp = q < t.rows ? t.s.pos + q / a.heads : -1;
+              const bool seen = ((on >> row) & 1) && pos <= qp && (a.rq.window <= 0 || pos > qp - a.rq.window);
+              const float w = bf16_lo(*reinterpret_cast<const uint16_t*>(
+                  lds + S::kP + m * kTB * 2 + ((half * 4 + ((in >> 2) & 3)) ^ ((m >> 1) & 7)) * 16 + (in >> 4) * 8 + (in & 3) * 2));
 #pragma unroll
-            for (int fb = 0; fb < S::kFB; ++fb) {
-              const int f = wv * (DC / 4) + fb * 16 + 4 * g;
-              const u32x2 v = *reinterpret_cast<const u32x2*>(buf + row * S::kRowB + ((f >> 3) ^ swizzle(row)) * 16 + (f & 7) * 2);
-              acc[fb][mb] += f32x4{p * bf16_lo(v.x), p * bf16_hi(v.x), p * bf16_lo(v.y), p * bf16_hi(v.y)};
+              for (int fb = 0; fb < S::kFB; ++fb) {
+                const int ch = wv * (DC / 32) + fb * 2 + (g >> 1);
+                const u32x2 v = *reinterpret_cast<const u32x2*>(buf + row * S::kRowB + (ch ^ latent_swizzle(row)) * 16 + (g & 1) * 8);
+                acc[fb][mb][0] += seen ? w * bf16_lo(v.x) : 0.0f;
+                acc[fb][mb][1] += seen ? w * bf16_hi(v.x) : 0.0f;
+                acc[fb][mb][2] += seen ? w * bf16_lo(v.y) : 0.0f;
+                acc[fb][mb][3] += seen ? w * bf16_hi(v.y) : 0.0f;
+              }
             }
           }
+          wait_lds_barrier();
+          for (int k = tid; k < 32 * DC / 8; k += kThreads)
+            if ((odd >> (k / (DC / 8))) & 1)
+              *reinterpret_cast<u32x4*>(buf + (half * 32 + k / (DC / 8)) * S::kRowB + k % (DC / 8) * 16) = u32x4{0u, 0u, 0u, 0u};
+          wait_lds_barrier();
         }
+      }
+
+      // ---- values
+      const char* vp[4] = {buf + value_at, buf + (value_at ^ 32), buf + (value_at ^ 64), buf + (value_at ^ 96)};
+      auto value = [&](int k) {  // K block k / kFB, features k % kFB
+        const int fb = k % S::kFB;
+        const char* at = vp[fb & 3] + (fb >> 2) * 128 + k / S::kFB * 32 * S::kRowB;
+        const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)at));
+        const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(at + 16 * S::kRowB)));
+        return u32x4{lo.x, lo.y, hi.x, hi.y};
+      };
+      const char* pp = lds + S::kP + i16 * kTB * 2;
+      const int p_at = (g ^ ((i16 >> 1) & 7)) * 16;  // (of the second K block: ^ 64)
+      u32x4 p[2][MB];
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) p[0][mb] = *reinterpret_cast<const u32x4*>(pp + mb * 16 * kTB * 2 + p_at);
+      constexpr int kDeep = 4, kSteps = 2 * S::kFB;
+      u32x4 vf[kDeep];
+#pragma unroll
+      for (int k = 0; k < kDeep - 1; ++k) vf[k] = value(k);
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) p[1][mb] = *reinterpret_cast<const u32x4*>(pp + mb * 16 * kTB * 2 + (p_at ^ 64));
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        if (k + kDeep - 1 < kSteps) vf[(k + kDeep - 1) % kDeep] = value(k + kDeep - 1);
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) acc[k % S::kFB][mb] = mfma16x16x32(vf[k % kDeep], p[k / S::kFB][mb], acc[k % S::kFB][mb]);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
 
     // ---- the sums of all positions, then the outputs or a part
 #pragma unroll
     for (int mb = 0; mb < S::kMBQ; ++mb) {
-      float l = l_own[mb];
-      l += __shfl_xor(l, 16, kWave);
-      l += __shfl_xor(l, 32, kWave);
+      const float l = quad_sum(l_own[mb]);
       if (g == 0) smax[tg * S::M + (rh * S::kMBQ + mb) * 16 + i16] = l;
     }
     wait_lds_barrier();
@@ -477,7 +399,7 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
 #pragma unroll
       for (int k = 1; k < S::kTG; ++k) l_all[mb] += smax[k * S::M + mb * 16 + i16];
     }
-    if (c0 == 0 && n == stages) {
+    if (c0 == 0 && n == t.stages) {
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb) {
         const int row = t.row0 + mb * 16 + i16;
@@ -494,8 +416,8 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
               l_all[mb] == 0.0f ? -kInf : (m_run[mb] + __builtin_amdgcn_logf(l_all[mb])) * 0.69314718f;
       }
     } else {
-      const int64_t at = 2 * w + (c0 == 0 ? 1 : 0);
-      f32x4* to = accs + at * (S::M * DC / 4) + wv * (S::kFB * MB * kWave) + lane;
+      const int64_t at = 2 * un.w + (c0 == 0 ? 1 : 0);
+      f32x4* to = space.acc + at * (S::M * DC / 4) + wv * (S::kFB * MB * kWave) + lane;
 #pragma unroll
       for (int fb = 0; fb < S::kFB; ++fb)
 #pragma unroll
@@ -503,66 +425,28 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
       if (wv == 0 && g == 0) {
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
-          ml[at * 2 * S::M + mb * 16 + i16] = m_run[mb];
-          ml[at * 2 * S::M + S::M + mb * 16 + i16] = l_all[mb];
+          space.ml[at * 2 * S::M + mb * 16 + i16] = m_run[mb];
+          space.ml[at * 2 * S::M + S::M + mb * 16 + i16] = l_all[mb];
         }
       }
-      if (tid == 0) parts[at] = Part{t.s.first, t.row0, t.rows, c0 + n == stages ? 1 : 0};
+      if (tid == 0) space.parts[at] = Part{t.s.first, t.row0, t.rows, c0 == 0 ? un.owner(un.u + t.stages - 1) : 0};
     }
 
     // ---- on to the next request with work, if this one is done
-    u += n;
-    rem += n;
-    if (u < u1 && rem == units) {
-      rem = 0;
-      for (int from = r + 1;; from += kThreads) {
-        wait_lds_barrier();
-        if (tid == 0) misc[0] = a.rq.R;
-        wait_lds_barrier();
-        if (from + tid < a.rq.R && span_of(a.rq, from + tid).tokens > 0) atomicMin(reinterpret_cast<unsigned long long*>(misc), (unsigned long long)(from + tid));
-        wait_lds_barrier();
-        r = __builtin_amdgcn_readfirstlane(int(misc[0]));
-        if (r < a.rq.R || from + kThreads >= a.rq.R) break;
-      }
-      if (r >= a.rq.R) break;  // (cannot be: the units say that there is one)
+    un.u += n;
+    un.rem += n;
+    if (un.u < un.u1 && un.rem == t.units) {
+      un.rem = 0;
+      un.r = next_request<kThreads>(a.rq, un.r, misc);
+      if (un.r >= a.rq.R) break;  // (cannot be: the units say that there is one)
     }
   }
 }
 
-// Adds the parts of the tile that begins in workgroup blockIdx.x's last segment, if others finish it.  A wave takes 16 features of 16 rows.
 template <int DC, int MB>
-__global__ __launch_bounds__(kWave) void k_absorbed_join(AbsorbedArgs a, int G) {
-  using S = Shape<DC, MB>;
-  const Part* parts = reinterpret_cast<const Part*>(a.workspace);
-  const float* ml = reinterpret_cast<const float*>(a.workspace + int64_t(G) * 2 * sizeof(Part));
-  const f32x4* accs = reinterpret_cast<const f32x4*>(a.workspace + int64_t(G) * 2 * (sizeof(Part) + S::kMLB));
-  const int w = blockIdx.x, lane = threadIdx.x, i16 = lane & 15, g = lane >> 4;
-  const Part p = parts[2 * w + 1];
-  if (p.rows == 0) return;
-  const int mb = blockIdx.y % MB, fbw = blockIdx.y / MB, wv = fbw / S::kFB, fb = fbw % S::kFB;
-  const int row = p.row0 + mb * 16 + i16;
-  int end = w + 1;  // the part that ends the tile
-  while (end < G - 1 && !(parts[2 * end].rows != 0 && parts[2 * end].last)) ++end;
-  float m = ml[(2 * w + 1) * 2 * S::M + mb * 16 + i16];
-  for (int k = w + 1; k <= end; ++k) m = fmaxf(m, ml[int64_t(2 * k) * 2 * S::M + mb * 16 + i16]);
-  const float ref = m == -kInf ? 0.0f : m;
-  float l = 0.0f;
-  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-  for (int k = w; k <= end; ++k) {
-    const int64_t at = k == w ? 2 * w + 1 : 2 * k;
-    const float f = __builtin_amdgcn_exp2f(ml[at * 2 * S::M + mb * 16 + i16] - ref);
-    l += f * ml[at * 2 * S::M + S::M + mb * 16 + i16];
-    acc += f * accs[at * (S::M * DC / 4) + (wv * S::kFB * MB + fb * MB + mb) * kWave + lane];
-  }
-  if (row >= p.rows) return;
-  const int tok = row / a.heads, head = row - tok * a.heads;
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  acc *= inv;
-  *reinterpret_cast<u32x2*>(a.out + (p.first + tok) * a.out_stride + int64_t(head) * DC + wv * (DC / 4) + fb * 16 + 4 * g) =
-      u32x2{pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3])};
-  if (a.lse != nullptr && fbw == 0 && g == 0)
-    a.lse[int64_t(p.first + tok) * a.heads + head] = l == 0.0f ? -kInf : (m + __builtin_amdgcn_logf(l)) * 0.69314718f;
+__global__ __launch_bounds__(kThreads) void k_absorbed_join(AbsorbedArgs a, int G) {
+  constexpr int kFB = DC / 64;  // of a wave's quarter
+  join_parts<DC, 16 * MB>(a, G, [](int blk, int fb) { return (fb / kFB * kFB + fb % kFB) * MB + blk; });
 }
 
 template <int DC, int MB, bool FP8>
@@ -573,7 +457,7 @@ hipError_t run(const AbsorbedArgs& a, int G, hipStream_t stream) {
                                            hipFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
   if (e != hipSuccess) return e;
   k_absorbed<DC, MB, FP8><<<dim3(G), dim3(kThreads), S::kBytes, stream>>>(a);
-  k_absorbed_join<DC, MB><<<dim3(G, 4 * S::kFB * MB), dim3(kWave), 0, stream>>>(a, G);
+  k_absorbed_join<DC, MB><<<dim3(4 * G), dim3(kThreads), 0, stream>>>(a, G);
   return hipGetLastError();
 }
 
@@ -586,19 +470,21 @@ template <int DC>
 hipError_t run(const AbsorbedArgs& a, int cus, hipStream_t stream) {
   const int G = DC == 128 ? 2 * cus : cus;
   // rows of a request: its tokens (the step's share of one) times the heads
-  int64_t tokens = (a.rq.n_tokens + a.rq.R - 1) / a.rq.R;
+  int64_t tokens = (a.rq.n_tokens + a.rq.R / 2) / a.rq.R;
+  if (tokens < 1) tokens = 1;
   if (a.rq.max_tokens > 0 && tokens > a.rq.max_tokens) tokens = a.rq.max_tokens;
   const int64_t rows = tokens * a.heads;
   if (rows <= 16) return run<DC, 1>(a, G, stream);
   if (rows <= 32) return run<DC, 2>(a, G, stream);
-  return run<DC, 4>(a, G, stream);
+  if (getenv("EXP") && atoi(getenv("EXP")) == 4) return run<DC, 4>(a, G, stream);
+  if (getenv("EXP") && atoi(getenv("EXP")) == 1) return launch_absorbed_rows(a, G, false, stream);
+  return launch_absorbed_rows(a, G, rows > 64, stream);
 }
 
 }  // namespace
 
 int64_t absorbed_workspace_bytes(int latent_dim, int cus) {
-  const int G = latent_dim == 128 ? 2 * cus : cus;
-  return int64_t(G) * 2 * (int64_t(sizeof(Part)) + 64 * 8 + int64_t(64) * latent_dim * 4);
+  return part_space_bytes(latent_dim == 128 ? 2 * cus : cus, 128, latent_dim);
 }
 
 hipError_t launch_latent_absorbed(const AbsorbedArgs& a, int cus, hipStream_t stream) {

@@ -1,0 +1,544 @@
+// Absorbed latent attention for many rows a request (tokens times heads): tiles of M = 64 RB rows.
+//
+// Each of the four waves takes 16 RB rows of the tile and all of the latent: its queries and its accumulators
+// (512 features: 144 and 256 registers a lane at RB 2) stay in registers, and a stage of 32 positions goes through
+// LDS as bf16, read twice by every wave: along the features for the scores, transposed for the values.
+// S^T = C Q^T leaves a lane with 4 consecutive positions of one query, which is an operand of out^T += C^T P^T
+// as it stands if that product counts its positions in the same order; so weights, maxima and sums never leave a wave.
+// (latent_absorbed.hip has the form for few rows, where the waves share the latent instead.)
+//
+// FP8 rows are copied to LDS as they are, three stages ahead, and converted one stage ahead by the lanes that
+// copied them; BF16 rows are copied two stages ahead to where they are read.
+//
+// What bounds it: LDS reads and the matrix units about equally (a wave's 32 queries use each 16 bytes that it reads
+// for 2 MFMAs of 16 cycles; four waves read 128 bytes a cycle).
+#include "latent_units.h"
+
+namespace engram {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTB = 32;  // positions per stage
+constexpr int kRing = 8;      // stages whose pages are kept
+constexpr int kSlotRing = 4;  // and the places of their rows
+
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Scores of two blocks of positions (k0, k1) and two of queries (q0, q1): s += k q^T.  In assembly, for the results to lie
+// in vector registers: the compiler keeps every MFMA's result of a kernel in accumulation registers, and at 512
+// features the 256 of them hold the outputs.  The first wait covers operands that a vector instruction wrote last.
+__device__ __forceinline__ void first_scores(f32x4 (&s)[2][2], u32x4 k0, u32x4 k1, u32x4 q0, u32x4 q1) {
+  asm("s_nop 1\n\t"
+      "v_mfma_f32_16x16x32_bf16 %0, %4, %6, 0\n\t"
+      "v_mfma_f32_16x16x32_bf16 %1, %4, %7, 0\n\t"
+      "v_mfma_f32_16x16x32_bf16 %2, %5, %6, 0\n\t"
+      "v_mfma_f32_16x16x32_bf16 %3, %5, %7, 0"
+      : "=&v"(s[0][0]), "=&v"(s[0][1]), "=&v"(s[1][0]), "=&v"(s[1][1])
+      : "v"(k0), "v"(k1), "v"(q0), "v"(q1));
+}
+__device__ __forceinline__ void add_scores(f32x4 (&s)[2][2], u32x4 k0, u32x4 k1, u32x4 q0, u32x4 q1) {
+  asm("s_nop 1\n\t"
+      "v_mfma_f32_16x16x32_bf16 %0, %4, %6, %0\n\t"
+      "v_mfma_f32_16x16x32_bf16 %1, %4, %7, %1\n\t"
+      "v_mfma_f32_16x16x32_bf16 %2, %5, %6, %2\n\t"
+      "v_mfma_f32_16x16x32_bf16 %3, %5, %7, %3"
+      : "+v"(s[0][0]), "+v"(s[0][1]), "+v"(s[1][0]), "+v"(s[1][1])
+      : "v"(k0), "v"(k1), "v"(q0), "v"(q1));
+}
+// Before a vector instruction reads them: an MFMA of 16 passes takes 19 wait states, these have fewer.
+__device__ __forceinline__ void finish_scores(f32x4 (&s)[2][2]) {
+  asm("s_nop 15\n\ts_nop 4" : "+v"(s[0][0]), "+v"(s[0][1]), "+v"(s[1][0]), "+v"(s[1][1]));
+}
+
+// What is seldom done to the accumulators (scaling them, adding a single row) is done in memory, in the part of the
+// workspace that the segment may write: touched by vector instructions anywhere in the loop over the stages, copies
+// of them all would be kept around it.  One store or load of 16 bytes a lane for each block; the stores take
+// them from accumulation registers, behind the waits that an MFMA's results need.
+template <int N, int RB>
+__device__ __forceinline__ void acc_to_memory(const f32x4 (&acc)[N][RB], char* to) {
+  asm volatile("s_nop 15\n\ts_nop 4" ::: "memory");
+#pragma unroll
+  for (int mb = 0; mb < RB; ++mb)
+#pragma unroll
+    for (int fb = 0; fb < N; ++fb) {
+      asm volatile("global_store_dwordx4 %0, %1, off" ::"v"(to), "a"(acc[fb][mb]) : "memory");
+      to += kWave * 16;
+    }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+template <int N, int RB>
+__device__ __forceinline__ void acc_from_memory(f32x4 (&acc)[N][RB], const char* from) {
+  asm volatile("" : "+v"(from)::"memory");
+#pragma unroll
+  for (int mb = 0; mb < RB; ++mb)
+#pragma unroll
+    for (int fb = 0; fb < N; ++fb) {
+      acc[fb][mb] = *reinterpret_cast<const f32x4*>(from);
+      from += kWave * 16;
+    }
+}
+
+template <int DC, int RB, bool FP8>
+struct Shape {
+  static constexpr int M = 64 * RB;
+  static constexpr int kChunks = (DC + 64) / 8, kRowB = kChunks * 16;  // of a row in LDS
+  static constexpr int kKB = DC / 32, kFB = DC / 16;
+  static constexpr int kStageB = kTB * kRowB;
+  static constexpr int kBufs = FP8 ? 2 : 3;
+  // FP8 rows as they are in the cache: codes, rope parts, and the scales once for each wave
+  static constexpr int kCodeB = kTB * DC, kRopeB = kTB * 128, kRawB = kCodeB + kRopeB + 4 * 1024, kRaws = 3;
+  static constexpr int kCodeCopies = kCodeB / 16 / kThreads;
+  static constexpr int kCopies = FP8 ? kCodeCopies + 2 : kTB * kChunks / kThreads;  // of a thread and stage
+  static constexpr int kRaw = kBufs * kStageB;  // offsets into LDS
+  // each wave's own: the pages of some stages' positions, where the rows lie, and which of them take part
+  static constexpr int kPages = kRaw + (FP8 ? kRaws * kRawB : 0);
+  static constexpr int kSlots = kPages + 4 * kRing * 256;
+  static constexpr int kAlive = kSlots + 4 * kSlotRing * kTB * 8;
+  static constexpr int kMisc = kAlive + 4 * kRing * 4;
+  static constexpr int kBytes = kMisc + 64;
+  static constexpr int kPerCU = 2 * kBytes <= 160 * 1024 ? 2 : 1;
+};
+
+template <int DC, int RB, bool FP8>
+__global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed_rows(AbsorbedArgs a) {
+  using S = Shape<DC, RB, FP8>;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int i16 = lane & 15, g = lane >> 4;
+  const int rkb = a.rope_dim / 32;
+  const int row_b = latent_row_bytes(DC, a.rope_dim, FP8);
+  int32_t* pages = reinterpret_cast<int32_t*>(lds + S::kPages) + wv * kRing * 64;
+  int64_t* slots = reinterpret_cast<int64_t*>(lds + S::kSlots) + wv * kSlotRing * kTB;
+  uint32_t* alive = reinterpret_cast<uint32_t*>(lds + S::kAlive) + wv * kRing;
+  int64_t* misc = reinterpret_cast<int64_t*>(lds + S::kMisc);
+  const PartSpace space = part_space(a.workspace, gridDim.x, S::M);
+  Units un;
+  if (!my_units<kThreads, S::M, kTB>(a.rq, a.heads, space.parts, misc, &un)) return;
+
+  // A chunk's place differs from row to row in the low three bits of its number only, so the reads of a stage take
+  // two (keys) and four (values) addresses and constants.  (Rows start at multiples of 128 bytes.)
+  const int key_at = i16 * S::kRowB + (g ^ latent_swizzle(i16)) * 16;
+  const int vrow = 4 * g + (i16 >> 2);
+  const int value_at = vrow * S::kRowB + (((i16 & 3) >> 1) ^ latent_swizzle(vrow)) * 16 + (i16 & 1) * 8;
+
+  while (un.u < un.u1) {
+    const Segment t = segment_of<S::M, kTB>(a.rq, a.heads, un);
+    const int c0 = t.c0, n = t.n;
+    const int w0 = t.row0 + wv * 16 * RB;  // the wave's first row
+
+    // ---- queries, and the position of each row's token (-1: no row)
+    u32x4 qf[RB][S::kKB + 2];
+    int qpos[RB];
+#pragma unroll
+    for (int mb = 0; mb < RB; ++mb) {
+      const int row = w0 + mb * 16 + i16, at = row < t.rows ? row : t.rows - 1;  // (rows past the last repeat it)
+      const int tok = at / a.heads, head = at - tok * a.heads;
+      qpos[mb] = row < t.rows ? t.s.pos + tok : -1;
+      const uint16_t* src = a.q + (t.s.first + tok) * a.q_stride + int64_t(head) * (DC + a.rope_dim) + 8 * g;
+#pragma unroll
+      for (int kb = 0; kb < S::kKB + 2; ++kb)
+        qf[mb][kb] = *reinterpret_cast<const u32x4*>(src + 32 * (kb < S::kKB + rkb ? kb : 0)) ^ a.q_sign;
+    }
+    f32x4 acc[S::kFB][RB];
+    float m_run[RB], l_own[RB];
+#pragma unroll
+    for (int mb = 0; mb < RB; ++mb) {
+      m_run[mb] = -kInf;
+      l_own[mb] = 0.0f;
+#pragma unroll
+      for (int fb = 0; fb < S::kFB; ++fb) acc[fb][mb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    const bool whole = c0 == 0 && n == t.stages;
+    const int64_t part_at = 2 * un.w + (c0 == 0 ? 1 : 0);  // (a whole tile's segment comes before the one that leaves this part)
+
+    auto acc_memory = [&]() {
+      uint32_t off = (wv * RB * S::kFB * kWave + lane) * 16;
+      asm volatile("" : "+v"(off));  // (made where it is used)
+      return reinterpret_cast<char*>(space.acc + part_at * (S::M * DC / 4)) + off;
+    };
+
+    // ---- staging
+    // (What these compute from the lane's number is made where it is used: kept around the loop it would take the
+    // registers that the queries and accumulators leave, and go through memory.)
+    auto fresh = [&]() {
+      int l = lane;
+      asm volatile("" : "+v"(l));
+      return l;
+    };
+    // Lane l < 32 looks after row l of a stage: its page is copied to LDS two stages before its slot is made (by a copy,
+    // like the rows: a load into a register would have to wait for all the copies before it), which is when its
+    // row is copied.  Every wave does so for itself.
+    const int32_t* table = a.rq.block_table + int64_t(un.r) * a.rq.max_blocks;
+    auto copy_pages = [&](int c) {
+      const int lane = fresh();
+      int pos = t.base + c * kTB + (lane & 31);
+      pos = pos < t.hi ? pos : t.hi - 1;  // (stages past the last: any page)
+      __builtin_amdgcn_global_load_lds((const void*)(table + a.rq.page_of(pos)), (lds_ptr_t)(pages + (c & (kRing - 1)) * 64), 4, 0, 0);
+    };
+    auto make_slots = [&](int c) {
+      const int lane = fresh();
+      const int pos = t.base + c * kTB + (lane & 31), page = pages[(c & (kRing - 1)) * 64 + (lane & 31)];
+      const bool in = c < c0 + n && pos >= t.lo && pos < t.hi, good = page >= 0 && page < a.rq.n_blocks;
+      const int64_t slot = in && good ? int64_t(page) * a.rq.block_size + (pos - a.rq.page_of(pos) * a.rq.block_size) : -1;
+      if (in && !good && wv == 0 && lane < kTB && t.tile == 0 && a.err_count != nullptr) atomicAdd(a.err_count, 1);
+      if (lane < kTB) slots[(c & (kSlotRing - 1)) * kTB + lane] = (slot < 0 ? 0 : slot) * row_b;
+      const uint32_t on = uint32_t(__ballot(slot >= 0));
+      if (lane == 0) alive[c & (kRing - 1)] = on;
+    };
+    // (rows that take no part are copied from the first slot and cleared later; stages past the last too, so that
+    // every wave has the same number of copies in flight)
+    auto row_offset = [&](int c, int k) -> int64_t {  // of the row of which copy k takes 16 bytes
+      const int lane = fresh(), tid = wv * kWave + lane;
+      const int64_t* sl = slots + (c & (kSlotRing - 1)) * kTB;
+      if constexpr (FP8) {
+        constexpr int kNP = DC / 16;
+        if (k < S::kCodeCopies) return sl[tid / kNP + k * (kThreads / kNP)];
+        if (k == S::kCodeCopies) return sl[rkb == 2 ? tid >> 3 : (tid >> 2) & 31];
+        return sl[lane & 31];
+      } else {
+        return sl[(k * kThreads + tid) / S::kChunks];
+      }
+    };
+    auto copy = [&](int c, int k, int64_t offset) {
+      const int lane = fresh(), tid = wv * kWave + lane;
+      const uint8_t* row = a.cache + offset;
+      if constexpr (FP8) {
+        constexpr int kNP = DC / 16;
+        char* raw = lds + S::kRaw + (c % S::kRaws) * S::kRawB;
+        const int at = k < S::kCodeCopies ? tid % kNP * 16 : (k == S::kCodeCopies ? DC + 16 + (rkb == 2 ? tid & 7 : tid & 3) * 16 : DC);
+        __builtin_amdgcn_global_load_lds((const void*)(row + at), (lds_ptr_t)(raw + (k * 4 + wv) * 1024), 16, 0, 0);
+      } else {
+        const int id = k * kThreads + tid, r = id / S::kChunks;
+        int ch = (id - r * S::kChunks) ^ latent_swizzle(r);
+        ch = ch < DC / 8 + 4 * rkb ? ch : 0;  // (a place that is not read)
+        __builtin_amdgcn_global_load_lds((const void*)(row + ch * 16),
+                                         (lds_ptr_t)(lds + (c % S::kBufs) * S::kStageB + (k * 4 + wv) * 1024), 16, 0, 0);
+      }
+    };
+    auto copy_stage = [&](int c) {
+#pragma unroll
+      for (int k = 0; k < S::kCopies; ++k) copy(c, k, row_offset(c, k));
+    };
+    // FP8: of what the wave's copy k brought (kRows rows of codes; the last one: rope parts), a lane's chunks are first
+    // and first + half a row, so that a wave's writes fill all banks
+    struct Raw {
+      u32x4 v;
+      uint32_t scale0, scale1;
+    };
+    constexpr int kHalf = DC / 16, kRows = 64 / kHalf;
+    auto read_raw = [&](int c, int k) {
+      const int lane = fresh(), tid = wv * kWave + lane;
+      const char* raw = lds + S::kRaw + (c % S::kRaws) * S::kRawB;
+      Raw r = {};
+      if (k == S::kCodeCopies) {
+        r.v = *reinterpret_cast<const u32x4*>(raw + (k * kThreads + tid) * 16);
+      } else {
+        const int row = (k * 4 + wv) * kRows + lane / kHalf, ch = lane % kHalf;
+        const u32x2 lo = *reinterpret_cast<const u32x2*>(raw + row * DC + ch * 8), hi = *reinterpret_cast<const u32x2*>(raw + row * DC + (ch + kHalf) * 8);
+        const uint8_t* sc = reinterpret_cast<const uint8_t*>(raw + S::kCodeB + S::kRopeB + wv * 1024 + row * 16);
+        r.v = u32x4{lo.x, lo.y, hi.x, hi.y};
+        r.scale0 = sc[ch / 4];
+        r.scale1 = sc[(ch + kHalf) / 4];
+      }
+      return r;
+    };
+    auto convert = [&](int c, int k, const Raw& r) {
+      const int lane = fresh(), tid = wv * kWave + lane;
+      const uint32_t on = __builtin_amdgcn_readfirstlane(alive[c & (kRing - 1)]);
+      char* buf = lds + (c & 1) * S::kStageB;
+      const u32x4 none = {0u, 0u, 0u, 0u};
+      if (k == S::kCodeCopies) {
+        const int rp = rkb == 2 ? tid & 7 : tid & 3, row = rkb == 2 ? tid >> 3 : (tid >> 2) & 31;
+        *reinterpret_cast<u32x4*>(buf + row * S::kRowB + ((DC / 8 + rp) ^ latent_swizzle(row)) * 16) = r.v;  // (only scores read it)
+      } else {
+        const int row = (k * 4 + wv) * kRows + lane / kHalf, ch = lane % kHalf;
+        u32x4 o0, o1;
+        latent8x2(r.v, r.scale0, r.scale1, o0, o1);
+        if (__builtin_expect(on != ~0u, 0))
+          if (!((on >> row) & 1)) o0 = o1 = none;
+        char* to = buf + row * S::kRowB + (ch ^ latent_swizzle(row)) * 16;
+        *reinterpret_cast<u32x4*>(to) = o0;
+        *reinterpret_cast<u32x4*>(to + kHalf * 16) = o1;  // (a multiple of 8 chunks further)
+      }
+    };
+    auto clear_dead = [&](int c) {  // BF16: of what this lane copied
+      const uint32_t on = alive[c & (kRing - 1)];
+      if (on == ~0u) return;
+      char* buf = lds + (c % S::kBufs) * S::kStageB;
+#pragma unroll 1
+      for (int k = 0; k < S::kCopies; ++k) {
+        const int id = k * kThreads + tid;
+        if (!((on >> (id / S::kChunks)) & 1)) *reinterpret_cast<u32x4*>(buf + id * 16) = u32x4{0u, 0u, 0u, 0u};
+      }
+    };
+
+    constexpr int kCopyStage = FP8 ? 3 : 2;  // stages that rows are copied ahead
+    wait_all_barrier();  // nobody reads LDS or copies into it any more
+#pragma unroll
+    for (int k = 0; k < kCopyStage; ++k) copy_pages(c0 + k);
+    wait_copies<0>();
+#pragma unroll
+    for (int k = 0; k < kCopyStage; ++k) {
+      make_slots(c0 + k);
+      copy_stage(c0 + k);
+      if (k >= kCopyStage - 2) copy_pages(c0 + k + 2);
+    }
+    if constexpr (FP8) {
+      wait_copies<2 * S::kCopies + 2>();
+#pragma unroll
+      for (int k = 0; k <= S::kCodeCopies; ++k) convert(c0, k, read_raw(c0, k));
+    }
+
+    for (int j = 0; j < n; ++j) {
+      const int c = c0 + j;
+      wait_copies<S::kCopies + 1>();  // FP8: of stage c + 1, BF16: of stage c, are there, and the pages of stage c + kCopyStage
+      if constexpr (!FP8) clear_dead(c);
+      wait_lds_barrier();
+      make_slots(c + kCopyStage);
+      char* buf = lds + (FP8 ? (c & 1) : c % S::kBufs) * S::kStageB;
+
+      f32x4 s[2][RB];
+      u32x4 p[RB];
+      const uint32_t on = __builtin_amdgcn_readfirstlane(alive[c & (kRing - 1)]);
+      const int j0 = t.base + c * kTB;
+      const bool differ = t.p_min != t.p_max && (j0 + kTB - 1 > t.p_min || (a.rq.window > 0 && j0 <= t.p_max - a.rq.window));
+      {
+        // ---- scores, and (FP8) the next stage's conversion between them
+        const char* kp[2] = {buf + key_at, buf + (key_at ^ 64)};
+        auto key = [&](int kb, int tb) { return *reinterpret_cast<const u32x4*>(kp[kb & 1] + tb * 16 * S::kRowB + (kb >> 1) * 128); };
+        constexpr int kDeep = RB == 2 ? 3 : 5;
+        u32x4 kf[kDeep][2];
+#pragma unroll
+        for (int kb = 0; kb < kDeep - 1; ++kb) {
+          kf[kb][0] = key(kb, 0);
+          kf[kb][1] = key(kb, 1);
+        }
+        if constexpr (RB == 1) s[0][0] = s[1][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        constexpr int kSteps = S::kKB + 2;
+        int64_t from;
+        // beside each step's products: the keys of a later step, and a row copied (its place read a step before)
+        auto side = [&](int kb) {
+          if (kb >= 1 && kb - 1 < S::kCopies) copy(c + kCopyStage, kb - 1, from);
+          if (kb < S::kCopies) from = row_offset(c + kCopyStage, kb);
+        };
+#pragma unroll
+        for (int kb = 0; kb < kSteps; ++kb) {
+          if (kb + kDeep - 1 < kSteps) {
+            kf[(kb + kDeep - 1) % kDeep][0] = key(kb + kDeep - 1, 0);
+            kf[(kb + kDeep - 1) % kDeep][1] = key(kb + kDeep - 1, 1);
+          }
+          side(kb);
+          if (kb < S::kKB + 1 || rkb == 2) {
+            if constexpr (RB == 2) {
+              if (kb == 0) first_scores(s, kf[0][0], kf[0][1], qf[0][0], qf[1][0]);
+              else add_scores(s, kf[kb % kDeep][0], kf[kb % kDeep][1], qf[0][kb], qf[1][kb]);
+            } else {
+#pragma unroll
+              for (int tb = 0; tb < 2; ++tb) s[tb][0] = mfma16x16x32(kf[kb % kDeep][tb], qf[0][kb], s[tb][0]);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int kb = kSteps; kb < S::kCopies + 1; ++kb) side(kb);  // what small latents leave
+        if constexpr (RB == 2) finish_scores(s);
+      }
+      copy_pages(c + kCopyStage + 2);
+
+      // ---- softmax
+      if (on != ~0u || differ) {
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+          for (int mb = 0; mb < RB; ++mb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int row = tb * 16 + 4 * g + e, pos = j0 + row;
+              const bool seen = ((on >> row) & 1) && pos <= qpos[mb] && (a.rq.window <= 0 || pos > qpos[mb] - a.rq.window);
+              s[tb][mb][e] = seen ? s[tb][mb][e] : -kInf;
+            }
+      }
+      float m_new[RB];
+      bool grow = false;
+#pragma unroll
+      for (int mb = 0; mb < RB; ++mb) {
+        float m = fmaxf(fmaxf(fmaxf(s[0][mb][0], s[0][mb][1]), fmaxf(s[0][mb][2], s[0][mb][3])),
+                        fmaxf(fmaxf(s[1][mb][0], s[1][mb][1]), fmaxf(s[1][mb][2], s[1][mb][3])));
+        m_new[mb] = quad_max(m) * a.scale_log2;  // (the scale is positive: its sign is in the queries)
+        if (m_run[mb] == -kInf) m_run[mb] = m_new[mb];  // (nothing is summed yet)
+        grow |= m_new[mb] > m_run[mb] + kGrow;
+      }
+      if (__any(grow)) {
+        char* mem = acc_memory();
+        acc_to_memory(acc, mem);
+#pragma unroll
+        for (int mb = 0; mb < RB; ++mb) {
+          const float m = fmaxf(m_run[mb], m_new[mb]);
+          const float alpha = m == -kInf ? 1.0f : __builtin_amdgcn_exp2f(m_run[mb] - m);
+          m_run[mb] = m;
+          l_own[mb] *= alpha;
+#pragma unroll 4
+          for (int fb = 0; fb < S::kFB; ++fb) *reinterpret_cast<f32x4*>(mem + (mb * S::kFB + fb) * (kWave * 16)) *= alpha;
+        }
+        acc_from_memory(acc, mem);
+      }
+#pragma unroll
+      for (int mb = 0; mb < RB; ++mb) {
+        const float ref = m_run[mb] == -kInf ? 0.0f : m_run[mb];
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[tb][mb][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[tb][mb][e], a.scale_log2, -ref));
+            l_own[mb] += s[tb][mb][e];
+          }
+          p[mb][2 * tb] = pack_bf16x2(s[tb][mb][0], s[tb][mb][1]);
+          p[mb][2 * tb + 1] = pack_bf16x2(s[tb][mb][2], s[tb][mb][3]);
+        }
+      }
+
+      // ---- values that are not finite, where the tile's tokens see different positions: added row by row where they are
+      // seen, and zeros for the product
+      if (differ) {
+        uint32_t odd = 0;
+#pragma unroll 1
+        for (int k = tid; k < kTB * DC / 8; k += kThreads) {
+          const int row = k / (DC / 8);
+          const u32x4 v = *reinterpret_cast<const u32x4*>(buf + row * S::kRowB + k % (DC / 8) * 16);
+          if (any_not_finite(v)) odd |= 1u << row;
+        }
+        odd = any_rows(odd, misc);
+        if (__builtin_expect(odd != 0, 0)) {
+          char* mem = acc_memory();
+          acc_to_memory(acc, mem);
+#pragma unroll 1
+          for (uint32_t left = odd; left != 0; left &= left - 1) {
+            const int row = __builtin_ctz(left), pos = j0 + row;
+#pragma unroll
+            for (int mb = 0; mb < RB; ++mb) {
+              float w = 0.0f;
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                if ((row >> 4) * 4 + (row & 3) == k) w = s[k >> 2][mb][k & 3];
+              w = __shfl(w, ((row >> 2) & 3) * 16 + i16, kWave);
+              if (!((on >> row) & 1) || pos > qpos[mb] || (a.rq.window > 0 && pos <= qpos[mb] - a.rq.window)) continue;
+#pragma unroll 1
+              for (int fb = 0; fb < S::kFB; ++fb) {
+                const u32x2 v = *reinterpret_cast<const u32x2*>(buf + row * S::kRowB + ((fb * 2 + (g >> 1)) ^ latent_swizzle(row)) * 16 + (g & 1) * 8);
+                f32x4* to = reinterpret_cast<f32x4*>(mem + (mb * S::kFB + fb) * (kWave * 16));
+                *to += f32x4{w * bf16_lo(v.x), w * bf16_hi(v.x), w * bf16_lo(v.y), w * bf16_hi(v.y)};
+              }
+            }
+          }
+          acc_from_memory(acc, mem);
+          wait_lds_barrier();
+          for (int k = tid; k < kTB * DC / 8; k += kThreads)
+            if ((odd >> (k / (DC / 8))) & 1)
+              *reinterpret_cast<u32x4*>(buf + k / (DC / 8) * S::kRowB + k % (DC / 8) * 16) = u32x4{0u, 0u, 0u, 0u};
+          wait_lds_barrier();
+        }
+      }
+
+      // ---- values
+      const char* vp[4] = {buf + value_at, buf + (value_at ^ 32), buf + (value_at ^ 64), buf + (value_at ^ 96)};
+      auto value = [&](int fb) {
+        const char* at = vp[fb & 3] + (fb >> 2) * 128;
+        const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)at));
+        const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(at + 16 * S::kRowB)));
+        return u32x4{lo.x, lo.y, hi.x, hi.y};
+      };
+      Raw raw;
+      constexpr int kDeep = 6;
+      u32x4 vf[kDeep];
+#pragma unroll
+      for (int fb = 0; fb < kDeep - 1; ++fb) vf[fb] = value(fb);
+#pragma unroll
+      for (int fb = 0; fb < S::kFB; ++fb) {
+        if (fb + kDeep - 1 < S::kFB) vf[(fb + kDeep - 1) % kDeep] = value(fb + kDeep - 1);
+        if constexpr (FP8) {  // and beside them the next stage's conversion
+          constexpr int kEvery = S::kFB / (S::kCodeCopies + 1);
+          if (fb % kEvery == kEvery - 1 && fb / kEvery <= S::kCodeCopies) convert(c + 1, fb / kEvery, raw);
+          if (fb % kEvery == 0 && fb / kEvery <= S::kCodeCopies) raw = read_raw(c + 1, fb / kEvery);
+        }
+#pragma unroll
+        for (int mb = 0; mb < RB; ++mb) acc[fb][mb] = mfma16x16x32(vf[fb % kDeep], p[mb], acc[fb][mb]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+
+    // ---- the outputs, or a part
+#pragma unroll
+    for (int mb = 0; mb < RB; ++mb) {
+      const float l = quad_sum(l_own[mb]);
+      const int row = w0 + mb * 16 + i16;
+      if (whole) {
+        if (row >= t.rows) continue;
+        const int tok = row / a.heads, head = row - tok * a.heads;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        uint16_t* out = a.out + (t.s.first + tok) * a.out_stride + int64_t(head) * DC + 4 * g;
+#pragma unroll
+        for (int fb = 0; fb < S::kFB; ++fb)
+          *reinterpret_cast<u32x2*>(out + fb * 16) = u32x2{pack_bf16x2(acc[fb][mb][0] * inv, acc[fb][mb][1] * inv),
+                                                           pack_bf16x2(acc[fb][mb][2] * inv, acc[fb][mb][3] * inv)};
+        if (a.lse != nullptr && g == 0)
+          a.lse[int64_t(t.s.first + tok) * a.heads + head] =
+              l == 0.0f ? -kInf : (m_run[mb] + __builtin_amdgcn_logf(l)) * 0.69314718f;
+      } else {
+        f32x4* to = space.acc + part_at * (S::M * DC / 4) + (wv * RB + mb) * (S::kFB * kWave) + lane;
+#pragma unroll
+        for (int fb = 0; fb < S::kFB; ++fb) to[fb * kWave] = acc[fb][mb];
+        if (g == 0) {
+          space.ml[part_at * 2 * S::M + (wv * RB + mb) * 16 + i16] = m_run[mb];
+          space.ml[part_at * 2 * S::M + S::M + (wv * RB + mb) * 16 + i16] = l;
+        }
+      }
+    }
+    if (!whole && tid == 0) space.parts[part_at] = Part{t.s.first, t.row0, t.rows, c0 == 0 ? un.owner(un.u + t.stages - 1) : 0};
+
+    un.u += n;
+    un.rem += n;
+    if (un.u < un.u1 && un.rem == t.units) {
+      un.rem = 0;
+      un.r = next_request<kThreads>(a.rq, un.r, misc);
+      if (un.r >= a.rq.R) break;  // (cannot be: the units say that there is one)
+    }
+  }
+}
+
+template <int DC, int M>
+__global__ __launch_bounds__(kThreads) void k_absorbed_rows_join(AbsorbedArgs a, int G) {
+  join_parts<DC, M>(a, G, [](int blk, int fb) { return blk * (DC / 16) + fb; });
+}
+
+template <int DC, int RB, bool FP8>
+hipError_t run(const AbsorbedArgs& a, int G, hipStream_t stream) {
+  using S = Shape<DC, RB, FP8>;
+  static_assert(S::kBytes <= 160 * 1024, "LDS of a CU");
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_absorbed_rows<DC, RB, FP8>),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+  if (e != hipSuccess) return e;
+  k_absorbed_rows<DC, RB, FP8><<<dim3(G), dim3(kThreads), S::kBytes, stream>>>(a);
+  k_absorbed_rows_join<DC, S::M><<<dim3(4 * G), dim3(kThreads), 0, stream>>>(a, G);
+  return hipGetLastError();
+}
+
+template <int DC>
+hipError_t run(const AbsorbedArgs& a, int G, bool wide, hipStream_t stream) {
+  if (wide) return a.fp8 ? run<DC, 2, true>(a, G, stream) : run<DC, 2, false>(a, G, stream);
+  return a.fp8 ? run<DC, 1, true>(a, G, stream) : run<DC, 1, false>(a, G, stream);
+}
+
+}  // namespace
+
+hipError_t launch_absorbed_rows(const AbsorbedArgs& a, int G, bool wide, hipStream_t stream) {
+  if (a.latent_dim == 128) return run<128>(a, G, wide, stream);
+  if (a.latent_dim == 256) return run<256>(a, G, wide, stream);
+  return run<512>(a, G, wide, stream);
+}
+
+}  // namespace engram

@@ -36,8 +36,7 @@ engram_status requests(const engram_latent_layout* l, const int32_t* token_start
   q->R = int(R);
   q->n_tokens = int(n_tokens);
   q->min_tokens = 1;
-  q->block_size = 1 << 30;  // (without pages: positions below 2^30)
-  q->max_blocks = 1;
+  q->set_pages(1 << 30, 1, 0);  // (without pages: positions below 2^30)
   q->window = l->window < (1 << 30) ? l->window : 1 << 30;  // (no position lies further back)
   return ENGRAM_OK;
 }
@@ -46,9 +45,7 @@ engram_status pages_of(const engram_page_layout* p, const int32_t* block_table, 
   if (q->R > 0 && !block_table) return ENGRAM_E_NULL;
   if (!aligned(block_table, 4)) return ENGRAM_E_ALIGN;
   q->block_table = block_table;
-  q->block_size = p->block_size;
-  q->max_blocks = p->max_blocks;
-  q->n_blocks = int(p->n_blocks);
+  q->set_pages(p->block_size, p->max_blocks, p->n_blocks);
   return ENGRAM_OK;
 }
 
@@ -176,7 +173,8 @@ engram_status engram_latent_attention(const engram_latent_layout* l, const engra
   a.err_count = err_count;
   a.q_stride = q_stride;
   a.out_stride = out_stride;
-  a.scale_log2 = l->scale * kLog2e;
+  a.scale_log2 = fmaxf(fabsf(l->scale) * kLog2e, 1e-44f);
+  a.q_sign = l->scale < 0.0f ? 0x80008000u : 0u;
   a.heads = l->heads;
   a.latent_dim = l->latent_dim;
   a.rope_dim = l->rope_dim;
@@ -233,7 +231,8 @@ engram_status engram_latent_attention_expanded(const engram_latent_layout* l, co
   a.rope_stride = rope_stride;
   a.out_stride = out_stride;
   a.n_rows = int(n_rows);
-  a.scale_log2 = l->scale * kLog2e;
+  a.scale_log2 = fmaxf(fabsf(l->scale) * kLog2e, 1e-44f);
+  a.q_sign = l->scale < 0.0f ? 0x80008000u : 0u;
   a.heads = l->heads;
   a.head_dim = l->head_dim;
   a.rope_dim = l->rope_dim;

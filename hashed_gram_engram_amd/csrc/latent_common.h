@@ -31,7 +31,7 @@ __device__ __forceinline__ Span span_of(const LatentRequests& q, int r) {
 
 // The slot of a request's position; -1 where its page is outside the pool.
 __device__ __forceinline__ int64_t slot_of(const LatentRequests& q, int r, int pos) {
-  const int b = pos / q.block_size;
+  const int b = q.page_of(pos);
   const int page = q.block_table[int64_t(r) * q.max_blocks + b];
   return page >= 0 && page < q.n_blocks ? int64_t(page) * q.block_size + (pos - b * q.block_size) : -1;
 }
@@ -47,6 +47,20 @@ __device__ __forceinline__ void latent16(u32x4 c, uint32_t scale, u32x4& o0, u32
   o0 = u32x4{scaled_pair(c.x, s, false), scaled_pair(c.x, s, true), scaled_pair(c.y, s, false), scaled_pair(c.y, s, true)};
   o1 = u32x4{scaled_pair(c.z, s, false), scaled_pair(c.z, s, true), scaled_pair(c.w, s, false), scaled_pair(c.w, s, true)};
   if (__builtin_expect(scale == 0u || scale == 255u, 0)) dequant16(c, e8m0_to_f32(scale), o0, o1);
+}
+
+// Eight codes each of two blocks.
+__device__ __forceinline__ void latent8x2(u32x4 c, uint32_t scale0, uint32_t scale1, u32x4& o0, u32x4& o1) {
+  const float s = __uint_as_float(scale0 << 23), t = __uint_as_float(scale1 << 23);
+  o0 = u32x4{scaled_pair(c.x, s, false), scaled_pair(c.x, s, true), scaled_pair(c.y, s, false), scaled_pair(c.y, s, true)};
+  o1 = u32x4{scaled_pair(c.z, t, false), scaled_pair(c.z, t, true), scaled_pair(c.w, t, false), scaled_pair(c.w, t, true)};
+  const uint32_t k0 = (scale0 + 1) & 255, k1 = (scale1 + 1) & 255;  // 0 and 255 become 1 and 0
+  if (__builtin_expect(__any((k0 < k1 ? k0 : k1) < 2), 0)) {
+    const float f0 = e8m0_to_f32(scale0), f1 = e8m0_to_f32(scale1);
+    const u32x2 a = dequant4_raw(c.x, f0), b = dequant4_raw(c.y, f0), d = dequant4_raw(c.z, f1), e = dequant4_raw(c.w, f1);
+    o0 = u32x4{a.x, a.y, b.x, b.y};
+    o1 = u32x4{d.x, d.y, e.x, e.y};
+  }
 }
 
 // Running sums over the lanes of a wave, and over the threads of a workgroup of THREADS (tmp: one word per

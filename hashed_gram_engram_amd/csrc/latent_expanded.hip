@@ -13,32 +13,21 @@
 //
 // Rows past the last stay zeros in LDS; where a stage holds a value that is not finite and tokens see different
 // rows of it, the product is taken row by row, only where it is seen (0 times infinity would not be 0).
-#include "latent_common.h"
-#include "serving.h"
+#include "latent_units.h"
 
 namespace engram {
 
 namespace {
 
-typedef __attribute__((address_space(3))) void* lds_ptr_t;
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) s16x4* lds_s16x4_t;
-
 constexpr int kTB = 64;
-constexpr float kGrow = 8.0f;
-constexpr float kInf = __builtin_inff();
-
-__device__ __forceinline__ void wait_all_barrier() {
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-}
 
 template <int HD, int NW, int RB>
 struct Shape {
   static constexpr int kThreads = NW * kWave, M = 16 * RB * NW;
   static constexpr int kKC = (HD + 64) / 8, kVC = HD / 8;  // 16-byte chunks of a key and of a value in LDS
   static constexpr int kKB = (HD + 64) / 32;
+  static constexpr int kKeyTurn = kKC % 16 == 0 ? 4 : 2;   // K blocks that a swizzle moves a chunk among
+  static constexpr int kValueTurn = kVC / 2;                  // 16-feature blocks, the same (8 or 4 pairs of chunks)
   static constexpr int kV = kTB * kKC * 16;                // offset of the values
   static constexpr int kStageB = kTB * (kKC + kVC) * 16;
   static constexpr int kBytes = 2 * kStageB;
@@ -127,16 +116,21 @@ __global__ __launch_bounds__(NW* kWave, NW / 4) void k_expanded(ExpandedArgs a) 
 #pragma unroll
   for (int mb = 0; mb < RB; ++mb) {
     const int tok = (wv * RB + mb) * 16 + i16;
-    const bool on = tok < t.tokens;
+    const bool on = tok < t.tokens;  // (tokens past the last repeat it)
     qrow[mb] = on ? t.s.pos + t.t0 + tok - t.base : -1;
-    const uint16_t* src = a.q + int64_t(t.s.first + t.t0 + (on ? tok : 0)) * a.q_stride + head * (HD + a.rope_dim) + 8 * g;
+    const uint16_t* src = a.q + int64_t(t.s.first + t.t0 + (on ? tok : t.tokens - 1)) * a.q_stride + head * (HD + a.rope_dim) + 8 * g;
 #pragma unroll
-    for (int kb = 0; kb < S::kKB; ++kb)
-      qf[mb][kb] = on && kb < HD / 32 + rkb ? *reinterpret_cast<const u32x4*>(src + 32 * kb) : u32x4{0u, 0u, 0u, 0u};
+    for (int kb = 0; kb < S::kKB; ++kb) qf[mb][kb] = *reinterpret_cast<const u32x4*>(src + 32 * (kb < HD / 32 + rkb ? kb : 0)) ^ a.q_sign;
   }
   // the rows that this wave's tokens see
   const int w0 = wv * RB * 16, wn = t.tokens - w0 < RB * 16 ? t.tokens - w0 : RB * 16;
+  const int t_min = t.s.pos + t.t0 - t.base;  // the last row that the tile's first token sees
   const int w_min = t.s.pos + t.t0 + w0 - t.base, w_max = w_min + wn - 1;  // (wn <= 0: no token)
+
+  // (a chunk's place differs from row to row in the low bits of its number only: addresses are one xor away from these)
+  const int key_at = i16 * S::kKC * 16 + (g ^ key_swizzle<S::kKC>(i16)) * 16;
+  const int vrow = 4 * g + (i16 >> 2);
+  const int value_at = vrow * S::kVC * 16 + (((i16 & 3) >> 1) ^ value_swizzle<S::kVC>(vrow)) * 16 + (i16 & 1) * 8;
 
   f32x4 acc[HD / 16][RB];
   float m_run[RB], l_own[RB];
@@ -187,10 +181,14 @@ __global__ __launch_bounds__(NW* kWave, NW / 4) void k_expanded(ExpandedArgs a) 
     }
     wait_all_barrier();
     if (c + 1 < c1) copy_stage(c + 1, lds + ((c - c0 + 1) & 1) * S::kStageB);
-    if (wn <= 0 || j0 > w_max || (a.rq.window > 0 && j0 + kTB <= w_min - a.rq.window + 1)) continue;  // nothing seen
+    // nothing of it is seen by this wave's tokens; whether the tile's tokens see different rows of it
+    const bool skip = wn <= 0 || j0 > w_max || (a.rq.window > 0 && j0 + kTB <= w_min - a.rq.window + 1);
+    const bool t_differ = t.tokens > 1 && (j0 + kTB - 1 > t_min || (a.rq.window > 0 && j0 <= t_min + t.tokens - 1 - a.rq.window));
 
-    // ---- scores
     f32x4 s[kTB / 16][RB];
+    u32x4 p[kTB / 32][RB];
+    if (!skip) {
+    // ---- scores
 #pragma unroll
     for (int tb = 0; tb < kTB / 16; ++tb)
 #pragma unroll
@@ -198,9 +196,10 @@ __global__ __launch_bounds__(NW* kWave, NW / 4) void k_expanded(ExpandedArgs a) 
 #pragma unroll
     for (int kb = 0; kb < S::kKB; ++kb) {
       if (kb == HD / 32 + 1 && rkb == 1) continue;
+      const char* at = buf + (key_at ^ (kb % S::kKeyTurn * 64)) + kb / S::kKeyTurn * S::kKeyTurn * 64;
 #pragma unroll
       for (int tb = 0; tb < kTB / 16; ++tb) {
-        const u32x4 k = *reinterpret_cast<const u32x4*>(buf + (tb * 16 + i16) * S::kKC * 16 + ((kb * 4 + g) ^ key_swizzle<S::kKC>(i16)) * 16);
+        const u32x4 k = *reinterpret_cast<const u32x4*>(at + tb * 16 * S::kKC * 16);
 #pragma unroll
         for (int mb = 0; mb < RB; ++mb) s[tb][mb] = mfma16x16x32(k, qf[mb][kb], s[tb][mb]);
       }
@@ -233,8 +232,7 @@ __global__ __launch_bounds__(NW* kWave, NW / 4) void k_expanded(ExpandedArgs a) 
       for (int tb = 0; tb < kTB / 16; ++tb)
 #pragma unroll
         for (int e = 0; e < 4; ++e) m = fmaxf(m, s[tb][mb][e]);
-      m = fmaxf(m, __shfl_xor(m, 16, kWave));
-      m = fmaxf(m, __shfl_xor(m, 32, kWave));
+      m = quad_max(m);
       m_new[mb] = m;
       grow |= m > m_run[mb] + kGrow;
     }
@@ -249,7 +247,6 @@ __global__ __launch_bounds__(NW* kWave, NW / 4) void k_expanded(ExpandedArgs a) 
         for (int fb = 0; fb < HD / 16; ++fb) acc[fb][mb] *= alpha;
       }
     }
-    u32x4 p[kTB / 32][RB];
 #pragma unroll
     for (int mb = 0; mb < RB; ++mb) {
       const float ref = m_run[mb] == -kInf ? 0.0f : m_run[mb];
@@ -264,58 +261,63 @@ __global__ __launch_bounds__(NW* kWave, NW / 4) void k_expanded(ExpandedArgs a) 
         p[tb >> 1][mb][(tb & 1) * 2 + 1] = pack_bf16x2(s[tb][mb][2], s[tb][mb][3]);
       }
     }
-    // ---- values
-    const char* vb = buf + S::kV;
-    bool odd = false;
-    if (differ) {
-      for (int k = lane; k < kTB * S::kVC; k += kWave) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(vb + k * 16);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) odd |= (v[e] & 0x7F80u) == 0x7F80u || (v[e] & 0x7F800000u) == 0x7F800000u;
-      }
-      odd = __any(odd);
     }
-    if (__builtin_expect(!odd, 1)) {
-      const int vrow = 4 * g + (i16 >> 2), vsw = value_swizzle<S::kVC>(vrow);
-#pragma unroll
-      for (int ks = 0; ks < kTB / 32; ++ks)
-#pragma unroll
-        for (int fb = 0; fb < HD / 16; ++fb) {
-          const char* at = vb + (ks * 32 + vrow) * S::kVC * 16 + ((fb * 2 + ((i16 & 3) >> 1)) ^ vsw) * 16 + (i16 & 1) * 8;
-          const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)at));
-          const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(at + 16 * S::kVC * 16)));
-          const u32x4 v = {lo.x, lo.y, hi.x, hi.y};
-#pragma unroll
-          for (int mb = 0; mb < RB; ++mb) acc[fb][mb] = mfma16x16x32(v, p[ks][mb], acc[fb][mb]);
-        }
-    } else {
+    // ---- values that are not finite, where the tile's tokens see different rows: added row by row where they are
+    // seen, and zeros for the product
+    char* vb = buf + S::kV;
+    if (t_differ) {
+      for (int half = 0; half < 2; ++half) {
+        uint32_t odd = 0;
+        for (int k = tid; k < 32 * S::kVC; k += S::kThreads)
+          if (any_not_finite(*reinterpret_cast<const u32x4*>(vb + (half * 32 * S::kVC + k) * 16))) odd |= 1u << (k / S::kVC);
+        odd = any_rows(odd, tmp);
+        if (__builtin_expect(odd == 0, 1)) continue;
 #pragma unroll 1
-      for (int row = 0; row < kTB; ++row) {
+        for (uint32_t left = skip ? 0 : odd; left != 0; left &= left - 1) {
+          const int row = half * 32 + __builtin_ctz(left), at = j0 + row;
 #pragma unroll
-        for (int mb = 0; mb < RB; ++mb) {
-          float w = 0.0f;
+          for (int mb = 0; mb < RB; ++mb) {
+            float w = 0.0f;
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            if ((row >> 4) * 4 + (row & 3) == k) w = s[k >> 2][mb][k & 3];
-          w = __shfl(w, ((row >> 2) & 3) * 16 + i16, kWave);
-          const int at = j0 + row;
-          if (at >= t.hi || at > qrow[mb] || (a.rq.window > 0 && at <= qrow[mb] - a.rq.window)) continue;
+            for (int k = 0; k < 16; ++k)
+              if ((row >> 4) * 4 + (row & 3) == k) w = s[k >> 2][mb][k & 3];
+            w = __shfl(w, ((row >> 2) & 3) * 16 + i16, kWave);
+            const bool seen = at < t.hi && at <= qrow[mb] && (a.rq.window <= 0 || at > qrow[mb] - a.rq.window);
 #pragma unroll
-          for (int fb = 0; fb < HD / 16; ++fb) {
-            const u32x2 v = *reinterpret_cast<const u32x2*>(vb + row * S::kVC * 16 + ((fb * 2 + (g >> 1)) ^ value_swizzle<S::kVC>(row)) * 16 + (g & 1) * 8);
-            acc[fb][mb] += f32x4{w * bf16_lo(v.x), w * bf16_hi(v.x), w * bf16_lo(v.y), w * bf16_hi(v.y)};
+            for (int fb = 0; fb < HD / 16; ++fb) {
+              const u32x2 v = *reinterpret_cast<const u32x2*>(vb + row * S::kVC * 16 + ((fb * 2 + (g >> 1)) ^ value_swizzle<S::kVC>(row)) * 16 + (g & 1) * 8);
+              acc[fb][mb][0] += seen ? w * bf16_lo(v.x) : 0.0f;
+              acc[fb][mb][1] += seen ? w * bf16_hi(v.x) : 0.0f;
+              acc[fb][mb][2] += seen ? w * bf16_lo(v.y) : 0.0f;
+              acc[fb][mb][3] += seen ? w * bf16_hi(v.y) : 0.0f;
+            }
           }
         }
+        wait_lds_barrier();
+        for (int k = tid; k < 32 * S::kVC; k += S::kThreads)
+          if ((odd >> (k / S::kVC)) & 1) *reinterpret_cast<u32x4*>(vb + (half * 32 * S::kVC + k) * 16) = u32x4{0u, 0u, 0u, 0u};
+        wait_lds_barrier();
       }
     }
+    if (skip) continue;
+    // ---- values
+#pragma unroll
+    for (int ks = 0; ks < kTB / 32; ++ks)
+#pragma unroll
+      for (int fb = 0; fb < HD / 16; ++fb) {
+        const char* at = vb + (value_at ^ (fb % S::kValueTurn * 32)) + fb / S::kValueTurn * S::kValueTurn * 32 + ks * 32 * S::kVC * 16;
+        const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)at));
+        const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(at + 16 * S::kVC * 16)));
+        const u32x4 v = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+        for (int mb = 0; mb < RB; ++mb) acc[fb][mb] = mfma16x16x32(v, p[ks][mb], acc[fb][mb]);
+      }
   }
 
   // ---- outputs, or a part: [part, token, head, HD + 2] fp32 with the maximum and the sum at the end
 #pragma unroll
   for (int mb = 0; mb < RB; ++mb) {
-    float l = l_own[mb];
-    l += __shfl_xor(l, 16, kWave);
-    l += __shfl_xor(l, 32, kWave);
+    const float l = quad_sum(l_own[mb]);
     const int tok = (wv * RB + mb) * 16 + i16;
     if (tok >= t.tokens) continue;
     const int64_t token = t.s.first + t.t0 + tok;
@@ -338,37 +340,53 @@ __global__ __launch_bounds__(NW* kWave, NW / 4) void k_expanded(ExpandedArgs a) 
   }
 }
 
-// Adds a tile's parts in order; a wave takes one token and head at a time.
-template <int HD, int NW, int RB>
-__global__ __launch_bounds__(NW* kWave) void k_expanded_join(ExpandedArgs a) {
-  using S = Shape<HD, NW, RB>;
-  __shared__ int64_t tmp[NW + 2];
+// Adds a tile's parts in order: a workgroup takes 16 tokens of a tile, a wave one at a time.  Lane p has part p's maximum
+// and sum (at most 32 parts).
+template <int HD, int M>
+__global__ __launch_bounds__(256) void k_expanded_join(ExpandedArgs a) {
+  __shared__ int64_t tmp[4 + 2];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int head = int(blockIdx.x / a.tiles);
+  const int tile = int(blockIdx.x % a.tiles), head = int(blockIdx.x / a.tiles);
   Tile t;
-  if (!find_tile<S::kThreads, S::M>(a, int(blockIdx.x - head * a.tiles), tmp, &t)) return;
+  if (!find_tile<256, M>(a, tile, tmp, &t)) return;
   constexpr int kPer = HD / 64;
+  typedef float vec __attribute__((ext_vector_type(kPer)));
   const int64_t rows = int64_t(a.rq.n_tokens) * a.heads;
-  for (int tok = wv; tok < t.tokens; tok += NW) {
+  const int last = blockIdx.y * 16 + 16 < t.tokens ? blockIdx.y * 16 + 16 : t.tokens;
+  for (int tok = blockIdx.y * 16 + wv; tok < last; tok += 4) {
     const int64_t token = t.s.first + t.t0 + tok, row = token * a.heads + head;
-    const float* ml = a.workspace + a.parts * rows * HD + row * 2;
-    float m = -kInf;
-    for (int p = 0; p < a.parts; ++p) m = fmaxf(m, ml[p * rows * 2]);
-    const float ref = m == -kInf ? 0.0f : m;
-    float l = 0.0f, v[kPer] = {};
-#pragma unroll 4
-    for (int p = 0; p < a.parts; ++p) {
-      const float f = __builtin_amdgcn_exp2f(ml[p * rows * 2] - ref);
-      l += f * ml[p * rows * 2 + 1];
-      const float* acc = a.workspace + (p * rows + row) * HD + lane * kPer;
+    float m = -kInf, l = 0.0f;
+    if (lane < a.parts) {
+      const f32x2 ml = *reinterpret_cast<const f32x2*>(a.workspace + a.parts * rows * HD + (lane * rows + row) * 2);
+      m = ml.x;
+      l = ml.y;
+    }
+    float top = m;
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) v[e] += f * acc[e];
+    for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, kWave));
+    top = __shfl(top, 0, kWave);
+    const float f = __builtin_amdgcn_exp2f(m - (top == -kInf ? 0.0f : top));
+    l *= f;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) l += __shfl_xor(l, o, kWave);
+    l = __shfl(l, 0, kWave);
+    vec v = {};
+    const float* from = a.workspace + row * HD + lane * kPer;
+    for (int p0 = 0; p0 < a.parts; p0 += 8) {  // (indexes past the last part repeat it, unused)
+      vec part[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) part[k] = *reinterpret_cast<const vec*>(from + (p0 + k < a.parts ? p0 + k : a.parts - 1) * rows * HD);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), p0 + k));
+        if (p0 + k < a.parts) v += w * part[k];
+      }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     uint16_t* out = a.out + token * a.out_stride + head * HD + lane * kPer;
     if constexpr (kPer == 2) *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(v[0] * inv, v[1] * inv);
     else *out = uint16_t(pack_bf16x2(v[0] * inv, 0.0f));
-    if (a.lse != nullptr && lane == 0) a.lse[row] = l == 0.0f ? -kInf : (m + __builtin_amdgcn_logf(l)) * 0.69314718f;
+    if (a.lse != nullptr && lane == 0) a.lse[row] = l == 0.0f ? -kInf : (top + __builtin_amdgcn_logf(l)) * 0.69314718f;
   }
 }
 
@@ -397,7 +415,7 @@ hipError_t run(const ExpandedArgs& a, hipStream_t stream) {
   if (e != hipSuccess) return e;
   const dim3 block(S::kThreads);
   k_expanded<HD, NW, RB><<<dim3(uint32_t(a.tiles) * a.heads * a.parts), block, S::kBytes, stream>>>(a);
-  if (a.parts > 1) k_expanded_join<HD, NW, RB><<<dim3(uint32_t(a.tiles) * a.heads), block, 0, stream>>>(a);
+  if (a.parts > 1) k_expanded_join<HD, S::M><<<dim3(uint32_t(a.tiles) * a.heads, S::M / 16), dim3(256), 0, stream>>>(a);
   return hipGetLastError();
 }
 
