@@ -17,6 +17,7 @@ struct LatentRequests {
   int min_tokens, max_tokens;  // requests with so many new tokens take part
   int window;                  // 0: none
   uint32_t page_mul, page_shift;  // of page_of
+  int stage_pages, stage_rest;    // 32 positions: whole pages, and positions more
   // pos / block_size of a position below 2^30: page_mul = ceil(2^(30 + s) / block_size) with s the bits of block_size - 1, so
   // that page_mul block_size - 2^(30 + s) < 2^s and the quotient is off by less than 1 / block_size
   __host__ __device__ int page_of(int pos) const { return int((uint64_t(uint32_t(pos)) * page_mul) >> page_shift); }
@@ -28,6 +29,8 @@ struct LatentRequests {
     while ((int64_t(1) << s) < block) ++s;
     page_mul = uint32_t(((uint64_t(1) << (30 + s)) + block - 1) / block);
     page_shift = 30 + s;
+    stage_pages = 32 / block;
+    stage_rest = 32 % block;
   }
 };
 

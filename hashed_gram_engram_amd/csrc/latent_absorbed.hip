@@ -6,8 +6,7 @@
 //  scores   S^T = C Q^T: a wave takes 16 (MB 4: 32) of the positions and keeps its queries in registers; a lane
 //           then holds 4 consecutive positions of one query.
 //  softmax  running maximum and sum in the base 2; the waves share each stage's maxima through LDS; a maximum
-//           that grows by less than 2^8 leaves the reference where it is (weights up to 2^8 cost nothing in
-//           fp32 sums and bf16 weights), so that accumulators are rarely rescaled.
+//           that grows by less than 2^16 leaves the reference where it is.
 //  values   out^T += C^T P^T: a wave takes a quarter of the latent's features for every query; the weights
 //           pass through LDS as bf16, the order of positions in the product being that of the score fragments.
 //
@@ -19,7 +18,6 @@
 // Rows that take no part (outside the tile's positions, on a bad page) are zeros in LDS and their scores
 // -infinity.  Where the tokens of a tile see different positions, a value that is not finite must not reach those that do
 // not see it (0 times infinity): such stages are looked through and, if they hold one, added by plain_values.
-#include <stdlib.h>
 #include "latent_units.h"
 
 namespace engram {
@@ -476,9 +474,12 @@ hipError_t run(const AbsorbedArgs& a, int cus, hipStream_t stream) {
   const int64_t rows = tokens * a.heads;
   if (rows <= 16) return run<DC, 1>(a, G, stream);
   if (rows <= 32) return run<DC, 2>(a, G, stream);
-  if (getenv("EXP") && atoi(getenv("EXP")) == 4) return run<DC, 4>(a, G, stream);
-  if (getenv("EXP") && atoi(getenv("EXP")) == 1) return launch_absorbed_rows(a, G, false, stream);
-  return launch_absorbed_rows(a, G, rows > 64, stream);
+  // Tiles of 128 rows read LDS half as often, but leave parts of twice the size: they pay where workgroups go over many
+  // stages each.  The lengths are not known here; at most, the requests fill the table.  (64 requests of up to 8192
+  // positions, 128 heads: 196 us, 217 us in tiles of 64 rows; 32 of up to 3001, 5 tokens of 32 heads: 54 us and 51;
+  // one of 65,536, 128 heads: 74 us and 59.)
+  const int64_t stages = (rows + 127) / 128 * a.rq.R * (int64_t(a.rq.max_blocks) * a.rq.block_size / 32);
+  return launch_absorbed_rows(a, G, rows > 64 && stages >= 32 * int64_t(G), stream);
 }
 
 }  // namespace

@@ -21,7 +21,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTB = 32;  // positions per stage
 constexpr int kRing = 8;      // stages whose pages are kept
-constexpr int kSlotRing = 4;  // and the places of their rows
+constexpr int kSlotRing = 4;  // and their slots
 
 template <int N>
 __device__ __forceinline__ void wait_copies() {
@@ -94,11 +94,11 @@ struct Shape {
   static constexpr int kCodeCopies = kCodeB / 16 / kThreads;
   static constexpr int kCopies = FP8 ? kCodeCopies + 2 : kTB * kChunks / kThreads;  // of a thread and stage
   static constexpr int kRaw = kBufs * kStageB;  // offsets into LDS
-  // each wave's own: the pages of some stages' positions, where the rows lie, and which of them take part
+  // each wave's own: the pages of some stages' positions, their places in the pages, and their slots
   static constexpr int kPages = kRaw + (FP8 ? kRaws * kRawB : 0);
-  static constexpr int kSlots = kPages + 4 * kRing * 256;
-  static constexpr int kAlive = kSlots + 4 * kSlotRing * kTB * 8;
-  static constexpr int kMisc = kAlive + 4 * kRing * 4;
+  static constexpr int kPlaces = kPages + 4 * kRing * 256;
+  static constexpr int kSlots = kPlaces + 4 * kRing * kTB * 4;
+  static constexpr int kMisc = kSlots + 4 * kSlotRing * kTB * 4;
   static constexpr int kBytes = kMisc + 64;
   static constexpr int kPerCU = 2 * kBytes <= 160 * 1024 ? 2 : 1;
 };
@@ -112,37 +112,40 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed_rows(A
   const int rkb = a.rope_dim / 32;
   const int row_b = latent_row_bytes(DC, a.rope_dim, FP8);
   int32_t* pages = reinterpret_cast<int32_t*>(lds + S::kPages) + wv * kRing * 64;
-  int64_t* slots = reinterpret_cast<int64_t*>(lds + S::kSlots) + wv * kSlotRing * kTB;
-  uint32_t* alive = reinterpret_cast<uint32_t*>(lds + S::kAlive) + wv * kRing;
+  int32_t* slots = reinterpret_cast<int32_t*>(lds + S::kSlots) + wv * kSlotRing * kTB;
+  int32_t* places = reinterpret_cast<int32_t*>(lds + S::kPlaces) + wv * kRing * kTB;
   int64_t* misc = reinterpret_cast<int64_t*>(lds + S::kMisc);
   const PartSpace space = part_space(a.workspace, gridDim.x, S::M);
   Units un;
   if (!my_units<kThreads, S::M, kTB>(a.rq, a.heads, space.parts, misc, &un)) return;
 
+  constexpr int kHalf = DC / 16, kRows = 64 / kHalf;  // of the conversion: chunks in half a row, rows of codes in a copy
+
+  // (Addresses in LDS and of copies are made from the lane's number where they are used: kept around the loop they
+  // would take the registers that queries and accumulators leave, and go through memory, behind all copies in flight.)
+  auto fresh = [&]() {
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    return l;
+  };
+  constexpr bool kLean = RB == 2 && DC != 256;
+  auto lane_now = [&]() { return kLean ? fresh() : lane; };
   // A chunk's place differs from row to row in the low three bits of its number only, so the reads of a stage take
-  // two (keys) and four (values) addresses and constants.  (Rows start at multiples of 128 bytes.)
-  const int key_at = i16 * S::kRowB + (g ^ latent_swizzle(i16)) * 16;
-  const int vrow = 4 * g + (i16 >> 2);
-  const int value_at = vrow * S::kRowB + (((i16 & 3) >> 1) ^ latent_swizzle(vrow)) * 16 + (i16 & 1) * 8;
+  // two addresses (keys) or four (values) and constants.  (Rows start at multiples of 128 bytes.)
+  auto key_place = [&]() {
+    const int l = lane_now(), i = l & 15;
+    return i * S::kRowB + ((l >> 4) ^ latent_swizzle(i)) * 16;
+  };
+  auto value_place = [&]() {
+    const int l = lane_now(), i = l & 15, row = (l >> 4) * 4 + (i >> 2);
+    return row * S::kRowB + (((i & 3) >> 1) ^ latent_swizzle(row)) * 16 + (i & 1) * 8;
+  };
 
   while (un.u < un.u1) {
     const Segment t = segment_of<S::M, kTB>(a.rq, a.heads, un);
     const int c0 = t.c0, n = t.n;
     const int w0 = t.row0 + wv * 16 * RB;  // the wave's first row
 
-    // ---- queries, and the position of each row's token (-1: no row)
-    u32x4 qf[RB][S::kKB + 2];
-    int qpos[RB];
-#pragma unroll
-    for (int mb = 0; mb < RB; ++mb) {
-      const int row = w0 + mb * 16 + i16, at = row < t.rows ? row : t.rows - 1;  // (rows past the last repeat it)
-      const int tok = at / a.heads, head = at - tok * a.heads;
-      qpos[mb] = row < t.rows ? t.s.pos + tok : -1;
-      const uint16_t* src = a.q + (t.s.first + tok) * a.q_stride + int64_t(head) * (DC + a.rope_dim) + 8 * g;
-#pragma unroll
-      for (int kb = 0; kb < S::kKB + 2; ++kb)
-        qf[mb][kb] = *reinterpret_cast<const u32x4*>(src + 32 * (kb < S::kKB + rkb ? kb : 0)) ^ a.q_sign;
-    }
     f32x4 acc[S::kFB][RB];
     float m_run[RB], l_own[RB];
 #pragma unroll
@@ -163,111 +166,132 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed_rows(A
     };
 
     // ---- staging
-    // (What these compute from the lane's number is made where it is used: kept around the loop it would take the
-    // registers that the queries and accumulators leave, and go through memory.)
-    auto fresh = [&]() {
-      int l = lane;
-      asm volatile("" : "+v"(l));
-      return l;
-    };
-    // Lane l < 32 looks after row l of a stage: its page is copied to LDS two stages before its slot is made (by a copy,
-    // like the rows: a load into a register would have to wait for all the copies before it), which is when its
-    // row is copied.  Every wave does so for itself.
+    // Lanes l and 32 + l look after row l of a stage.  Its page is copied to LDS some stages before its slot is made (by a
+    // copy, like the rows: a load into a register would have to wait for all the copies before it), which is before
+    // its row is copied.  Every wave does so for itself.  The page's entry and the place in it go on by 32 positions a
+    // stage; entries past the table repeat its last one (those positions are not the request's).
     const int32_t* table = a.rq.block_table + int64_t(un.r) * a.rq.max_blocks;
-    auto copy_pages = [&](int c) {
-      const int lane = fresh();
-      int pos = t.base + c * kTB + (lane & 31);
-      pos = pos < t.hi ? pos : t.hi - 1;  // (stages past the last: any page)
-      __builtin_amdgcn_global_load_lds((const void*)(table + a.rq.page_of(pos)), (lds_ptr_t)(pages + (c & (kRing - 1)) * 64), 4, 0, 0);
-    };
-    auto make_slots = [&](int c) {
-      const int lane = fresh();
-      const int pos = t.base + c * kTB + (lane & 31), page = pages[(c & (kRing - 1)) * 64 + (lane & 31)];
-      const bool in = c < c0 + n && pos >= t.lo && pos < t.hi, good = page >= 0 && page < a.rq.n_blocks;
-      const int64_t slot = in && good ? int64_t(page) * a.rq.block_size + (pos - a.rq.page_of(pos) * a.rq.block_size) : -1;
-      if (in && !good && wv == 0 && lane < kTB && t.tile == 0 && a.err_count != nullptr) atomicAdd(a.err_count, 1);
-      if (lane < kTB) slots[(c & (kSlotRing - 1)) * kTB + lane] = (slot < 0 ? 0 : slot) * row_b;
-      const uint32_t on = uint32_t(__ballot(slot >= 0));
-      if (lane == 0) alive[c & (kRing - 1)] = on;
-    };
-    // (rows that take no part are copied from the first slot and cleared later; stages past the last too, so that
-    // every wave has the same number of copies in flight)
-    auto row_offset = [&](int c, int k) -> int64_t {  // of the row of which copy k takes 16 bytes
-      const int lane = fresh(), tid = wv * kWave + lane;
-      const int64_t* sl = slots + (c & (kSlotRing - 1)) * kTB;
-      if constexpr (FP8) {
-        constexpr int kNP = DC / 16;
-        if (k < S::kCodeCopies) return sl[tid / kNP + k * (kThreads / kNP)];
-        if (k == S::kCodeCopies) return sl[rkb == 2 ? tid >> 3 : (tid >> 2) & 31];
-        return sl[lane & 31];
-      } else {
-        return sl[(k * kThreads + tid) / S::kChunks];
+    int entry = a.rq.page_of(t.base + c0 * kTB + (lane & 31)), place = t.base + c0 * kTB + (lane & 31) - entry * a.rq.block_size;
+    auto copy_pages = [&](int c) {  // stages one after the other
+      const int row = lane_now() & 31;
+      const int e = entry < a.rq.max_blocks ? entry : a.rq.max_blocks - 1;
+      __builtin_amdgcn_global_load_lds((const void*)(table + e), (lds_ptr_t)(pages + (c & (kRing - 1)) * 64), 4, 0, 0);
+      places[(c & (kRing - 1)) * kTB + row] = place;
+      entry += a.rq.stage_pages;
+      place += a.rq.stage_rest;
+      if (place >= a.rq.block_size) {
+        place -= a.rq.block_size;
+        ++entry;
       }
     };
-    auto copy = [&](int c, int k, int64_t offset) {
-      const int lane = fresh(), tid = wv * kWave + lane;
-      const uint8_t* row = a.cache + offset;
+    struct Page {
+      int page, place;
+    };
+    auto read_page = [&](int c) {
+      const int row = lane_now() & 31;
+      return Page{pages[(c & (kRing - 1)) * 64 + row], places[(c & (kRing - 1)) * kTB + row]};
+    };
+    // Writes the slots of stage c, 0 for rows that take no part; returns those that do.
+    auto make_slots = [&](int c, const Page& p) -> uint32_t {
+      const bool good = uint32_t(p.page) < uint32_t(a.rq.n_blocks);
+      slots[(c & (kSlotRing - 1)) * kTB + (lane_now() & 31)] = good ? p.page * a.rq.block_size + p.place : 0;
+      const int j0 = t.base + c * kTB, from = t.lo - j0, to = c < c0 + n ? t.hi - j0 : 0;  // rows [from, to)
+      const uint32_t below = to >= 32 ? ~0u : (to <= 0 ? 0u : (1u << to) - 1u), above = from <= 0 ? ~0u : (from >= 32 ? 0u : ~0u << from);
+      const uint32_t in = below & above, on = in & uint32_t(__ballot(good));
+      if (__builtin_expect(on != in, 0))
+        if (wv == 0 && lane == 0 && t.tile == 0 && a.err_count != nullptr) atomicAdd(a.err_count, __builtin_popcount(in ^ on));
+      return on;
+    };
+    uint32_t on_ring[5];  // rows that take part in stages c .. c + 4
+    // (rows that take no part are copied from the first slot and cleared later; stages past the last too, so that
+    // every wave has the same number of copies in flight)
+    // A lane's part in the copies of a stage: where the slots of its rows stand, and what it takes of a row.
+    struct Copies {
+      const int32_t* code;
+      const int32_t* rope;
+      const int32_t* scale;
+      const uint8_t* code_from;
+      const uint8_t* rope_from;
+    };
+    auto copies_of = [&](int c) {
+      const int l = lane_now(), tid = wv * kWave + l;
+      const int32_t* sl = slots + (c & (kSlotRing - 1)) * kTB;
+      return Copies{sl + wv * kRows + l / kHalf, sl + (rkb == 2 ? tid >> 3 : (tid >> 2) & 31), sl + (l & 31),
+                    a.cache + l % kHalf * 16, a.cache + DC + 16 + (rkb == 2 ? tid & 7 : tid & 3) * 16};
+    };
+    auto row_slot = [&](const Copies& p, int c, int k) -> int {  // of which copy k takes 16 bytes
+      if constexpr (FP8) return k < S::kCodeCopies ? p.code[k * 4 * kRows] : (k == S::kCodeCopies ? *p.rope : *p.scale);
+      const int id = k * kThreads + wv * kWave + lane_now();
+      return slots[(c & (kSlotRing - 1)) * kTB + id / S::kChunks];
+    };
+    auto copy = [&](const Copies& p, int c, int k, int slot) {
+      const uint64_t at = uint64_t(uint32_t(slot)) * uint32_t(row_b);
       if constexpr (FP8) {
-        constexpr int kNP = DC / 16;
-        char* raw = lds + S::kRaw + (c % S::kRaws) * S::kRawB;
-        const int at = k < S::kCodeCopies ? tid % kNP * 16 : (k == S::kCodeCopies ? DC + 16 + (rkb == 2 ? tid & 7 : tid & 3) * 16 : DC);
-        __builtin_amdgcn_global_load_lds((const void*)(row + at), (lds_ptr_t)(raw + (k * 4 + wv) * 1024), 16, 0, 0);
+        const uint8_t* from = k < S::kCodeCopies ? p.code_from : (k == S::kCodeCopies ? p.rope_from : a.cache + DC);
+        __builtin_amdgcn_global_load_lds((const void*)(from + at), (lds_ptr_t)(lds + S::kRaw + (c % S::kRaws) * S::kRawB + (k * 4 + wv) * 1024), 16, 0, 0);
       } else {
-        const int id = k * kThreads + tid, r = id / S::kChunks;
+        const int id = k * kThreads + wv * kWave + lane_now(), r = id / S::kChunks;
         int ch = (id - r * S::kChunks) ^ latent_swizzle(r);
         ch = ch < DC / 8 + 4 * rkb ? ch : 0;  // (a place that is not read)
-        __builtin_amdgcn_global_load_lds((const void*)(row + ch * 16),
+        __builtin_amdgcn_global_load_lds((const void*)(a.cache + at + ch * 16),
                                          (lds_ptr_t)(lds + (c % S::kBufs) * S::kStageB + (k * 4 + wv) * 1024), 16, 0, 0);
       }
     };
     auto copy_stage = [&](int c) {
+      const Copies p = copies_of(c);
 #pragma unroll
-      for (int k = 0; k < S::kCopies; ++k) copy(c, k, row_offset(c, k));
+      for (int k = 0; k < S::kCopies; ++k) copy(p, c, k, row_slot(p, c, k));
     };
     // FP8: of what the wave's copy k brought (kRows rows of codes; the last one: rope parts), a lane's chunks are first
-    // and first + half a row, so that a wave's writes fill all banks
+    // and first + half a row, so that a wave's writes fill all banks.  Row 4 kRows k + row0: its swizzle differs from row0's in
+    // the bits that row / 8 has there.
+    struct Places {
+      const char* raw;
+      const uint8_t* scale;
+      int write;
+      const char* rope;
+      char* rope_write;
+      int row0;
+    };
+    auto places_of = [&](int c) {
+      const int l = lane_now(), row0 = wv * kRows + l / kHalf, tid = wv * kWave + l;
+      const int rp = rkb == 2 ? tid & 7 : tid & 3, rr = rkb == 2 ? tid >> 3 : (tid >> 2) & 31;
+      const char* raw = lds + S::kRaw + (c % S::kRaws) * S::kRawB;
+      const char* buf = lds + (c & 1) * S::kStageB;
+      return Places{raw + row0 * DC + l % kHalf * 8,
+                    reinterpret_cast<const uint8_t*>(raw + S::kCodeB + S::kRopeB + wv * 1024 + row0 * 16 + l % kHalf / 4),
+                    int(buf - lds) + row0 * S::kRowB + (l % kHalf ^ latent_swizzle(row0)) * 16, raw + S::kCodeB + tid * 16,
+                    lds + (c & 1) * S::kStageB + rr * S::kRowB + ((DC / 8 + rp) ^ latent_swizzle(rr)) * 16, row0};
+    };
     struct Raw {
       u32x4 v;
       uint32_t scale0, scale1;
     };
-    constexpr int kHalf = DC / 16, kRows = 64 / kHalf;
-    auto read_raw = [&](int c, int k) {
-      const int lane = fresh(), tid = wv * kWave + lane;
-      const char* raw = lds + S::kRaw + (c % S::kRaws) * S::kRawB;
+    constexpr int kStep = 4 * kRows;  // rows between a wave's copies
+    auto read_raw = [&](const Places& p, int k) {
       Raw r = {};
       if (k == S::kCodeCopies) {
-        r.v = *reinterpret_cast<const u32x4*>(raw + (k * kThreads + tid) * 16);
+        r.v = *reinterpret_cast<const u32x4*>(p.rope);
       } else {
-        const int row = (k * 4 + wv) * kRows + lane / kHalf, ch = lane % kHalf;
-        const u32x2 lo = *reinterpret_cast<const u32x2*>(raw + row * DC + ch * 8), hi = *reinterpret_cast<const u32x2*>(raw + row * DC + (ch + kHalf) * 8);
-        const uint8_t* sc = reinterpret_cast<const uint8_t*>(raw + S::kCodeB + S::kRopeB + wv * 1024 + row * 16);
+        const u32x2 lo = *reinterpret_cast<const u32x2*>(p.raw + k * kStep * DC), hi = *reinterpret_cast<const u32x2*>(p.raw + k * kStep * DC + kHalf * 8);
         r.v = u32x4{lo.x, lo.y, hi.x, hi.y};
-        r.scale0 = sc[ch / 4];
-        r.scale1 = sc[(ch + kHalf) / 4];
+        r.scale0 = p.scale[k * kStep * 16];
+        r.scale1 = p.scale[k * kStep * 16 + kHalf / 4];
       }
       return r;
     };
-    auto convert = [&](int c, int k, const Raw& r) {
-      const int lane = fresh(), tid = wv * kWave + lane;
-      const uint32_t on = __builtin_amdgcn_readfirstlane(alive[c & (kRing - 1)]);
-      char* buf = lds + (c & 1) * S::kStageB;
-      const u32x4 none = {0u, 0u, 0u, 0u};
+    auto convert = [&](const Places& p, uint32_t on, int k, int half, const Raw& r) {  // the lane's first chunk, or its second
       if (k == S::kCodeCopies) {
-        const int rp = rkb == 2 ? tid & 7 : tid & 3, row = rkb == 2 ? tid >> 3 : (tid >> 2) & 31;
-        *reinterpret_cast<u32x4*>(buf + row * S::kRowB + ((DC / 8 + rp) ^ latent_swizzle(row)) * 16) = r.v;  // (only scores read it)
-      } else {
-        const int row = (k * 4 + wv) * kRows + lane / kHalf, ch = lane % kHalf;
-        u32x4 o0, o1;
-        latent8x2(r.v, r.scale0, r.scale1, o0, o1);
-        if (__builtin_expect(on != ~0u, 0))
-          if (!((on >> row) & 1)) o0 = o1 = none;
-        char* to = buf + row * S::kRowB + (ch ^ latent_swizzle(row)) * 16;
-        *reinterpret_cast<u32x4*>(to) = o0;
-        *reinterpret_cast<u32x4*>(to + kHalf * 16) = o1;  // (a multiple of 8 chunks further)
+        if (half == 0) *reinterpret_cast<u32x4*>(p.rope_write) = r.v;  // (only scores read it: no need to clear)
+        return;
       }
+      u32x4 o = latent8(half == 0 ? u32x2{r.v.x, r.v.y} : u32x2{r.v.z, r.v.w}, half == 0 ? r.scale0 : r.scale1);
+      if (__builtin_expect(on != ~0u, 0))
+        if (!((on >> (p.row0 + k * kStep)) & 1)) o = u32x4{0u, 0u, 0u, 0u};
+      *reinterpret_cast<u32x4*>(lds + (p.write ^ (latent_swizzle(k * kStep) * 16)) + k * kStep * S::kRowB + half * kHalf * 16) = o;  // (kHalf: whole 8 chunks)
     };
     auto clear_dead = [&](int c) {  // BF16: of what this lane copied
-      const uint32_t on = alive[c & (kRing - 1)];
+      const uint32_t on = on_ring[0];
       if (on == ~0u) return;
       char* buf = lds + (c % S::kBufs) * S::kStageB;
 #pragma unroll 1
@@ -280,35 +304,62 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed_rows(A
     constexpr int kCopyStage = FP8 ? 3 : 2;  // stages that rows are copied ahead
     wait_all_barrier();  // nobody reads LDS or copies into it any more
 #pragma unroll
-    for (int k = 0; k < kCopyStage; ++k) copy_pages(c0 + k);
+    for (int k = 0; k <= kCopyStage; ++k) copy_pages(c0 + k);
+
+    // ---- queries, and the position of each row's token (-1: no row)
+    u32x4 qf[RB][S::kKB + 2];
+    int qpos[RB];
+#pragma unroll
+    for (int mb = 0; mb < RB; ++mb) {
+      const int row = w0 + mb * 16 + i16, at = row < t.rows ? row : t.rows - 1;  // (rows past the last repeat it)
+      const int tok = at / a.heads, head = at - tok * a.heads;
+      qpos[mb] = row < t.rows ? t.s.pos + tok : -1;
+      const uint16_t* src = a.q + (t.s.first + tok) * a.q_stride + int64_t(head) * (DC + a.rope_dim) + 8 * g;
+#pragma unroll
+      for (int kb = 0; kb < S::kKB + 2; ++kb)
+        qf[mb][kb] = *reinterpret_cast<const u32x4*>(src + 32 * (kb < S::kKB + rkb ? kb : 0)) ^ a.q_sign;
+    }
     wait_copies<0>();
+    {
+      Page page[kCopyStage + 1];
+#pragma unroll
+      for (int k = 0; k <= kCopyStage; ++k) page[k] = read_page(c0 + k);
+#pragma unroll
+      for (int k = 0; k <= kCopyStage; ++k) on_ring[k] = make_slots(c0 + k, page[k]);
+    }
 #pragma unroll
     for (int k = 0; k < kCopyStage; ++k) {
-      make_slots(c0 + k);
       copy_stage(c0 + k);
-      if (k >= kCopyStage - 2) copy_pages(c0 + k + 2);
+      if (k >= kCopyStage - 2) copy_pages(c0 + k + 3);
     }
     if constexpr (FP8) {
       wait_copies<2 * S::kCopies + 2>();
+      const Places at = places_of(c0);
+      Raw raw[S::kCodeCopies + 1];
 #pragma unroll
-      for (int k = 0; k <= S::kCodeCopies; ++k) convert(c0, k, read_raw(c0, k));
+      for (int k = 0; k <= S::kCodeCopies; ++k) raw[k] = read_raw(at, k);
+#pragma unroll
+      for (int k = 0; k <= S::kCodeCopies; ++k) {
+        convert(at, on_ring[0], k, 0, raw[k]);
+        convert(at, on_ring[0], k, 1, raw[k]);
+      }
     }
 
     for (int j = 0; j < n; ++j) {
       const int c = c0 + j;
-      wait_copies<S::kCopies + 1>();  // FP8: of stage c + 1, BF16: of stage c, are there, and the pages of stage c + kCopyStage
+      wait_copies<S::kCopies + 1>();  // FP8: of stage c + 1, BF16: of stage c, are there, and the pages of stage c + kCopyStage + 1
       if constexpr (!FP8) clear_dead(c);
       wait_lds_barrier();
-      make_slots(c + kCopyStage);
       char* buf = lds + (FP8 ? (c & 1) : c % S::kBufs) * S::kStageB;
 
       f32x4 s[2][RB];
       u32x4 p[RB];
-      const uint32_t on = __builtin_amdgcn_readfirstlane(alive[c & (kRing - 1)]);
+      const uint32_t on = on_ring[0], on_next = on_ring[1];
       const int j0 = t.base + c * kTB;
       const bool differ = t.p_min != t.p_max && (j0 + kTB - 1 > t.p_min || (a.rq.window > 0 && j0 <= t.p_max - a.rq.window));
       {
         // ---- scores, and (FP8) the next stage's conversion between them
+        const int key_at = key_place();
         const char* kp[2] = {buf + key_at, buf + (key_at ^ 64)};
         auto key = [&](int kb, int tb) { return *reinterpret_cast<const u32x4*>(kp[kb & 1] + tb * 16 * S::kRowB + (kb >> 1) * 128); };
         constexpr int kDeep = RB == 2 ? 3 : 5;
@@ -320,11 +371,12 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed_rows(A
         }
         if constexpr (RB == 1) s[0][0] = s[1][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         constexpr int kSteps = S::kKB + 2;
-        int64_t from;
-        // beside each step's products: the keys of a later step, and a row copied (its place read a step before)
+        int from[2];
+        const Copies cp = copies_of(c + kCopyStage);
+        // beside each step's products: the keys of a later step, and a row copied (its slot read two steps before)
         auto side = [&](int kb) {
-          if (kb >= 1 && kb - 1 < S::kCopies) copy(c + kCopyStage, kb - 1, from);
-          if (kb < S::kCopies) from = row_offset(c + kCopyStage, kb);
+          if (kb >= 2 && kb - 2 < S::kCopies) copy(cp, c + kCopyStage, kb - 2, from[kb & 1]);
+          if (kb < S::kCopies) from[kb & 1] = row_slot(cp, c + kCopyStage, kb);
         };
 #pragma unroll
         for (int kb = 0; kb < kSteps; ++kb) {
@@ -345,10 +397,10 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed_rows(A
           __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
-        for (int kb = kSteps; kb < S::kCopies + 1; ++kb) side(kb);  // what small latents leave
+        for (int kb = kSteps; kb < S::kCopies + 2; ++kb) side(kb);  // what small latents leave
         if constexpr (RB == 2) finish_scores(s);
       }
-      copy_pages(c + kCopyStage + 2);
+      copy_pages(c + kCopyStage + 3);
 
       // ---- softmax
       if (on != ~0u || differ) {
@@ -382,8 +434,15 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed_rows(A
           const float alpha = m == -kInf ? 1.0f : __builtin_amdgcn_exp2f(m_run[mb] - m);
           m_run[mb] = m;
           l_own[mb] *= alpha;
-#pragma unroll 4
-          for (int fb = 0; fb < S::kFB; ++fb) *reinterpret_cast<f32x4*>(mem + (mb * S::kFB + fb) * (kWave * 16)) *= alpha;
+#pragma unroll 1
+          for (int fb = 0; fb < S::kFB; fb += 8) {
+            f32x4* at = reinterpret_cast<f32x4*>(mem + (mb * S::kFB + fb) * (kWave * 16));
+            f32x4 v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = at[e * kWave];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) at[e * kWave] = v[e] * alpha;
+          }
         }
         acc_from_memory(acc, mem);
       }
@@ -445,15 +504,18 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed_rows(A
       }
 
       // ---- values
+      const int value_at = value_place();
       const char* vp[4] = {buf + value_at, buf + (value_at ^ 32), buf + (value_at ^ 64), buf + (value_at ^ 96)};
       auto value = [&](int fb) {
-        const char* at = vp[fb & 3] + (fb >> 2) * 128;
-        const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)at));
-        const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(at + 16 * S::kRowB)));
+        const char* from = vp[fb & 3] + (fb >> 2) * 128;
+        const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)from));
+        const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(from + 16 * S::kRowB)));
         return u32x4{lo.x, lo.y, hi.x, hi.y};
       };
+      const Places at = places_of(c + 1);
       Raw raw;
-      constexpr int kDeep = 6;
+      Page page;
+      constexpr int kDeep = FP8 || RB == 1 ? 6 : 5;
       u32x4 vf[kDeep];
 #pragma unroll
       for (int fb = 0; fb < kDeep - 1; ++fb) vf[fb] = value(fb);
@@ -462,13 +524,19 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed_rows(A
         if (fb + kDeep - 1 < S::kFB) vf[(fb + kDeep - 1) % kDeep] = value(fb + kDeep - 1);
         if constexpr (FP8) {  // and beside them the next stage's conversion
           constexpr int kEvery = S::kFB / (S::kCodeCopies + 1);
-          if (fb % kEvery == kEvery - 1 && fb / kEvery <= S::kCodeCopies) convert(c + 1, fb / kEvery, raw);
-          if (fb % kEvery == 0 && fb / kEvery <= S::kCodeCopies) raw = read_raw(c + 1, fb / kEvery);
+          const int k = fb / kEvery, in = fb % kEvery;
+          if (k <= S::kCodeCopies && in == kEvery - 2) convert(at, on_next, k, 0, raw);
+          if (k <= S::kCodeCopies && in == kEvery - 1) convert(at, on_next, k, 1, raw);
+          if (k <= S::kCodeCopies && in == 0) raw = read_raw(at, k);
         }
+        if (fb == 1) page = read_page(c + kCopyStage + 1);
+        if (fb == S::kFB / 2) on_ring[kCopyStage + 1] = make_slots(c + kCopyStage + 1, page);
 #pragma unroll
         for (int mb = 0; mb < RB; ++mb) acc[fb][mb] = mfma16x16x32(vf[fb % kDeep], p[mb], acc[fb][mb]);
         __builtin_amdgcn_sched_barrier(0);
       }
+#pragma unroll
+      for (int k = 0; k <= kCopyStage; ++k) on_ring[k] = on_ring[k + 1];
     }
 
     // ---- the outputs, or a part

@@ -41,6 +41,12 @@ engram_status requests(const engram_latent_layout* l, const int32_t* token_start
   return ENGRAM_OK;
 }
 
+engram_status latent_pages_check(const engram_page_layout* p) {
+  const engram_status st = engram_page_layout_check(p);
+  if (st != ENGRAM_OK) return st;
+  return p->n_blocks > 0x7FFFFFFF / p->block_size ? ENGRAM_E_LAYOUT : ENGRAM_OK;  // slots are counted in 32 bits
+}
+
 engram_status pages_of(const engram_page_layout* p, const int32_t* block_table, LatentRequests* q) {
   if (q->R > 0 && !block_table) return ENGRAM_E_NULL;
   if (!aligned(block_table, 4)) return ENGRAM_E_ALIGN;
@@ -75,7 +81,7 @@ engram_status engram_latent_write(const engram_latent_layout* l, const engram_pa
                                   engram_stream_t stream) {
   engram_status st = engram_latent_layout_check(l);
   if (st != ENGRAM_OK) return st;
-  if ((st = engram_page_layout_check(p)) != ENGRAM_OK) return st;
+  if ((st = latent_pages_check(p)) != ENGRAM_OK) return st;
   if (n_tokens < 0 || n_tokens > (int64_t(1) << 30)) return ENGRAM_E_SHAPE;
   if (n_tokens == 0) return ENGRAM_OK;
   if (!latent || !rope || !slots || !cache) return ENGRAM_E_NULL;
@@ -108,7 +114,7 @@ engram_status engram_latent_read(const engram_latent_layout* l, const engram_pag
                                  engram_stream_t stream) {
   engram_status st = engram_latent_layout_check(l);
   if (st != ENGRAM_OK) return st;
-  if ((st = engram_page_layout_check(p)) != ENGRAM_OK) return st;
+  if ((st = latent_pages_check(p)) != ENGRAM_OK) return st;
   LatentReadArgs a;
   memset(&a, 0, sizeof(a));
   if ((st = requests(l, token_start, start_pos, R, n_tokens, &a.rq)) != ENGRAM_OK) return st;
@@ -147,7 +153,7 @@ engram_status engram_latent_attention(const engram_latent_layout* l, const engra
                                       engram_stream_t stream) {
   engram_status st = engram_latent_layout_check(l);
   if (st != ENGRAM_OK) return st;
-  if ((st = engram_page_layout_check(p)) != ENGRAM_OK) return st;
+  if ((st = latent_pages_check(p)) != ENGRAM_OK) return st;
   AbsorbedArgs a;
   memset(&a, 0, sizeof(a));
   if ((st = requests(l, token_start, start_pos, R, n_tokens, &a.rq)) != ENGRAM_OK) return st;

@@ -62,7 +62,7 @@ __global__ __launch_bounds__(kThreads) void k_latent_write(LatentWriteArgs a) {
       top = b > top ? b : top;
     }
     int scale = int(top >> 23) - 8 + ((top & 0x007FFFFFu) > 0x00600000u ? 1 : 0);
-    scale = scale < 0 ? 0 : scale;
+    scale = scale < 1 ? 1 : scale;  // (what 2^-126 leaves of smaller values is still exact: bf16 has none below 2^-133)
     const float up = __uint_as_float(uint32_t(254 - scale) << 23);  // 2^(127 - scale)
     // 248 and more would become 256, which the largest scale takes past bf16: 240 there
     const float most = scale == 247 ? 240.0f : 448.0f;

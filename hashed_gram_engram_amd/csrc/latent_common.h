@@ -49,18 +49,10 @@ __device__ __forceinline__ void latent16(u32x4 c, uint32_t scale, u32x4& o0, u32
   if (__builtin_expect(scale == 0u || scale == 255u, 0)) dequant16(c, e8m0_to_f32(scale), o0, o1);
 }
 
-// Eight codes each of two blocks.
-__device__ __forceinline__ void latent8x2(u32x4 c, uint32_t scale0, uint32_t scale1, u32x4& o0, u32x4& o1) {
-  const float s = __uint_as_float(scale0 << 23), t = __uint_as_float(scale1 << 23);
-  o0 = u32x4{scaled_pair(c.x, s, false), scaled_pair(c.x, s, true), scaled_pair(c.y, s, false), scaled_pair(c.y, s, true)};
-  o1 = u32x4{scaled_pair(c.z, t, false), scaled_pair(c.z, t, true), scaled_pair(c.w, t, false), scaled_pair(c.w, t, true)};
-  const uint32_t k0 = (scale0 + 1) & 255, k1 = (scale1 + 1) & 255;  // 0 and 255 become 1 and 0
-  if (__builtin_expect(__any((k0 < k1 ? k0 : k1) < 2), 0)) {
-    const float f0 = e8m0_to_f32(scale0), f1 = e8m0_to_f32(scale1);
-    const u32x2 a = dequant4_raw(c.x, f0), b = dequant4_raw(c.y, f0), d = dequant4_raw(c.z, f1), e = dequant4_raw(c.w, f1);
-    o0 = u32x4{a.x, a.y, b.x, b.y};
-    o1 = u32x4{d.x, d.y, e.x, e.y};
-  }
+// Eight codes, of a scale that engram_latent_write makes (1 .. 247).
+__device__ __forceinline__ u32x4 latent8(u32x2 c, uint32_t scale) {
+  const float s = __uint_as_float(scale << 23);
+  return u32x4{scaled_pair(c.x, s, false), scaled_pair(c.x, s, true), scaled_pair(c.y, s, false), scaled_pair(c.y, s, true)};
 }
 
 // Running sums over the lanes of a wave, and over the threads of a workgroup of THREADS (tmp: one word per

@@ -5,8 +5,8 @@
 // memory, two buffers.  S^T = K Q^T leaves a lane with 4 consecutive keys of one query, which is an operand
 // of out^T += V^T P^T as it stands if the keys of that product are counted in the same order: the weights never
 // leave the registers, and a query's maximum and sum are shared by 4 lanes of one wave.  Values are read
-// transposed (ds_read_tr16).  The softmax is in the base 2; a maximum that grows by less than 2^8 leaves the
-// reference where it is, so that accumulators are rarely rescaled.
+// transposed (ds_read_tr16).  The softmax is in the base 2; a maximum that grows by less than 2^16 leaves the
+// reference where it is.
 //
 // Where few tiles meet many rows, each tile's stages are shared out in parts; their fp32 sums go to the workspace
 // and k_expanded_join adds them in order.
@@ -142,27 +142,40 @@ __global__ __launch_bounds__(NW* kWave, NW / 4) void k_expanded(ExpandedArgs a) 
     for (int fb = 0; fb < HD / 16; ++fb) acc[fb][mb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  // copies: 16 bytes a lane, in the order of the buffer; keys, then values
-  constexpr int kKeyCopies = kTB * S::kKC / S::kThreads, kValueCopies = kTB * S::kVC / S::kThreads;
+  // Copies: 16 bytes a lane, in the order of the buffer; keys, then values.  A lane's place in the rows moves on by a stage
+  // at a time; only the last stage may have fewer rows, those past the end then repeat the last.
+  constexpr int kKeyCopies = kTB * S::kKC / S::kThreads, kCopies = kKeyCopies + kTB * S::kVC / S::kThreads;
   static_assert(kTB * S::kKC % S::kThreads == 0 && kTB * S::kVC % S::kThreads == 0, "whole copies");
-  auto copy_stage = [&](int c, char* buf) {
-    const int j0 = t.lo + c * kTB;
+  const uint16_t* from[kCopies];
+  uint32_t step[kCopies];  // bytes from row to row
+  auto row_of = [&](int k) { return k < kKeyCopies ? (k * S::kThreads + tid) / S::kKC : ((k - kKeyCopies) * S::kThreads + tid) / S::kVC; };
 #pragma unroll
-    for (int k = 0; k < kKeyCopies; ++k) {
-      const int at = k * S::kThreads + tid, row = at / S::kKC;
-      const int ch = (at - row * S::kKC) ^ key_swizzle<S::kKC>(row);
-      const int64_t src = t.first_row + (j0 + row < t.hi ? j0 + row : t.hi - 1);
-      const uint16_t* from = ch < HD / 8 ? a.kv + src * a.kv_stride + head * 2 * HD + ch * 8
-                                         : a.rope + src * a.rope_stride + (ch - HD / 8 < 4 * rkb ? ch - HD / 8 : 0) * 8;
-      __builtin_amdgcn_global_load_lds((const void*)from, (lds_ptr_t)(buf + (k * NW + wv) * 1024), 16, 0, 0);
+  for (int k = 0; k < kCopies; ++k) {
+    const int row = row_of(k);
+    const uint16_t* base;
+    if (k < kKeyCopies) {
+      const int ch = (k * S::kThreads + tid - row * S::kKC) ^ key_swizzle<S::kKC>(row);
+      const bool own = ch < HD / 8;
+      base = own ? a.kv + head * 2 * HD + ch * 8 : a.rope + (ch - HD / 8 < 4 * rkb ? ch - HD / 8 : 0) * 8;
+      step[k] = uint32_t(own ? a.kv_stride : a.rope_stride) * 2;
+    } else {
+      const int ch = ((k - kKeyCopies) * S::kThreads + tid - row * S::kVC) ^ value_swizzle<S::kVC>(row);
+      base = a.kv + head * 2 * HD + HD + ch * 8;
+      step[k] = uint32_t(a.kv_stride) * 2;
     }
+    from[k] = base + int64_t(t.first_row + t.lo + c0 * kTB + row) * (step[k] / 2);
+  }
+  auto copy_stage = [&](int c, char* buf) {
+    const int left = t.hi - (t.lo + c * kTB);
 #pragma unroll
-    for (int k = 0; k < kValueCopies; ++k) {
-      const int at = k * S::kThreads + tid, row = at / S::kVC;
-      const int ch = (at - row * S::kVC) ^ value_swizzle<S::kVC>(row);
-      const int64_t src = t.first_row + (j0 + row < t.hi ? j0 + row : t.hi - 1);
-      __builtin_amdgcn_global_load_lds((const void*)(a.kv + src * a.kv_stride + head * 2 * HD + HD + ch * 8),
-                                       (lds_ptr_t)(buf + S::kV + (k * NW + wv) * 1024), 16, 0, 0);
+    for (int k = 0; k < kCopies; ++k) {
+      const uint16_t* at = from[k];
+      if (left < kTB) {
+        const int row = row_of(k);
+        if (row >= left) at -= int64_t(row - left + 1) * (step[k] / 2);
+      }
+      __builtin_amdgcn_global_load_lds((const void*)at, (lds_ptr_t)(buf + (k * NW + wv) * 1024), 16, 0, 0);
+      from[k] += uint64_t(step[k]) * (kTB / 2);
     }
   };
 
@@ -174,7 +187,7 @@ __global__ __launch_bounds__(NW* kWave, NW / 4) void k_expanded(ExpandedArgs a) 
     if (live < kTB) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll 1
-      for (int k = 0; k < kValueCopies; ++k) {
+      for (int k = 0; k < kCopies - kKeyCopies; ++k) {
         const int at = k * S::kThreads + tid;
         if (at / S::kVC >= live) *reinterpret_cast<u32x4*>(buf + S::kV + at * 16) = u32x4{0u, 0u, 0u, 0u};
       }
@@ -214,13 +227,8 @@ __global__ __launch_bounds__(NW* kWave, NW / 4) void k_expanded(ExpandedArgs a) 
           for (int e = 0; e < 4; ++e) {
             const int row = j0 + tb * 16 + 4 * g + e;
             const bool seen = row < t.hi && row <= qrow[mb] && (a.rq.window <= 0 || row > qrow[mb] - a.rq.window);
-            s[tb][mb][e] = seen ? s[tb][mb][e] * a.scale_log2 : -kInf;
+            s[tb][mb][e] = seen ? s[tb][mb][e] : -kInf;
           }
-    } else {
-#pragma unroll
-      for (int tb = 0; tb < kTB / 16; ++tb)
-#pragma unroll
-        for (int mb = 0; mb < RB; ++mb) s[tb][mb] *= a.scale_log2;
     }
     // ---- softmax
     float m_new[RB];
@@ -232,7 +240,7 @@ __global__ __launch_bounds__(NW* kWave, NW / 4) void k_expanded(ExpandedArgs a) 
       for (int tb = 0; tb < kTB / 16; ++tb)
 #pragma unroll
         for (int e = 0; e < 4; ++e) m = fmaxf(m, s[tb][mb][e]);
-      m = quad_max(m);
+      m = quad_max(m) * a.scale_log2;  // (the scale is positive: its sign is in the queries)
       m_new[mb] = m;
       grow |= m > m_run[mb] + kGrow;
     }
@@ -254,7 +262,7 @@ __global__ __launch_bounds__(NW* kWave, NW / 4) void k_expanded(ExpandedArgs a) 
       for (int tb = 0; tb < kTB / 16; ++tb) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          s[tb][mb][e] = __builtin_amdgcn_exp2f(s[tb][mb][e] - ref);
+          s[tb][mb][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[tb][mb][e], a.scale_log2, -ref));
           l_own[mb] += s[tb][mb][e];
         }
         p[tb >> 1][mb][(tb & 1) * 2] = pack_bf16x2(s[tb][mb][0], s[tb][mb][1]);

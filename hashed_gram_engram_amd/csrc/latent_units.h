@@ -13,7 +13,9 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4_t;
 
 constexpr float kInf = __builtin_inff();
-constexpr float kGrow = 8.0f;  // a reference maximum moves when it is passed by more than a factor 2^8
+// A reference maximum moves when it is passed by more than a factor 2^16: weights up to that cost nothing in fp32 sums
+// and bf16 weights, and accumulators are rarely scaled.
+constexpr float kGrow = 16.0f;
 
 // 16-byte chunk c of row r lies at position c ^ swizzle(r): 16 rows' reads of one chunk cover all 64 banks once
 // (rows start at even multiples of 128 bytes or odd ones by turns), and so do 8 rows' transposed reads of
@@ -107,12 +109,14 @@ struct Units {
 template <int THREADS, int M, int STAGE>
 __device__ __forceinline__ bool my_units(const LatentRequests& q, int heads, Part* parts, int64_t* misc, Units* out) {
   const int tid = threadIdx.x, items = (q.R + THREADS - 1) / THREADS, r0 = tid * items, G = gridDim.x;
-  int64_t mine = 0, total;
-  for (int k = r0; k < r0 + items && k < q.R; ++k) {
+  auto units_of = [&](int k) -> int64_t {
     int tiles, stages;
     tiles_of<M, STAGE>(span_of(q, k), heads, &tiles, &stages);
-    mine += int64_t(tiles) * stages;
-  }
+    return int64_t(tiles) * stages;
+  };
+  const int64_t first = r0 < q.R ? units_of(r0) : 0;  // (up to THREADS requests: each has one)
+  int64_t mine = first, total;
+  for (int k = r0 + 1; k < r0 + items && k < q.R; ++k) mine += units_of(k);
   const int64_t before = block_scan64<THREADS>(mine, misc + 2, &total);
   // where every workgroup has work, an XCD takes neighbours (they share tiles' rows); else all XCDs take some
   const int n = total < G ? int(total) : G;
@@ -129,18 +133,14 @@ __device__ __forceinline__ bool my_units(const LatentRequests& q, int heads, Par
   out->u = out->begin(w);  // (each of the n has a unit at least: a tile's parts are neighbours)
   out->u1 = out->begin(w + 1);
   if (out->u >= before && out->u < before + mine) {
-    int64_t at = before;
-    for (int k = r0; k < r0 + items && k < q.R; ++k) {
-      int tiles, stages;
-      tiles_of<M, STAGE>(span_of(q, k), heads, &tiles, &stages);
-      const int64_t units = int64_t(tiles) * stages;
-      if (out->u < at + units) {
-        misc[0] = k;
-        misc[1] = out->u - at;
-        break;
-      }
+    int64_t at = before, units = first;
+    int k = r0;
+    while (out->u >= at + units) {
       at += units;
+      units = units_of(++k);
     }
+    misc[0] = k;
+    misc[1] = out->u - at;
   }
   __syncthreads();
   out->r = __builtin_amdgcn_readfirstlane(int(misc[0]));

@@ -429,13 +429,15 @@ size_t engram_linear_workspace_bytes_up_to(const engram_linear_layout* layout, i
  * token_start, start_pos, slots are a plan's (engram_batch_plan_out); the new tokens of request r are flat
  * tokens token_start[r] .. token_start[r + 1] - 1, at positions start_pos[r] .. .  Whatever these arrays
  * hold, no access leaves the tensors: token ranges are cut to n_tokens, positions to max_blocks * block_size.
- * The ranges of different requests must not overlap (a plan's do not).  At most 4096 requests.
+ * The ranges of different requests must not overlap (a plan's do not).  At most 4096 requests, and 2^31 - 1 slots
+ * (n_blocks * block_size) in a cache, else ENGRAM_E_LAYOUT.
  * The conventions above hold; calls that write different buffers may overlap in time. */
 
 /* A cache row (one slot of a page), engram_latent_row_bytes() bytes.
  * BF16: latent_dim, then rope_dim bf16.  MXFP8: latent_dim e4m3fn codes; 16 bytes, the first
  * latent_dim / 32 of them E8M0 scales, one per 32 features; rope_dim bf16.  A feature is
- * e4m3(code) * 2^(scale - 127), which bf16 holds exactly wherever engram_latent_write made it. */
+ * e4m3(code) * 2^(scale - 127), which bf16 holds exactly wherever engram_latent_write made it (scales 1 .. 247;
+ * engram_latent_read takes any, the attentions these). */
 typedef enum { ENGRAM_CACHE_BF16 = 0, ENGRAM_CACHE_MXFP8 = 1 } engram_cache_format;
 
 typedef struct {
@@ -458,8 +460,8 @@ size_t engram_latent_row_bytes(const engram_latent_layout* layout);
  *          one past the pool too and adds 1 to *err_count.  Two tokens must not share a slot (a plan's do
  *          not): its row then holds parts of either.
  *   cache  [n_blocks, block_size, row bytes] in/out
- * MXFP8: the scale of a block of 32 features is the least power of two, 2^-127 at least, that brings its finite
- * magnitudes within 448 (a block of zeros takes 2^-127); codes are rounded to nearest even (with the scale 2^120 to
+ * MXFP8: the scale of a block of 32 features is the least power of two, 2^-126 at least, that brings its finite
+ * magnitudes within 448; codes are rounded to nearest even (with the scale 2^120 to
  * 240 at most: the next code stands for 2^128, which bf16 has not); a feature that is not finite becomes a
  * NaN code.  The rope part keeps its bits, as BF16 rows do. */
 engram_status engram_latent_write(const engram_latent_layout* layout, const engram_page_layout* pages,

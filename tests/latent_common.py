@@ -39,7 +39,7 @@ def quantise_row(x):
     for b in range(len(x) // 32):
         v = x[32 * b: 32 * b + 32]
         top = max([abs(a) for a in v if math.isfinite(a)], default=0.0)
-        byte = 0
+        byte = 1
         while top > 448 * 2.0 ** (byte - 127):
             byte += 1
         scales[b] = byte
