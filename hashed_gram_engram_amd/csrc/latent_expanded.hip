@@ -206,16 +206,24 @@ __global__ __launch_bounds__(NW* kWave, NW / 4) void k_expanded(ExpandedArgs a) 
     for (int tb = 0; tb < kTB / 16; ++tb)
 #pragma unroll
       for (int mb = 0; mb < RB; ++mb) s[tb][mb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // (a step's keys are read one step before its products: 128 cycles of this wave, and as many of its neighbour's)
+    auto key = [&](int kb, int tb) {
+      return *reinterpret_cast<const u32x4*>(buf + (key_at ^ (kb % S::kKeyTurn * 64)) + kb / S::kKeyTurn * S::kKeyTurn * 64 + tb * 16 * S::kKC * 16);
+    };
+    u32x4 kf[2][kTB / 16];
+#pragma unroll
+    for (int tb = 0; tb < kTB / 16; ++tb) kf[0][tb] = key(0, tb);
 #pragma unroll
     for (int kb = 0; kb < S::kKB; ++kb) {
-      if (kb == HD / 32 + 1 && rkb == 1) continue;
-      const char* at = buf + (key_at ^ (kb % S::kKeyTurn * 64)) + kb / S::kKeyTurn * S::kKeyTurn * 64;
+      if (kb + 1 < S::kKB)
 #pragma unroll
-      for (int tb = 0; tb < kTB / 16; ++tb) {
-        const u32x4 k = *reinterpret_cast<const u32x4*>(at + tb * 16 * S::kKC * 16);
+        for (int tb = 0; tb < kTB / 16; ++tb) kf[(kb + 1) & 1][tb] = key(kb + 1, tb);
+      if (kb < HD / 32 + 1 || rkb == 2)
 #pragma unroll
-        for (int mb = 0; mb < RB; ++mb) s[tb][mb] = mfma16x16x32(k, qf[mb][kb], s[tb][mb]);
-      }
+        for (int tb = 0; tb < kTB / 16; ++tb)
+#pragma unroll
+          for (int mb = 0; mb < RB; ++mb) s[tb][mb] = mfma16x16x32(kf[kb & 1][tb], qf[mb][kb], s[tb][mb]);
+      __builtin_amdgcn_sched_barrier(0);
     }
     const bool differ = j0 + kTB - 1 > w_min || (a.rq.window > 0 && j0 <= w_max - a.rq.window);
     if (live < kTB || differ || wn < RB * 16) {
@@ -309,17 +317,25 @@ __global__ __launch_bounds__(NW* kWave, NW / 4) void k_expanded(ExpandedArgs a) 
     }
     if (skip) continue;
     // ---- values
+    auto value = [&](int k) {  // rows 32 (k / (HD / 16)) .., features 16 (k % (HD / 16)) ..
+      const int fb = k % (HD / 16);
+      const char* at = vb + (value_at ^ (fb % S::kValueTurn * 32)) + fb / S::kValueTurn * S::kValueTurn * 32 + k / (HD / 16) * 32 * S::kVC * 16;
+      const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)at));
+      const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(at + 16 * S::kVC * 16)));
+      return u32x4{lo.x, lo.y, hi.x, hi.y};
+    };
+    constexpr int kDeep = 5, kSteps = kTB / 32 * (HD / 16);
+    u32x4 vf[kDeep];
 #pragma unroll
-    for (int ks = 0; ks < kTB / 32; ++ks)
+    for (int k = 0; k < kDeep - 1; ++k) vf[k] = value(k);
 #pragma unroll
-      for (int fb = 0; fb < HD / 16; ++fb) {
-        const char* at = vb + (value_at ^ (fb % S::kValueTurn * 32)) + fb / S::kValueTurn * S::kValueTurn * 32 + ks * 32 * S::kVC * 16;
-        const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)at));
-        const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(at + 16 * S::kVC * 16)));
-        const u32x4 v = {lo.x, lo.y, hi.x, hi.y};
+    for (int k = 0; k < kSteps; ++k) {
+      if (k + kDeep - 1 < kSteps) vf[(k + kDeep - 1) % kDeep] = value(k + kDeep - 1);
 #pragma unroll
-        for (int mb = 0; mb < RB; ++mb) acc[fb][mb] = mfma16x16x32(v, p[ks][mb], acc[fb][mb]);
-      }
+      for (int mb = 0; mb < RB; ++mb)
+        acc[k % (HD / 16)][mb] = mfma16x16x32(vf[k % kDeep], p[k / (HD / 16)][mb], acc[k % (HD / 16)][mb]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
 
   // ---- outputs, or a part: [part, token, head, HD + 2] fp32 with the maximum and the sum at the end
