@@ -3,12 +3,16 @@
 // A row of a tile is a (token, head) pair of one request, M = 16 MB rows to a tile; a tile goes over its
 // positions in stages of 64 rows of the cache, which lie in LDS as bf16 (FP8 rows are converted on the way in,
 // exactly), read twice: along the features for the scores, and transposed (ds_read_tr16) for the values.
-//  scores   S^T = C Q^T: a wave takes 16 (MB 4: 32) of the positions and keeps its queries in registers; a lane
-//           then holds 4 consecutive positions of one query.
+//  scores   S^T = C Q^T: a wave takes 16 of the positions and keeps all queries in registers; a lane then holds 4
+//           consecutive positions of one query.
 //  softmax  running maximum and sum in the base 2; the waves share each stage's maxima through LDS; a maximum
 //           that grows by less than 2^16 leaves the reference where it is.
 //  values   out^T += C^T P^T: a wave takes a quarter of the latent's features for every query; the weights
-//           pass through LDS as bf16, the order of positions in the product being that of the score fragments.
+//           pass through LDS, rounded to bf16 for the product (their sum is of the unrounded ones), the order of
+//           positions in the product being that of the score fragments.
+//
+// For 32 rows a request and fewer, where the cache's bytes are what costs: 128 requests of up to 8192 positions, 16 heads,
+// BF16 rows of 512 + 64: 175 us for 793 MB, 4.5 TB/s.
 //
 // Work is shared out in units of one stage of one tile: workgroup w of G takes units [w U / G, (w + 1) U / G) of
 // the step's U, whatever the requests' lengths, so every CU has the same share.  What a workgroup holds of a
@@ -17,7 +21,7 @@
 //
 // Rows that take no part (outside the tile's positions, on a bad page) are zeros in LDS and their scores
 // -infinity.  Where the tokens of a tile see different positions, a value that is not finite must not reach those that do
-// not see it (0 times infinity): such stages are looked through and, if they hold one, added by plain_values.
+// not see it (0 times infinity): such stages are looked through, and rows with one added where they are seen, one by one.
 #include "latent_units.h"
 
 namespace engram {
@@ -33,8 +37,6 @@ struct Shape {
   static constexpr int kChunks = (DC + 64) / 8, kRowB = kChunks * 16;  // of a row in LDS
   static constexpr int kKB = DC / 32;                                  // K blocks of the latent
   static constexpr int kFB = DC / 64;                                  // 16-feature blocks of a wave's quarter
-  static constexpr int kQSplit = MB == 4 ? 2 : 1;                      // the waves share the queries in so many parts
-  static constexpr int kMBQ = MB / kQSplit, kTBQ = kQSplit, kTG = 4 / kQSplit;
   static constexpr int kStageB = kTB * kRowB;
   static constexpr int kP = 2 * kStageB;                               // offsets into LDS
   static constexpr int kMax = kP + M * kTB * 2;
@@ -50,7 +52,6 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i16 = lane & 15, g = lane >> 4;
-  const int rh = wv % S::kQSplit, tg = wv / S::kQSplit;
   const int rkb = a.rope_dim / 32;
   const int row_b = latent_row_bytes(DC, a.rope_dim, FP8);
   int64_t* slots = reinterpret_cast<int64_t*>(lds + S::kSlots);
@@ -61,7 +62,7 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
   const PartSpace space = part_space(a.workspace, gridDim.x, S::M);
   // A chunk's place differs from row to row in the low three bits of its number only, so the reads of a stage take
   // two (keys) and four (values) addresses and constants.  (Rows start at multiples of 128 bytes.)
-  const int key_at = (tg * S::kTBQ * 16 + i16) * S::kRowB + (g ^ latent_swizzle(i16)) * 16;
+  const int key_at = (wv * 16 + i16) * S::kRowB + (g ^ latent_swizzle(i16)) * 16;
   const int vrow = 4 * g + (i16 >> 2);
   const int value_at = vrow * S::kRowB + ((wv * (DC / 32) + ((i16 & 3) >> 1)) ^ latent_swizzle(vrow)) * 16 + (i16 & 1) * 8;
   Units un;
@@ -72,11 +73,11 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
     const int c0 = t.c0, n = t.n;
 
     // ---- queries: fragments in registers, and the position of each row's token (-1: no row)
-    u32x4 qf[S::kMBQ][S::kKB + 2];
-    int qpos[S::kMBQ];
+    u32x4 qf[MB][S::kKB + 2];
+    int qpos[MB];
 #pragma unroll
-    for (int mb = 0; mb < S::kMBQ; ++mb) {
-      const int row = t.row0 + (rh * S::kMBQ + mb) * 16 + i16, at = row < t.rows ? row : t.rows - 1;  // (rows past the last repeat it)
+    for (int mb = 0; mb < MB; ++mb) {
+      const int row = t.row0 + mb * 16 + i16, at = row < t.rows ? row : t.rows - 1;  // (rows past the last repeat it)
       const int tok = at / a.heads, head = at - tok * a.heads;
       qpos[mb] = row < t.rows ? t.s.pos + tok : -1;
       const uint16_t* src = a.q + (t.s.first + tok) * a.q_stride + int64_t(head) * (DC + a.rope_dim) + 8 * g;
@@ -85,7 +86,7 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
         qf[mb][kb] = *reinterpret_cast<const u32x4*>(src + 32 * (kb < S::kKB + rkb ? kb : 0)) ^ a.q_sign;
     }
     f32x4 acc[S::kFB][MB];
-    float m_run[MB], l_own[S::kMBQ];
+    float m_run[MB], l_own[MB];
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
       m_run[mb] = -kInf;
@@ -93,7 +94,7 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
       for (int fb = 0; fb < S::kFB; ++fb) acc[fb][mb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 #pragma unroll
-    for (int mb = 0; mb < S::kMBQ; ++mb) l_own[mb] = 0.0f;
+    for (int mb = 0; mb < MB; ++mb) l_own[mb] = 0.0f;
 
     // ---- staging
     auto find_slot = [&](int c) -> int64_t {  // (wave 0) slot of the lane's row of stage c
@@ -203,30 +204,22 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
       if (wv == 0) slot2 = find_slot(c + 2);
 
       // ---- scores
-      f32x4 s[S::kTBQ][S::kMBQ];
+      f32x4 s[MB];
 #pragma unroll
-      for (int tb = 0; tb < S::kTBQ; ++tb)
-#pragma unroll
-        for (int mb = 0; mb < S::kMBQ; ++mb) s[tb][mb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int mb = 0; mb < MB; ++mb) s[mb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       {
         const char* kp[2] = {buf + key_at, buf + (key_at ^ 64)};
-        auto key = [&](int kb, int tb) { return *reinterpret_cast<const u32x4*>(kp[kb & 1] + tb * 16 * S::kRowB + (kb >> 1) * 128); };
+        auto key = [&](int kb) { return *reinterpret_cast<const u32x4*>(kp[kb & 1] + (kb >> 1) * 128); };
         constexpr int kDeep = 4;
-        u32x4 kf[kDeep][S::kTBQ];
+        u32x4 kf[kDeep];
 #pragma unroll
-        for (int kb = 0; kb < kDeep - 1; ++kb)
-#pragma unroll
-          for (int tb = 0; tb < S::kTBQ; ++tb) kf[kb][tb] = key(kb, tb);
+        for (int kb = 0; kb < kDeep - 1; ++kb) kf[kb] = key(kb);
 #pragma unroll
         for (int kb = 0; kb < S::kKB + 2; ++kb) {
-          if (kb + kDeep - 1 < S::kKB + 2)
-#pragma unroll
-            for (int tb = 0; tb < S::kTBQ; ++tb) kf[(kb + kDeep - 1) % kDeep][tb] = key(kb + kDeep - 1, tb);
+          if (kb + kDeep - 1 < S::kKB + 2) kf[(kb + kDeep - 1) % kDeep] = key(kb + kDeep - 1);
           if (kb == S::kKB + 1 && rkb == 1) continue;
 #pragma unroll
-          for (int tb = 0; tb < S::kTBQ; ++tb)
-#pragma unroll
-            for (int mb = 0; mb < S::kMBQ; ++mb) s[tb][mb] = mfma16x16x32(kf[kb % kDeep][tb], qf[mb][kb], s[tb][mb]);
+          for (int mb = 0; mb < MB; ++mb) s[mb] = mfma16x16x32(kf[kb % kDeep], qf[mb][kb], s[mb]);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -235,27 +228,20 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
       const bool differ = t.p_min != t.p_max && (j0 + kTB - 1 > t.p_min || (a.rq.window > 0 && j0 <= t.p_max - a.rq.window));
       const bool edge = on != ~uint64_t(0) || differ;
 #pragma unroll
-      for (int tb = 0; tb < S::kTBQ; ++tb)
-#pragma unroll
-        for (int mb = 0; mb < S::kMBQ; ++mb)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[tb][mb][e] *= a.scale_log2;
-            if (edge) {
-              const int row = (tg * S::kTBQ + tb) * 16 + 4 * g + e, pos = j0 + row;
-              const bool seen = ((on >> row) & 1) && pos <= qpos[mb] && (a.rq.window <= 0 || pos > qpos[mb] - a.rq.window);
-              s[tb][mb][e] = seen ? s[tb][mb][e] : -kInf;
-            }
-          }
-#pragma unroll
-      for (int mb = 0; mb < S::kMBQ; ++mb) {
+      for (int mb = 0; mb < MB; ++mb) {
         float m = -kInf;
 #pragma unroll
-        for (int tb = 0; tb < S::kTBQ; ++tb)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) m = fmaxf(m, s[tb][mb][e]);
+        for (int e = 0; e < 4; ++e) {
+          s[mb][e] *= a.scale_log2;
+          if (edge) {
+            const int row = wv * 16 + 4 * g + e, pos = j0 + row;
+            const bool seen = ((on >> row) & 1) && pos <= qpos[mb] && (a.rq.window <= 0 || pos > qpos[mb] - a.rq.window);
+            s[mb][e] = seen ? s[mb][e] : -kInf;
+          }
+          m = fmaxf(m, s[mb][e]);
+        }
         m = quad_max(m);
-        if (g == 0) smax[tg * S::M + (rh * S::kMBQ + mb) * 16 + i16] = m;
+        if (g == 0) smax[wv * S::M + mb * 16 + i16] = m;
       }
       if (wv == 0) put_slot(c + 2, slot2);
       wait_lds_barrier();
@@ -267,7 +253,7 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
       for (int mb = 0; mb < MB; ++mb) {
         float m = smax[mb * 16 + i16];
 #pragma unroll
-        for (int k = 1; k < S::kTG; ++k) m = fmaxf(m, smax[k * S::M + mb * 16 + i16]);
+        for (int k = 1; k < 4; ++k) m = fmaxf(m, smax[k * S::M + mb * 16 + i16]);
         m_new[mb] = m;
         grow |= m > m_run[mb] + kGrow;
       }
@@ -279,33 +265,22 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
           m_run[mb] = m;
 #pragma unroll
           for (int fb = 0; fb < S::kFB; ++fb) acc[fb][mb] *= alpha;
-          if (mb / S::kMBQ == rh) {
-#pragma unroll
-            for (int k = 0; k < S::kMBQ; ++k)
-              if (mb % S::kMBQ == k) l_own[k] *= alpha;
-          }
+          l_own[mb] *= alpha;
         }
       }
 #pragma unroll
-      for (int mb = 0; mb < S::kMBQ; ++mb) {
-        float ref = 0.0f;
+      for (int mb = 0; mb < MB; ++mb) {
+        const float ref = m_run[mb] == -kInf ? 0.0f : m_run[mb];
+        const int row = mb * 16 + i16;
+        float p[4];
 #pragma unroll
-        for (int k = 0; k < S::kQSplit; ++k)
-          if (rh == k) ref = m_run[k * S::kMBQ + mb];
-        ref = ref == -kInf ? 0.0f : ref;
-        const int row = (rh * S::kMBQ + mb) * 16 + i16;
-#pragma unroll
-        for (int tb = 0; tb < S::kTBQ; ++tb) {
-          float p[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            p[e] = __builtin_amdgcn_exp2f(s[tb][mb][e] - ref);
-            l_own[mb] += p[e];
-          }
-          const int blk = tg * S::kTBQ + tb;  // positions 16 blk + 4 g .. : half blk & 1 of K block blk / 2
-          *reinterpret_cast<u32x2*>(lds + S::kP + row * kTB * 2 + (((blk >> 1) * 4 + g) ^ ((row >> 1) & 7)) * 16 + (blk & 1) * 8) =
-              u32x2{pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3])};
+        for (int e = 0; e < 4; ++e) {
+          p[e] = __builtin_amdgcn_exp2f(s[mb][e] - ref);
+          l_own[mb] += p[e];
         }
+        // (the wave's positions 16 wv + 4 g ..: half wv & 1 of K block wv / 2)
+        *reinterpret_cast<u32x2*>(lds + S::kP + row * kTB * 2 + (((wv >> 1) * 4 + g) ^ ((row >> 1) & 7)) * 16 + (wv & 1) * 8) =
+            u32x2{pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3])};
       }
       if constexpr (FP8) {
         if (j + 1 < n) store_stage(c + 1, next);
@@ -316,19 +291,17 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
       // ---- values that are not finite, where the tile's tokens see different positions: added row by row where they are
       // seen, and zeros for the product
       if (differ) {
+        uint64_t odd = 0;
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          uint32_t odd = 0;
+        for (int k = tid; k < kTB * DC / 8; k += kThreads) {
+          const int row = k / (DC / 8);
+          if (any_not_finite(*reinterpret_cast<const u32x4*>(buf + row * S::kRowB + k % (DC / 8) * 16))) odd |= uint64_t{1} << row;
+        }
+        odd = any_rows(odd, misc);
+        if (__builtin_expect(odd != 0, 0)) {
 #pragma unroll 1
-          for (int k = tid; k < 32 * DC / 8; k += kThreads) {
-            const int row = k / (DC / 8);
-            if (any_not_finite(*reinterpret_cast<const u32x4*>(buf + (half * 32 + row) * S::kRowB + k % (DC / 8) * 16))) odd |= 1u << row;
-          }
-          odd = any_rows(odd, misc);
-          if (__builtin_expect(odd == 0, 1)) continue;
-#pragma unroll 1
-          for (uint32_t left = odd; left != 0; left &= left - 1) {
-            const int in = __builtin_ctz(left), row = half * 32 + in, pos = j0 + row;
+          for (uint64_t left = odd; left != 0; left &= left - 1) {
+            const int row = __builtin_ctzll(left), half = row >> 5, in = row & 31, pos = j0 + row;
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
               const int m = mb * 16 + i16, q = t.row0 + m, qp = q < t.rows ? t.s.pos + q / a.heads : -1;
@@ -347,9 +320,8 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
             }
           }
           wait_lds_barrier();
-          for (int k = tid; k < 32 * DC / 8; k += kThreads)
-            if ((odd >> (k / (DC / 8))) & 1)
-              *reinterpret_cast<u32x4*>(buf + (half * 32 + k / (DC / 8)) * S::kRowB + k % (DC / 8) * 16) = u32x4{0u, 0u, 0u, 0u};
+          for (int k = tid; k < kTB * DC / 8; k += kThreads)
+            if ((odd >> (k / (DC / 8))) & 1) *reinterpret_cast<u32x4*>(buf + k / (DC / 8) * S::kRowB + k % (DC / 8) * 16) = u32x4{0u, 0u, 0u, 0u};
           wait_lds_barrier();
         }
       }
@@ -385,9 +357,9 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
 
     // ---- the sums of all positions, then the outputs or a part
 #pragma unroll
-    for (int mb = 0; mb < S::kMBQ; ++mb) {
+    for (int mb = 0; mb < MB; ++mb) {
       const float l = quad_sum(l_own[mb]);
-      if (g == 0) smax[tg * S::M + (rh * S::kMBQ + mb) * 16 + i16] = l;
+      if (g == 0) smax[wv * S::M + mb * 16 + i16] = l;
     }
     wait_lds_barrier();
     float l_all[MB];
@@ -395,7 +367,7 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
     for (int mb = 0; mb < MB; ++mb) {
       l_all[mb] = smax[mb * 16 + i16];
 #pragma unroll
-      for (int k = 1; k < S::kTG; ++k) l_all[mb] += smax[k * S::M + mb * 16 + i16];
+      for (int k = 1; k < 4; ++k) l_all[mb] += smax[k * S::M + mb * 16 + i16];
     }
     if (c0 == 0 && n == t.stages) {
 #pragma unroll
@@ -443,8 +415,7 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
 
 template <int DC, int MB>
 __global__ __launch_bounds__(kThreads) void k_absorbed_join(AbsorbedArgs a, int G) {
-  constexpr int kFB = DC / 64;  // of a wave's quarter
-  join_parts<DC, 16 * MB>(a, G, [](int blk, int fb) { return (fb / kFB * kFB + fb % kFB) * MB + blk; });
+  join_parts<DC, 16 * MB>(a, G, [](int blk, int fb) { return fb * MB + blk; });
 }
 
 template <int DC, int MB, bool FP8>

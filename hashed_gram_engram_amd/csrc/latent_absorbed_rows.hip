@@ -100,7 +100,6 @@ struct Shape {
   static constexpr int kSlots = kPlaces + 4 * kRing * kTB * 4;
   static constexpr int kMisc = kSlots + 4 * kSlotRing * kTB * 4;
   static constexpr int kBytes = kMisc + 64;
-  static constexpr int kPerCU = 2 * kBytes <= 160 * 1024 ? 2 : 1;
 };
 
 template <int DC, int RB, bool FP8>
@@ -115,6 +114,7 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed_rows(A
   int32_t* slots = reinterpret_cast<int32_t*>(lds + S::kSlots) + wv * kSlotRing * kTB;
   int32_t* places = reinterpret_cast<int32_t*>(lds + S::kPlaces) + wv * kRing * kTB;
   int64_t* misc = reinterpret_cast<int64_t*>(lds + S::kMisc);
+  const uint32_t lds_at = lds_address(lds);
   const PartSpace space = part_space(a.workspace, gridDim.x, S::M);
   Units un;
   if (!my_units<kThreads, S::M, kTB>(a.rq, a.heads, space.parts, misc, &un)) return;
@@ -175,7 +175,7 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed_rows(A
     auto copy_pages = [&](int c) {  // stages one after the other
       const int row = lane_now() & 31;
       const int e = entry < a.rq.max_blocks ? entry : a.rq.max_blocks - 1;
-      __builtin_amdgcn_global_load_lds((const void*)(table + e), (lds_ptr_t)(pages + (c & (kRing - 1)) * 64), 4, 0, 0);
+      copy_to_lds<4>(table + e, lds_at + S::kPages + (wv * kRing + (c & (kRing - 1))) * 256);
       places[(c & (kRing - 1)) * kTB + row] = place;
       entry += a.rq.stage_pages;
       place += a.rq.stage_rest;
@@ -228,13 +228,12 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed_rows(A
       const uint64_t at = uint64_t(uint32_t(slot)) * uint32_t(row_b);
       if constexpr (FP8) {
         const uint8_t* from = k < S::kCodeCopies ? p.code_from : (k == S::kCodeCopies ? p.rope_from : a.cache + DC);
-        __builtin_amdgcn_global_load_lds((const void*)(from + at), (lds_ptr_t)(lds + S::kRaw + (c % S::kRaws) * S::kRawB + (k * 4 + wv) * 1024), 16, 0, 0);
+        copy_to_lds<16>(from + at, lds_at + S::kRaw + (c % S::kRaws) * S::kRawB + (k * 4 + wv) * 1024);
       } else {
         const int id = k * kThreads + wv * kWave + lane_now(), r = id / S::kChunks;
         int ch = (id - r * S::kChunks) ^ latent_swizzle(r);
         ch = ch < DC / 8 + 4 * rkb ? ch : 0;  // (a place that is not read)
-        __builtin_amdgcn_global_load_lds((const void*)(a.cache + at + ch * 16),
-                                         (lds_ptr_t)(lds + (c % S::kBufs) * S::kStageB + (k * 4 + wv) * 1024), 16, 0, 0);
+        copy_to_lds<16>(a.cache + at + ch * 16, lds_at + (c % S::kBufs) * S::kStageB + (k * 4 + wv) * 1024);
       }
     };
     auto copy_stage = [&](int c) {
@@ -471,7 +470,7 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed_rows(A
           const u32x4 v = *reinterpret_cast<const u32x4*>(buf + row * S::kRowB + k % (DC / 8) * 16);
           if (any_not_finite(v)) odd |= 1u << row;
         }
-        odd = any_rows(odd, misc);
+        odd = uint32_t(any_rows(odd, misc));
         if (__builtin_expect(odd != 0, 0)) {
           char* mem = acc_memory();
           acc_to_memory(acc, mem);
@@ -538,6 +537,7 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed_rows(A
 #pragma unroll
       for (int k = 0; k <= kCopyStage; ++k) on_ring[k] = on_ring[k + 1];
     }
+    wait_copies<0>();  // (none is in flight when LDS goes to another workgroup)
 
     // ---- the outputs, or a part
 #pragma unroll

@@ -22,7 +22,7 @@ engram_status launched(hipError_t e) { return e == hipSuccess ? ENGRAM_OK : ENGR
 hipStream_t hip_stream(engram_stream_t s) { return reinterpret_cast<hipStream_t>(s); }
 
 // Elements between rows of `row` elements: at least so many, whole 16 bytes, offsets far from 64 bits.
-bool stride_ok(int64_t stride, int64_t row) { return stride >= row && stride % 8 == 0 && stride <= (int64_t(1) << 31); }
+bool stride_ok(int64_t stride, int64_t row) { return stride >= row && stride % 8 == 0 && stride <= (int64_t(1) << 28); }
 
 // The checks that both attentions and the read share; fills `q`.
 engram_status requests(const engram_latent_layout* l, const int32_t* token_start, const int32_t* start_pos, int64_t R,

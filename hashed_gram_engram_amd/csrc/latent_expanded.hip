@@ -2,17 +2,24 @@
 //
 // A workgroup takes M = 16 RB NW tokens of one request and one head; each of its NW waves holds the queries of
 // 16 RB tokens in registers.  Keys and values come through LDS in stages of 64 rows, copied straight from
-// memory, two buffers.  S^T = K Q^T leaves a lane with 4 consecutive keys of one query, which is an operand
+// memory.  S^T = K Q^T leaves a lane with 4 consecutive keys of one query, which is an operand
 // of out^T += V^T P^T as it stands if the keys of that product are counted in the same order: the weights never
 // leave the registers, and a query's maximum and sum are shared by 4 lanes of one wave.  Values are read
 // transposed (ds_read_tr16).  The softmax is in the base 2; a maximum that grows by less than 2^16 leaves the
-// reference where it is.
+// reference where it is.  The weights are rounded to bf16 for the second product, their sum is of the unrounded ones.
+//
+// Large tiles: eight waves, two on each SIMD, the second four half a stage behind (a barrier after each half), so that one of
+// a SIMD's two is at its products while the other is at its softmax; with all eight in step, 8192 tokens by 64 heads of
+// 128 features took 1.64 ms, so 1.49 (0.92 PFLOP/s; with neither softmax, copies nor reads of LDS the products alone take
+// 1.04: they run at the power limit).
 //
 // Where few tiles meet many rows, each tile's stages are shared out in parts; their fp32 sums go to the workspace
 // and k_expanded_join adds them in order.
 //
 // Rows past the last stay zeros in LDS; where a stage holds a value that is not finite and tokens see different
 // rows of it, the product is taken row by row, only where it is seen (0 times infinity would not be 0).
+#include <type_traits>
+
 #include "latent_units.h"
 
 namespace engram {
@@ -24,13 +31,18 @@ constexpr int kTB = 64;
 template <int HD, int NW, int RB>
 struct Shape {
   static constexpr int kThreads = NW * kWave, M = 16 * RB * NW;
-  static constexpr int kKC = (HD + 64) / 8, kVC = HD / 8;  // 16-byte chunks of a key and of a value in LDS
+  // a stage in LDS: the rows' own parts of the keys, their rope parts (64 places), and their values
+  static constexpr int kChunks = HD / 8;  // 16-byte chunks of a row's own part of a key, and of its value
+  static constexpr int kRowB = HD * 2;
   static constexpr int kKB = (HD + 64) / 32;
-  static constexpr int kKeyTurn = kKC % 16 == 0 ? 4 : 2;   // K blocks that a swizzle moves a chunk among
-  static constexpr int kValueTurn = kVC / 2;                  // 16-feature blocks, the same (8 or 4 pairs of chunks)
-  static constexpr int kV = kTB * kKC * 16;                // offset of the values
-  static constexpr int kStageB = kTB * (kKC + kVC) * 16;
-  static constexpr int kBytes = 2 * kStageB;
+  static constexpr int kRope = kTB * kRowB, kV = kRope + kTB * 128;  // offsets
+  static constexpr int kStageB = kV + kTB * kRowB;
+  static constexpr int kTurn = kChunks / 2;  // 16-feature blocks of a value among which a swizzle moves a pair of chunks
+  // Eight waves: two on each SIMD, and the second four are half a stage behind, so that one of a SIMD's two is at its
+  // products while the other is at its softmax.
+  static constexpr bool kTurns = NW == 8;
+  static constexpr int kBuffers = kTurns ? 3 : 2;
+  static constexpr int kBytes = kBuffers * kStageB;
 };
 
 // Chunk c of row r lies at c ^ swizzle: 16 rows' reads of a chunk of a key, and 8 rows' transposed reads of a
@@ -93,20 +105,22 @@ __device__ __forceinline__ uint32_t in_order(uint32_t b, uint32_t n) {  // an XC
 }
 
 template <int HD, int NW, int RB>
-__global__ __launch_bounds__(NW* kWave, NW / 4) void k_expanded(ExpandedArgs a) {
+__global__ __launch_bounds__(NW* kWave, 2) void k_expanded(ExpandedArgs a) {
   using S = Shape<HD, NW, RB>;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   __shared__ int64_t tmp[NW + 2];
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i16 = lane & 15, g = lane >> 4;
   const int rkb = a.rope_dim / 32;
-  // heads, then tiles (the last, which sees the most, first), then parts
+  // pairs of heads, then tiles (the last, which sees the most, first), then the pair's heads, then parts: neighbours share
+  // rows in their L2
   uint32_t id = in_order(blockIdx.x, gridDim.x);
   const int part = int(id % a.parts);
   id /= a.parts;
-  const int head = int(id / a.tiles);
+  const int pair = int(id / (2 * a.tiles)), in = int(id - pair * 2 * a.tiles), of = pair * 2 + 1 < a.heads ? 2 : 1;
+  const int head = pair * 2 + in % of;
   Tile t;
-  if (!find_tile<S::kThreads, S::M>(a, a.tiles - 1 - int(id - head * a.tiles), tmp, &t)) return;
+  if (!find_tile<S::kThreads, S::M>(a, a.tiles - 1 - in / of, tmp, &t)) return;
   const int stages_all = (t.hi - t.lo + kTB - 1) / kTB;
   const int c0 = int(int64_t(stages_all) * part / a.parts), c1 = int(int64_t(stages_all) * (part + 1) / a.parts);
 
@@ -127,10 +141,11 @@ __global__ __launch_bounds__(NW* kWave, NW / 4) void k_expanded(ExpandedArgs a) 
   const int t_min = t.s.pos + t.t0 - t.base;  // the last row that the tile's first token sees
   const int w_min = t.s.pos + t.t0 + w0 - t.base, w_max = w_min + wn - 1;  // (wn <= 0: no token)
 
-  // (a chunk's place differs from row to row in the low bits of its number only: addresses are one xor away from these)
-  const int key_at = i16 * S::kKC * 16 + (g ^ key_swizzle<S::kKC>(i16)) * 16;
+  // (a swizzle changes bits of a chunk's number, so a row's chunks are one xor away from the first)
+  const int key_at = i16 * S::kRowB + (g ^ key_swizzle<S::kChunks>(i16)) * 16;
+  const int rope_at = S::kRope + i16 * 128 + (g ^ key_swizzle<8>(i16)) * 16;
   const int vrow = 4 * g + (i16 >> 2);
-  const int value_at = vrow * S::kVC * 16 + (((i16 & 3) >> 1) ^ value_swizzle<S::kVC>(vrow)) * 16 + (i16 & 1) * 8;
+  const int value_at = S::kV + vrow * S::kRowB + (((i16 & 3) >> 1) ^ value_swizzle<S::kChunks>(vrow)) * 16 + (i16 & 1) * 8;
 
   f32x4 acc[HD / 16][RB];
   float m_run[RB], l_own[RB];
@@ -142,91 +157,125 @@ __global__ __launch_bounds__(NW* kWave, NW / 4) void k_expanded(ExpandedArgs a) 
     for (int fb = 0; fb < HD / 16; ++fb) acc[fb][mb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  // Copies: 16 bytes a lane, in the order of the buffer; keys, then values.  A lane's place in the rows moves on by a stage
-  // at a time; only the last stage may have fewer rows, those past the end then repeat the last.
-  constexpr int kKeyCopies = kTB * S::kKC / S::kThreads, kCopies = kKeyCopies + kTB * S::kVC / S::kThreads;
-  static_assert(kTB * S::kKC % S::kThreads == 0 && kTB * S::kVC % S::kThreads == 0, "whole copies");
-  const uint16_t* from[kCopies];
-  uint32_t step[kCopies];  // bytes from row to row
-  auto row_of = [&](int k) { return k < kKeyCopies ? (k * S::kThreads + tid) / S::kKC : ((k - kKeyCopies) * S::kThreads + tid) / S::kVC; };
-#pragma unroll
-  for (int k = 0; k < kCopies; ++k) {
-    const int row = row_of(k);
-    const uint16_t* base;
-    if (k < kKeyCopies) {
-      const int ch = (k * S::kThreads + tid - row * S::kKC) ^ key_swizzle<S::kKC>(row);
-      const bool own = ch < HD / 8;
-      base = own ? a.kv + head * 2 * HD + ch * 8 : a.rope + (ch - HD / 8 < 4 * rkb ? ch - HD / 8 : 0) * 8;
-      step[k] = uint32_t(own ? a.kv_stride : a.rope_stride) * 2;
-    } else {
-      const int ch = ((k - kKeyCopies) * S::kThreads + tid - row * S::kVC) ^ value_swizzle<S::kVC>(row);
-      base = a.kv + head * 2 * HD + HD + ch * 8;
-      step[k] = uint32_t(a.kv_stride) * 2;
-    }
-    from[k] = base + int64_t(t.first_row + t.lo + c0 * kTB + row) * (step[k] / 2);
-  }
-  auto copy_stage = [&](int c, char* buf) {
+  // Copies, by four of the waves: 16 bytes a lane in the order of the buffer, a few whole rows by each.  A lane's place from a
+  // copy's first row on is the same in all copies of a kind, which go through the rows in order, stage after stage.
+  // Only the last stage may have fewer rows: its last one is repeated.
+  constexpr int kPer = 64 / S::kChunks;  // rows of a copy
+  constexpr int kOwn = kTB / (kPer * 4), kRopes = kTB / (8 * 4), kCopies = 2 * kOwn + kRopes;
+  static_assert(kPer * 4 % 16 == 0, "the same swizzles in all copies of a wave");
+  const bool late = S::kTurns && wv >= 4;
+  const int cw = S::kTurns ? wv - 4 : wv, row_l = lane / S::kChunks, rope_l = lane >> 3;
+  const int rope_ch = (lane & 7) ^ key_swizzle<8>(cw * 8 + rope_l);
+  const uint32_t kv_step = uint32_t(a.kv_stride) * 2, rope_step = uint32_t(a.rope_stride) * 2;  // bytes from row to row
+  const uint32_t key_off = row_l * kv_step + (lane % S::kChunks ^ key_swizzle<S::kChunks>(cw * kPer + row_l)) * 16;
+  const uint32_t value_off = row_l * kv_step + (HD / 8 + (lane % S::kChunks ^ value_swizzle<S::kChunks>(cw * kPer + row_l))) * 16;
+  const uint32_t rope_off = rope_l * rope_step + (rope_ch < 4 * rkb ? rope_ch : 0) * 16;
+  const int64_t first_copied = t.first_row + t.lo + c0 * kTB;
+  const char* kv_from = reinterpret_cast<const char*>(a.kv + head * 2 * HD + (first_copied + cw * kPer) * a.kv_stride);
+  const char* rope_from = reinterpret_cast<const char*>(a.rope + (first_copied + cw * 8) * a.rope_stride);
+  const uint32_t to = lds_address(lds) + cw * 1024;
+  auto copy_stage = [&](int c, uint32_t buf) {
     const int left = t.hi - (t.lo + c * kTB);
-#pragma unroll
-    for (int k = 0; k < kCopies; ++k) {
-      const uint16_t* at = from[k];
+    auto copy = [&](int n, bool rope, uint32_t off, uint32_t at) {
+      const char* from = rope ? rope_from : kv_from;
       if (left < kTB) {
-        const int row = row_of(k);
-        if (row >= left) at -= int64_t(row - left + 1) * (step[k] / 2);
+        const int row = (n * 4 + cw) * (rope ? 8 : kPer), back = row < left ? 0 : row - (left - 1);
+        const int over = (rope ? rope_l : row_l) - (left - 1 - (row - back));
+        const uint32_t step = rope ? rope_step : kv_step;
+        if (over > 0) off -= over * step;
+        from -= int64_t(back) * step;
       }
-      __builtin_amdgcn_global_load_lds((const void*)at, (lds_ptr_t)(buf + (k * NW + wv) * 1024), 16, 0, 0);
-      from[k] += uint64_t(step[k]) * (kTB / 2);
+      copy_to_lds(from, off, to + buf + at + n * 4096);
+    };
+#pragma unroll
+    for (int n = 0; n < kOwn; ++n) {
+      copy(n, false, key_off, 0);
+      copy(n, false, value_off, S::kV);
+      kv_from += uint64_t(kv_step) * (4 * kPer);
+    }
+#pragma unroll
+    for (int n = 0; n < kRopes; ++n) {
+      copy(n, true, rope_off, S::kRope);
+      rope_from += uint64_t(rope_step) * 32;
     }
   };
-
-  __syncthreads();
-  if (c0 < c1) copy_stage(c0, lds);
-  for (int c = c0; c < c1; ++c) {
-    char* buf = lds + ((c - c0) & 1) * S::kStageB;
-    const int j0 = t.lo + c * kTB, live = t.hi - j0;  // rows of the stage
+  // This lane's copies of stage c are there; its values past the last row are made zeros.
+  auto arrive = [&](int c, char* buf) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const int live = t.hi - (t.lo + c * kTB);
     if (live < kTB) {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll 1
-      for (int k = 0; k < kCopies - kKeyCopies; ++k) {
-        const int at = k * S::kThreads + tid;
-        if (at / S::kVC >= live) *reinterpret_cast<u32x4*>(buf + S::kV + at * 16) = u32x4{0u, 0u, 0u, 0u};
+      for (int k = 0; k < kOwn; ++k) {
+        const int at = (k * 4 + cw) * kWave + lane;
+        if (at / S::kChunks >= live) *reinterpret_cast<u32x4*>(buf + S::kV + at * 16) = u32x4{0u, 0u, 0u, 0u};
       }
     }
-    wait_all_barrier();
-    if (c + 1 < c1) copy_stage(c + 1, lds + ((c - c0 + 1) & 1) * S::kStageB);
-    // nothing of it is seen by this wave's tokens; whether the tile's tokens see different rows of it
-    const bool skip = wn <= 0 || j0 > w_max || (a.rq.window > 0 && j0 + kTB <= w_min - a.rq.window + 1);
-    const bool t_differ = t.tokens > 1 && (j0 + kTB - 1 > t_min || (a.rq.window > 0 && j0 <= t_min + t.tokens - 1 - a.rq.window));
+  };
+  // Rows of stage c with values that are not finite, looked for where the tile's tokens see different rows.
+  auto scan = [&](int c, const char* buf) {
+    const int j0 = t.lo + c * kTB;
+    if (!(t.tokens > 1 && (j0 + kTB - 1 > t_min || (a.rq.window > 0 && j0 <= t_min + t.tokens - 1 - a.rq.window)))) return uint64_t{0};
+    uint64_t mine = 0;
+#pragma unroll 1
+    for (int k = tid; k < kTB * S::kChunks; k += S::kThreads)
+      if (any_not_finite(*reinterpret_cast<const u32x4*>(buf + S::kV + k * 16))) mine |= uint64_t{1} << (k / S::kChunks);
+    return any_rows(mine, tmp);
+  };
+  auto clear = [&](char* buf, uint64_t odd) {  // those rows, once every wave has added what it sees of them
+    wait_lds_barrier();
+#pragma unroll 1
+    for (int k = tid; k < kTB * S::kChunks; k += S::kThreads)
+      if ((odd >> (k / S::kChunks)) & 1) *reinterpret_cast<u32x4*>(buf + S::kV + k * 16) = u32x4{0u, 0u, 0u, 0u};
+    wait_lds_barrier();
+  };
+  auto unseen = [&](int c) {  // by all of this wave's tokens
+    const int j0 = t.lo + c * kTB;
+    return wn <= 0 || j0 > w_max || (a.rq.window > 0 && j0 + kTB <= w_min - a.rq.window + 1);
+  };
 
-    f32x4 s[kTB / 16][RB];
-    u32x4 p[kTB / 32][RB];
-    if (!skip) {
-    // ---- scores
-#pragma unroll
-    for (int tb = 0; tb < kTB / 16; ++tb)
-#pragma unroll
-      for (int mb = 0; mb < RB; ++mb) s[tb][mb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    // (a step's keys are read one step before its products: 128 cycles of this wave, and as many of its neighbour's)
-    auto key = [&](int kb, int tb) {
-      return *reinterpret_cast<const u32x4*>(buf + (key_at ^ (kb % S::kKeyTurn * 64)) + kb / S::kKeyTurn * S::kKeyTurn * 64 + tb * 16 * S::kKC * 16);
+  f32x4 s[kTB / 16][RB];
+  u32x4 p[kTB / 32][RB];
+  // out += values (of vbuf) by the weights, and scores = keys (of kbuf) by the queries, as one run of operands of RB
+  // products each, read kDeep - 1 operands ahead.
+  constexpr int kValueSteps = kTB / 32 * (HD / 16), kKeySteps = S::kKB * (kTB / 16);
+  auto products = [&](auto with_values, auto with_keys, const char* vbuf, const char* kbuf) {
+    constexpr int kFirst = with_values ? kValueSteps : 0, kSteps = kFirst + (with_keys ? kKeySteps : 0);
+    auto read = [&](int k) {
+      if (k < kFirst) {  // rows 32 (k / (HD / 16)) .., features 16 (k % (HD / 16)) ..
+        const int fb = k % (HD / 16);
+        const char* at = vbuf + (value_at ^ (fb % S::kTurn * 32)) + fb / S::kTurn * S::kTurn * 32 + k / (HD / 16) * 32 * S::kRowB;
+        const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)at));
+        const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(at + 16 * S::kRowB)));
+        return u32x4{lo.x, lo.y, hi.x, hi.y};
+      }
+      const int kb = (k - kFirst) / (kTB / 16), tb = (k - kFirst) % (kTB / 16);
+      if (kb < HD / 32) return *reinterpret_cast<const u32x4*>(kbuf + (key_at ^ (kb * 64)) + tb * 16 * S::kRowB);
+      return *reinterpret_cast<const u32x4*>(kbuf + (rope_at ^ ((kb - HD / 32) * 64)) + tb * 16 * 128);
     };
-    u32x4 kf[2][kTB / 16];
+    constexpr int kDeep = S::kTurns ? 9 : 5;
+    u32x4 f[kDeep];
 #pragma unroll
-    for (int tb = 0; tb < kTB / 16; ++tb) kf[0][tb] = key(0, tb);
+    for (int k = 0; k < kDeep - 1; ++k) f[k] = read(k);
 #pragma unroll
-    for (int kb = 0; kb < S::kKB; ++kb) {
-      if (kb + 1 < S::kKB)
+    for (int k = 0; k < kSteps; ++k) {
+      if (k + kDeep - 1 < kSteps) f[(k + kDeep - 1) % kDeep] = read(k + kDeep - 1);
+      if (k < kFirst) {
 #pragma unroll
-        for (int tb = 0; tb < kTB / 16; ++tb) kf[(kb + 1) & 1][tb] = key(kb + 1, tb);
-      if (kb < HD / 32 + 1 || rkb == 2)
+        for (int mb = 0; mb < RB; ++mb)
+          acc[k % (HD / 16)][mb] = mfma16x16x32(f[k % kDeep], p[k / (HD / 16)][mb], acc[k % (HD / 16)][mb]);
+      } else {
+        const int kb = (k - kFirst) / (kTB / 16), tb = (k - kFirst) % (kTB / 16);
+        if (kb < HD / 32 + 1 || rkb == 2)
 #pragma unroll
-        for (int tb = 0; tb < kTB / 16; ++tb)
-#pragma unroll
-          for (int mb = 0; mb < RB; ++mb) s[tb][mb] = mfma16x16x32(kf[kb & 1][tb], qf[mb][kb], s[tb][mb]);
+          for (int mb = 0; mb < RB; ++mb) s[tb][mb] = mfma16x16x32(f[k % kDeep], qf[mb][kb], kb == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : s[tb][mb]);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
+  };
+  auto mask = [&](int c) {
+    const int j0 = t.lo + c * kTB;
     const bool differ = j0 + kTB - 1 > w_min || (a.rq.window > 0 && j0 <= w_max - a.rq.window);
-    if (live < kTB || differ || wn < RB * 16) {
+    if (t.hi - j0 < kTB || differ || wn < RB * 16) {
 #pragma unroll
       for (int tb = 0; tb < kTB / 16; ++tb)
 #pragma unroll
@@ -238,7 +287,8 @@ __global__ __launch_bounds__(NW* kWave, NW / 4) void k_expanded(ExpandedArgs a) 
             s[tb][mb][e] = seen ? s[tb][mb][e] : -kInf;
           }
     }
-    // ---- softmax
+  };
+  auto softmax = [&]() {
     float m_new[RB];
     bool grow = false;
 #pragma unroll
@@ -277,64 +327,128 @@ __global__ __launch_bounds__(NW* kWave, NW / 4) void k_expanded(ExpandedArgs a) 
         p[tb >> 1][mb][(tb & 1) * 2 + 1] = pack_bf16x2(s[tb][mb][2], s[tb][mb][3]);
       }
     }
-    }
-    // ---- values that are not finite, where the tile's tokens see different rows: added row by row where they are
-    // seen, and zeros for the product
-    char* vb = buf + S::kV;
-    if (t_differ) {
-      for (int half = 0; half < 2; ++half) {
-        uint32_t odd = 0;
-        for (int k = tid; k < 32 * S::kVC; k += S::kThreads)
-          if (any_not_finite(*reinterpret_cast<const u32x4*>(vb + (half * 32 * S::kVC + k) * 16))) odd |= 1u << (k / S::kVC);
-        odd = any_rows(odd, tmp);
-        if (__builtin_expect(odd == 0, 1)) continue;
+  };
+  // Rows that are not finite, one by one where they are seen.
+  auto add_odd = [&](int c, const char* buf, uint64_t odd) {
 #pragma unroll 1
-        for (uint32_t left = skip ? 0 : odd; left != 0; left &= left - 1) {
-          const int row = half * 32 + __builtin_ctz(left), at = j0 + row;
+    for (uint64_t left = odd; left != 0; left &= left - 1) {
+      const int row = __builtin_ctzll(left), at = t.lo + c * kTB + row;
 #pragma unroll
-          for (int mb = 0; mb < RB; ++mb) {
-            float w = 0.0f;
+      for (int mb = 0; mb < RB; ++mb) {
+        float w = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if ((row >> 4) * 4 + (row & 3) == k) w = s[k >> 2][mb][k & 3];
-            w = __shfl(w, ((row >> 2) & 3) * 16 + i16, kWave);
-            const bool seen = at < t.hi && at <= qrow[mb] && (a.rq.window <= 0 || at > qrow[mb] - a.rq.window);
+        for (int k = 0; k < 16; ++k)
+          if ((row >> 4) * 4 + (row & 3) == k) w = s[k >> 2][mb][k & 3];
+        w = __shfl(w, ((row >> 2) & 3) * 16 + i16, kWave);
+        const bool seen = at < t.hi && at <= qrow[mb] && (a.rq.window <= 0 || at > qrow[mb] - a.rq.window);
 #pragma unroll
-            for (int fb = 0; fb < HD / 16; ++fb) {
-              const u32x2 v = *reinterpret_cast<const u32x2*>(vb + row * S::kVC * 16 + ((fb * 2 + (g >> 1)) ^ value_swizzle<S::kVC>(row)) * 16 + (g & 1) * 8);
-              acc[fb][mb][0] += seen ? w * bf16_lo(v.x) : 0.0f;
-              acc[fb][mb][1] += seen ? w * bf16_hi(v.x) : 0.0f;
-              acc[fb][mb][2] += seen ? w * bf16_lo(v.y) : 0.0f;
-              acc[fb][mb][3] += seen ? w * bf16_hi(v.y) : 0.0f;
-            }
-          }
+        for (int fb = 0; fb < HD / 16; ++fb) {
+          const u32x2 v = *reinterpret_cast<const u32x2*>(buf + S::kV + row * S::kRowB + ((fb * 2 + (g >> 1)) ^ value_swizzle<S::kChunks>(row)) * 16 + (g & 1) * 8);
+          acc[fb][mb][0] += seen ? w * bf16_lo(v.x) : 0.0f;
+          acc[fb][mb][1] += seen ? w * bf16_hi(v.x) : 0.0f;
+          acc[fb][mb][2] += seen ? w * bf16_lo(v.y) : 0.0f;
+          acc[fb][mb][3] += seen ? w * bf16_hi(v.y) : 0.0f;
         }
-        wait_lds_barrier();
-        for (int k = tid; k < 32 * S::kVC; k += S::kThreads)
-          if ((odd >> (k / S::kVC)) & 1) *reinterpret_cast<u32x4*>(vb + (half * 32 * S::kVC + k) * 16) = u32x4{0u, 0u, 0u, 0u};
-        wait_lds_barrier();
       }
     }
-    if (skip) continue;
-    // ---- values
-    auto value = [&](int k) {  // rows 32 (k / (HD / 16)) .., features 16 (k % (HD / 16)) ..
-      const int fb = k % (HD / 16);
-      const char* at = vb + (value_at ^ (fb % S::kValueTurn * 32)) + fb / S::kValueTurn * S::kValueTurn * 32 + k / (HD / 16) * 32 * S::kVC * 16;
-      const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)at));
-      const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(at + 16 * S::kVC * 16)));
-      return u32x4{lo.x, lo.y, hi.x, hi.y};
-    };
-    constexpr int kDeep = 5, kSteps = kTB / 32 * (HD / 16);
-    u32x4 vf[kDeep];
+  };
+  constexpr auto yes = std::true_type{};
+  constexpr auto no = std::false_type{};
+
+  __syncthreads();
+  if constexpr (S::kTurns) {
+    // Phases, a barrier after each: in phase 2c the first four waves are at the products (values of stage c - 1, scores of
+    // stage c) and the others at the softmax of c - 1; in phase 2c + 1 the other way round.  A stage is read in the phases
+    // 2c .. 2c + 3, and stage c + 3 is copied to its place in phase 2c + 4 by the waves at the softmax.  The stages
+    // [plain0, plain1) are whole and seen by all tokens of the tile.
+    const int plain0 = a.rq.window > 0 ? (t_min + t.tokens - 1 - a.rq.window - t.lo + kTB) / kTB : 0;
+    const int plain1 = t.tokens < S::M ? 0 : ((t_min + 1 < t.hi ? t_min + 1 : t.hi) - t.lo) / kTB;
+    auto plain = [&](int c) { return c >= plain0 && c < plain1; };
+    uint64_t odd = 0, odd_next = 0;
+    bool saw = false;  // this wave's tokens, something of the stage before
+    int buf = 0, next = S::kStageB, last = 2 * S::kStageB;
+    if (c0 < c1) {
+      // (before the first stage: weights of zero and values of zero)
+      for (int k = tid; k < kTB * S::kChunks; k += S::kThreads) *reinterpret_cast<u32x4*>(lds + last + S::kV + k * 16) = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int k = 0; k < kDeep - 1; ++k) vf[k] = value(k);
+      for (int kb = 0; kb < kTB / 32; ++kb)
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      if (k + kDeep - 1 < kSteps) vf[(k + kDeep - 1) % kDeep] = value(k + kDeep - 1);
+        for (int mb = 0; mb < RB; ++mb) p[kb][mb] = u32x4{0u, 0u, 0u, 0u};
+      if (late) {
+        copy_stage(c0, buf);
+        arrive(c0, lds + buf);
+      }
+      wait_lds_barrier();
+      if (late) {
+        if (c0 + 1 < c1) copy_stage(c0 + 1, next);
+        odd = scan(c0, lds + buf);
+        wait_lds_barrier();
+      }
+      for (int c = c0; c < c1; ++c) {
+        const int after = next + S::kStageB < S::kBytes ? next + S::kStageB : 0;
+        const bool more = c + 1 < c1;
+        if (!late) {
+          if (!plain(c)) odd_next = scan(c, lds + buf);
+          if (odd != 0) clear(lds + last, odd);
+          odd = odd_next;
+          odd_next = 0;
+        }
+        const bool sees = plain(c) || !unseen(c);
+        if (sees || saw) {
+          __builtin_amdgcn_s_setprio(1);
+          products(yes, yes, lds + last, lds + buf);
+          __builtin_amdgcn_s_setprio(0);
+        }
+        saw = sees;
+        if (!plain(c)) mask(c);
+        if (late && more) arrive(c + 1, lds + next);
+        wait_lds_barrier();
+        if (late) {
+          odd_next = more && !plain(c + 1) ? scan(c + 1, lds + next) : 0;
+          if (c + 2 < c1) copy_stage(c + 2, after);
+        }
+        if (sees) {
+          softmax();
+        } else {
 #pragma unroll
-      for (int mb = 0; mb < RB; ++mb)
-        acc[k % (HD / 16)][mb] = mfma16x16x32(vf[k % kDeep], p[k / (HD / 16)][mb], acc[k % (HD / 16)][mb]);
-      __builtin_amdgcn_sched_barrier(0);
+          for (int kb = 0; kb < kTB / 32; ++kb)
+#pragma unroll
+            for (int mb = 0; mb < RB; ++mb) p[kb][mb] = u32x4{0u, 0u, 0u, 0u};
+        }
+        if (odd != 0) add_odd(c, lds + buf, odd);
+        if (late) {
+          if (odd != 0) clear(lds + buf, odd);
+          odd = odd_next;
+        }
+        wait_lds_barrier();
+        last = buf;
+        buf = next;
+        next = after;
+      }
+      if (!late && odd != 0) clear(lds + last, odd);
+      if (saw) products(yes, no, lds + last, lds + last);
+      if (!late) wait_lds_barrier();
+    }
+  } else {
+    if (c0 < c1) copy_stage(c0, 0);
+    for (int c = c0; c < c1; ++c) {
+      const int at = ((c - c0) & 1) * S::kStageB;
+      char* buf = lds + at;
+      arrive(c, buf);
+      wait_lds_barrier();
+      if (c + 1 < c1) copy_stage(c + 1, S::kStageB - at);
+      const bool skip = unseen(c);
+      if (!skip) {
+        products(no, yes, buf, buf);
+        mask(c);
+        softmax();
+      }
+      const uint64_t odd = scan(c, buf);
+      if (odd != 0) {
+        if (!skip) add_odd(c, buf, odd);
+        clear(buf, odd);
+      }
+      if (!skip) products(yes, no, buf, buf);
     }
   }
 
@@ -418,17 +532,25 @@ struct Choice {
   bool large;  // 256 tokens per tile, else 64
   int tiles, parts;
 };
-Choice choose(int64_t R, int64_t n_tokens, int64_t n_rows, int heads, int cus) {
-  Choice c;
-  // tiles of 256 where they fill the device or nearly all are whole
-  c.large = n_tokens / 256 * heads >= cus || n_tokens / R >= 512;
-  const int64_t M = c.large ? 256 : 64, some = R < n_tokens ? R : n_tokens;
-  c.tiles = int(n_tokens / M + some);
-  const int64_t tiles = (n_tokens + M * some - 1) / (M * some) * some * heads, stages = n_rows / R / kTB;
-  int64_t parts = tiles >= cus ? 1 : (2 * cus + tiles - 1) / tiles;
-  parts = parts < stages / 4 ? parts : stages / 4;
-  c.parts = int(parts < 1 ? 1 : (parts > 32 ? 32 : parts));
-  return c;
+// With 128 features a token costs 1.5 times as much in a tile of 64 as in one of 256 (12 prompts of 1500 tokens behind 2000,
+// 20 heads, window 1000: 645 us and 430 us), so tiles of 256 are taken where they are no emptier than that, counted by the
+// mean request (16 of 37 tokens behind 1000, 128 heads: 304 us with tiles of 256, 96 us with 64), and where there are two a
+// CU or parts of ten stages and more (one prompt of 2048 tokens, 16 heads: 78 us and 54 us; 512 tokens behind 7680:
+// 94 us and 100 us).  With 64 features they gain less, and from 2048 tokens on (2048 behind 6144, 32 heads: 212 us and
+// 262 us; four of 1000 behind 2000, 64 heads: 357 us and 254 us).
+Choice choose(int64_t R, int64_t n_tokens, int64_t n_rows, int heads, int head_dim, int cus) {
+  const int64_t some = R < n_tokens ? R : n_tokens, mean = (n_tokens + some - 1) / some, stages = n_rows / R / kTB;
+  auto with = [&](int64_t M) {
+    const int64_t tiles = (mean + M - 1) / M * some * heads;
+    int64_t parts = tiles >= cus ? 1 : (2 * cus + tiles - 1) / tiles;
+    parts = parts < stages / 4 ? parts : stages / 4;
+    return Choice{M == 256, int(n_tokens / M + some), int(parts < 1 ? 1 : (parts > 32 ? 32 : parts))};
+  };
+  const int64_t room = (mean + 255) / 256 * 256;
+  const Choice c = with(256);
+  const bool full = head_dim == 128 ? 2 * room <= 3 * ((mean + 63) / 64 * 64) : mean >= 2048;
+  if (full && (room / 256 * some * heads >= 2 * cus || stages >= 10 * c.parts)) return c;
+  return with(64);
 }
 
 template <int HD, int NW, int RB>
@@ -446,12 +568,12 @@ hipError_t run(const ExpandedArgs& a, hipStream_t stream) {
 }  // namespace
 
 int64_t expanded_workspace_bytes(int64_t R, int64_t n_tokens, int64_t n_rows, int heads, int head_dim, int cus) {
-  const Choice c = choose(R, n_tokens, n_rows, heads, cus);
+  const Choice c = choose(R, n_tokens, n_rows, heads, head_dim, cus);
   return c.parts > 1 ? int64_t(c.parts) * n_tokens * heads * (head_dim + 2) * 4 : 0;
 }
 
 hipError_t launch_latent_expanded(ExpandedArgs a, int cus, hipStream_t stream) {
-  const Choice c = choose(a.rq.R, a.rq.n_tokens, a.n_rows, a.heads, cus);
+  const Choice c = choose(a.rq.R, a.rq.n_tokens, a.n_rows, a.heads, a.head_dim, cus);
   a.tiles = c.tiles;
   a.parts = c.parts;
   if (a.head_dim == 128) return c.large ? run<128, 8, 2>(a, stream) : run<128, 4, 1>(a, stream);

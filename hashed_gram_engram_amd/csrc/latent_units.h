@@ -38,6 +38,23 @@ __device__ __forceinline__ float quad_sum(float v) {
   return __uint_as_float(q[0]) + __uint_as_float(q[1]);
 }
 
+// The address in LDS of `at`.
+__device__ __forceinline__ uint32_t lds_address(const void* at) { return uint32_t(uintptr_t((lds_ptr_t)at)); }
+
+// Copies 16 or 4 bytes a lane from memory to LDS, lane l's to `to` + l times that; `to` is the same in every lane.  Whoever
+// reads them waits first: the compiler does not know of them.  (It has a builtin for this, but then lets every
+// transposed read of LDS wait for all copies in flight.)
+template <int BYTES>
+__device__ __forceinline__ void copy_to_lds(const void* from, uint32_t to) {
+  to = __builtin_amdgcn_readfirstlane(to);
+  if constexpr (BYTES == 16) asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from));
+  else asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from));
+}
+// 16 bytes a lane from `off` bytes after `from`, which is the same in every lane.
+__device__ __forceinline__ void copy_to_lds(const void* from, uint32_t off, uint32_t to) {
+  to = __builtin_amdgcn_readfirstlane(to);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(from));
+}
 __device__ __forceinline__ void wait_lds_barrier() {
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -55,14 +72,15 @@ __device__ __forceinline__ bool any_not_finite(u32x4 v) {  // of eight bf16
   for (int e = 0; e < 4; ++e) odd |= (v[e] & 0x7F80u) == 0x7F80u || (v[e] & 0x7F800000u) == 0x7F800000u;
   return odd;
 }
-// The union of all threads' rows (uniform).
-__device__ __forceinline__ uint32_t any_rows(uint32_t rows, int64_t* misc) {
-  uint32_t* word = reinterpret_cast<uint32_t*>(misc);
+// The union of all threads' rows (uniform).  A barrier lies between two calls.
+__device__ __forceinline__ uint64_t any_rows(uint64_t rows, int64_t* misc) {
+  unsigned long long* word = reinterpret_cast<unsigned long long*>(misc);
   if (threadIdx.x == 0) *word = 0;
   wait_lds_barrier();
-  if (rows != 0) atomicOr(word, rows);
+  if (rows != 0) atomicOr(word, static_cast<unsigned long long>(rows));
   wait_lds_barrier();
-  return __builtin_amdgcn_readfirstlane(*word);
+  const uint64_t all = *word;
+  return uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(all >> 32)))) << 32 | uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(all)));
 }
 
 // A part of a tile in the workspace, for the join.

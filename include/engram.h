@@ -430,7 +430,7 @@ size_t engram_linear_workspace_bytes_up_to(const engram_linear_layout* layout, i
  * tokens token_start[r] .. token_start[r + 1] - 1, at positions start_pos[r] .. .  Whatever these arrays
  * hold, no access leaves the tensors: token ranges are cut to n_tokens, positions to max_blocks * block_size.
  * The ranges of different requests must not overlap (a plan's do not).  At most 4096 requests, and 2^31 - 1 slots
- * (n_blocks * block_size) in a cache, else ENGRAM_E_LAYOUT.
+ * (n_blocks * block_size) in a cache, else ENGRAM_E_LAYOUT.  Strides are 2^28 at most.
  * The conventions above hold; calls that write different buffers may overlap in time. */
 
 /* A cache row (one slot of a page), engram_latent_row_bytes() bytes.
