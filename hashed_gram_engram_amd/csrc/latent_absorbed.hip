@@ -426,7 +426,7 @@ hipError_t run(const AbsorbedArgs& a, int G, hipStream_t stream) {
                                            hipFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
   if (e != hipSuccess) return e;
   k_absorbed<DC, MB, FP8><<<dim3(G), dim3(kThreads), S::kBytes, stream>>>(a);
-  k_absorbed_join<DC, MB><<<dim3(4 * G), dim3(kThreads), 0, stream>>>(a, G);
+  k_absorbed_join<DC, MB><<<dim3(MB * G), dim3(kThreads), 0, stream>>>(a, G);
   return hipGetLastError();
 }
 
