@@ -198,3 +198,9 @@ def test_the_oracle_of_codes_and_scales():
         assert (y.abs().view(2, 32).amax(1) <= 448).all() and (y.abs().view(2, 32).amax(1) > 224).all()
     v = torch.arange(256, dtype=torch.int32).to(torch.uint8).view(torch.float8_e4m3fn).double().numpy()
     assert np.array_equal(v, e4m3_values(), equal_nan=True)
+
+
+@pytest.mark.parametrize("call,change", [(write, dict(ls=(1 << 28) + 8)), (write, dict(rs=(1 << 28) + 8)), (absorbed, dict(qs=(1 << 28) + 8)),
+                                         (absorbed, dict(os=(1 << 28) + 8)), (expanded, dict(ks=(1 << 28) + 8)), (expanded, dict(rs=(1 << 28) + 8))])
+def test_strides_are_2_to_the_28_at_most(call, change):
+    assert call(**change) == -3
