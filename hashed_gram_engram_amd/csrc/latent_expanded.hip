@@ -277,15 +277,16 @@ __global__ __launch_bounds__(NW* kWave, 2) void k_expanded(ExpandedArgs a) {
     const bool differ = j0 + kTB - 1 > w_min || (a.rq.window > 0 && j0 <= w_max - a.rq.window);
     if (t.hi - j0 < kTB || differ || wn < RB * 16) {
 #pragma unroll
-      for (int tb = 0; tb < kTB / 16; ++tb)
+      for (int mb = 0; mb < RB; ++mb) {
+        // rows first .. first + n - 1 are seen, of rows from 0 on
+        const int first = a.rq.window > 0 && qrow[mb] >= a.rq.window ? qrow[mb] - a.rq.window + 1 : 0;
+        const int end = qrow[mb] + 1 < t.hi ? qrow[mb] + 1 : t.hi, n = end > first ? end - first : 0;
+        const int at = j0 + 4 * g - first;
 #pragma unroll
-        for (int mb = 0; mb < RB; ++mb)
+        for (int tb = 0; tb < kTB / 16; ++tb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int row = j0 + tb * 16 + 4 * g + e;
-            const bool seen = row < t.hi && row <= qrow[mb] && (a.rq.window <= 0 || row > qrow[mb] - a.rq.window);
-            s[tb][mb][e] = seen ? s[tb][mb][e] : -kInf;
-          }
+          for (int e = 0; e < 4; ++e) s[tb][mb][e] = uint32_t(at + tb * 16 + e) < uint32_t(n) ? s[tb][mb][e] : -kInf;
+      }
     }
   };
   auto softmax = [&]() {
