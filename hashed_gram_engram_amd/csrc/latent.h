@@ -76,7 +76,7 @@ struct AbsorbedArgs {
   char* workspace;
 };
 int64_t absorbed_workspace_bytes(int latent_dim, int cus);
-hipError_t launch_absorbed_rows(const AbsorbedArgs& a, int G, bool wide, hipStream_t stream);  // 64 rows and more a request
+hipError_t launch_absorbed_rows(const AbsorbedArgs& a, int G, bool wide, hipStream_t stream);  // 33 rows and more a request
 hipError_t launch_latent_absorbed(const AbsorbedArgs& a, int cus, hipStream_t stream);
 
 struct ExpandedArgs {

@@ -42,8 +42,9 @@ __device__ __forceinline__ float quad_sum(float v) {
 __device__ __forceinline__ uint32_t lds_address(const void* at) { return uint32_t(uintptr_t((lds_ptr_t)at)); }
 
 // Copies 16 or 4 bytes a lane from memory to LDS, lane l's to `to` + l times that; `to` is the same in every lane.  Whoever
-// reads them waits first: the compiler does not know of them.  (It has a builtin for this, but then lets every
-// transposed read of LDS wait for all copies in flight.)
+// reads them waits first: the compiler does not know of them (its own waits, for loads into registers, then only wait
+// for more than they need).  m0 is set for each copy; kernels with these use nothing else that keeps it.  (The compiler
+// has a builtin, but then lets every transposed read of LDS wait for all copies in flight.)
 template <int BYTES>
 __device__ __forceinline__ void copy_to_lds(const void* from, uint32_t to) {
   to = __builtin_amdgcn_readfirstlane(to);
