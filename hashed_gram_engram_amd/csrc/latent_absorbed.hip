@@ -101,7 +101,7 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
       const int pos = t.base + c * kTB + lane;
       if (c >= c0 + n || pos < t.lo || pos >= t.hi) return -1;
       const int64_t slot = slot_of(a.rq, un.r, pos);
-      if (slot < 0 && t.tile == 0 && a.err_count != nullptr) atomicAdd(a.err_count, 1);
+      if (slot < 0 && pos >= t.fresh && a.err_count != nullptr) atomicAdd(a.err_count, 1);
       return slot;
     };
     auto put_slot = [&](int c, int64_t slot) {

@@ -200,8 +200,11 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed_rows(A
       const int j0 = t.base + c * kTB, from = t.lo - j0, to = c < c0 + n ? t.hi - j0 : 0;  // rows [from, to)
       const uint32_t below = to >= 32 ? ~0u : (to <= 0 ? 0u : (1u << to) - 1u), above = from <= 0 ? ~0u : (from >= 32 ? 0u : ~0u << from);
       const uint32_t in = below & above, on = in & uint32_t(__ballot(good));
-      if (__builtin_expect(on != in, 0))
-        if (wv == 0 && lane == 0 && t.tile == 0 && a.err_count != nullptr) atomicAdd(a.err_count, __builtin_popcount(in ^ on));
+      if (__builtin_expect(on != in, 0)) {
+        const int old = t.fresh - j0;  // (rows that an earlier tile has counted)
+        const uint32_t bad = (in ^ on) & (old <= 0 ? ~0u : (old >= 32 ? 0u : ~0u << old));
+        if (wv == 0 && lane == 0 && bad != 0 && a.err_count != nullptr) atomicAdd(a.err_count, __builtin_popcount(bad));
+      }
       return on;
     };
     uint32_t on_ring[5];  // rows that take part in stages c .. c + 4

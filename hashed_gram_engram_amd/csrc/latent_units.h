@@ -194,6 +194,7 @@ struct Segment {
   int lo, hi;           // positions that any of the tile's rows sees
   int p_min, p_max;     // positions of its first and last row's tokens
   int base;             // position of stage 0
+  int fresh;            // the first position that no earlier tile of the request sees
 };
 template <int M, int STAGE>
 __device__ __forceinline__ Segment segment_of(const LatentRequests& q, int heads, const Units& un) {
@@ -213,6 +214,7 @@ __device__ __forceinline__ Segment segment_of(const LatentRequests& q, int heads
   t.base = t.s.lo;
   t.lo = q.window > 0 && t.p_min + 1 > q.window ? t.p_min + 1 - q.window : 0;
   t.hi = t.p_max + 1;
+  t.fresh = t.tile == 0 ? t.lo : t.s.pos + (t.row0 - 1) / heads + 1;
   return t;
 }
 

@@ -489,9 +489,9 @@ engram_status engram_latent_read(const engram_latent_layout* layout, const engra
  *   lse [n_tokens, heads] fp32 out, or NULL: the natural logarithm of the softmax's sum
  * For the token at position p: s_j = scale * q . row_j over the positions j <= p (window: j > p - window),
  * out = sum_j softmax(s)_j latent_j.  Positions that are masked, past the request or on a page outside
- * [0, n_blocks) take no part, whatever they hold (a bad page among the visible ones makes *err_count
- * grow); where none is left out is 0 and lse -infinity.  Scores, softmax and sums are fp32, the weights
- * are rounded to bf16 for the second product, out once.  Rows of other tokens stay as they are. */
+ * [0, n_blocks) take no part, whatever they hold (each position on a bad page that any of its request's tokens
+ * would see adds 1 to *err_count); where none is left out is 0 and lse -infinity.  Scores, softmax and sums are
+ * fp32, the weights are rounded to bf16 for the second product, out once.  Rows of other tokens stay as they are. */
 engram_status engram_latent_attention(const engram_latent_layout* layout, const engram_page_layout* pages,
                                       const uint16_t* q, int64_t q_stride, const void* cache,
                                       const int32_t* token_start, const int32_t* start_pos, int64_t R,
