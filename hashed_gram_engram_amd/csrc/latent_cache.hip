@@ -19,7 +19,9 @@ namespace engram {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWriteTokens = 4;  // per workgroup
+constexpr int kWriteTokens = 4;  // per workgroup and turn
+// A launch of 2^32 threads and more loses some without an error: from 2^24 tokens on workgroups take several turns.
+constexpr int kWriteGroups = 1 << 22;
 
 __device__ __forceinline__ uint32_t abs_bits_finite(float v) {
   const uint32_t b = __float_as_uint(v) & 0x7FFFFFFFu;
@@ -29,61 +31,62 @@ __device__ __forceinline__ uint32_t abs_bits_finite(float v) {
 __global__ __launch_bounds__(kThreads) void k_latent_write(LatentWriteArgs a) {
   const int lat = a.latent_dim / 8, chunks = lat + a.rope_dim / 8;  // multiples of 4: a block of 32 stays in 4 lanes
   const int row = latent_row_bytes(a.latent_dim, a.rope_dim, a.fp8 != 0);
-  const int t0 = blockIdx.x * kWriteTokens;
-  for (int i = threadIdx.x; i < kWriteTokens * chunks; i += kThreads) {
-    const int t = t0 + i / chunks, c = i % chunks;
-    const bool on = t < a.n_tokens;
-    int64_t slot = on ? a.slots[t] : -1;
-    if (slot >= a.n_slots) {
-      if (c == 0 && a.err_count != nullptr) atomicAdd(a.err_count, 1);
-      slot = -1;
-    }
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if (slot >= 0)
-      v = *reinterpret_cast<const u32x4*>(c < lat ? a.latent + t * a.latent_stride + c * 8 : a.rope + t * a.rope_stride + (c - lat) * 8);
-    uint8_t* to = a.cache + (slot < 0 ? 0 : slot) * row;
-    if (!a.fp8 || c >= lat) {
-      if (slot >= 0) *reinterpret_cast<u32x4*>(to + (a.fp8 ? a.latent_dim + 16 + (c - lat) * 16 : c * 16)) = v;
-      continue;  // (whole groups of 4 lanes)
-    }
-    float x[8];
-    uint32_t top = 0;
+  for (int t0 = blockIdx.x * kWriteTokens; t0 < a.n_tokens; t0 += gridDim.x * kWriteTokens) {
+    for (int i = threadIdx.x; i < kWriteTokens * chunks; i += kThreads) {
+      const int t = t0 + i / chunks, c = i % chunks;
+      const bool on = t < a.n_tokens;
+      int64_t slot = on ? a.slots[t] : -1;
+      if (slot >= a.n_slots) {
+        if (c == 0 && a.err_count != nullptr) atomicAdd(a.err_count, 1);
+        slot = -1;
+      }
+      u32x4 v = {0u, 0u, 0u, 0u};
+      if (slot >= 0)
+        v = *reinterpret_cast<const u32x4*>(c < lat ? a.latent + t * a.latent_stride + c * 8 : a.rope + t * a.rope_stride + (c - lat) * 8);
+      uint8_t* to = a.cache + (slot < 0 ? 0 : slot) * row;
+      if (!a.fp8 || c >= lat) {
+        if (slot >= 0) *reinterpret_cast<u32x4*>(to + (a.fp8 ? a.latent_dim + 16 + (c - lat) * 16 : c * 16)) = v;
+        continue;  // (whole groups of 4 lanes)
+      }
+      float x[8];
+      uint32_t top = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[2 * e] = bf16_lo(v[e]);
-      x[2 * e + 1] = bf16_hi(v[e]);
-    }
+      for (int e = 0; e < 4; ++e) {
+        x[2 * e] = bf16_lo(v[e]);
+        x[2 * e + 1] = bf16_hi(v[e]);
+      }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t b = abs_bits_finite(x[e]);
-      top = b > top ? b : top;
-    }
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t b = abs_bits_finite(x[e]);
+        top = b > top ? b : top;
+      }
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      const uint32_t b = uint32_t(__shfl_xor(int(top), o, kWave));
-      top = b > top ? b : top;
-    }
-    int scale = int(top >> 23) - 8 + ((top & 0x007FFFFFu) > 0x00600000u ? 1 : 0);
-    scale = scale < 1 ? 1 : scale;  // (what 2^-126 leaves of smaller values is still exact: bf16 has none below 2^-133)
-    const float up = __uint_as_float(uint32_t(254 - scale) << 23);  // 2^(127 - scale)
-    // 248 and more would become 256, which the largest scale takes past bf16: 240 there
-    const float most = scale == 247 ? 240.0f : 448.0f;
-    u32x2 code;
+      for (int o = 1; o < 4; o <<= 1) {
+        const uint32_t b = uint32_t(__shfl_xor(int(top), o, kWave));
+        top = b > top ? b : top;
+      }
+      int scale = int(top >> 23) - 8 + ((top & 0x007FFFFFu) > 0x00600000u ? 1 : 0);
+      scale = scale < 1 ? 1 : scale;  // (what 2^-126 leaves of smaller values is still exact: bf16 has none below 2^-133)
+      const float up = __uint_as_float(uint32_t(254 - scale) << 23);  // 2^(127 - scale)
+      // 248 and more would become 256, which the largest scale takes past bf16: 240 there
+      const float most = scale == 247 ? 240.0f : 448.0f;
+      u32x2 code;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float y[4];
+      for (int h = 0; h < 2; ++h) {
+        float y[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = __builtin_amdgcn_fmed3f(x[4 * h + e] * up, -most, most);
-      int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
-      w = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
+        for (int e = 0; e < 4; ++e) y[e] = __builtin_amdgcn_fmed3f(x[4 * h + e] * up, -most, most);
+        int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (!(__builtin_fabsf(x[4 * h + e]) <= kFltMax)) w |= 0x7F << (8 * e);  // (not finite)
-      code[h] = uint32_t(w);
-    }
-    if (slot >= 0) {
-      *reinterpret_cast<u32x2*>(to + c * 8) = code;
-      if ((c & 3) == 0) to[a.latent_dim + (c >> 2)] = uint8_t(scale);
+        for (int e = 0; e < 4; ++e)
+          if (!(__builtin_fabsf(x[4 * h + e]) <= kFltMax)) w |= 0x7F << (8 * e);  // (not finite)
+        code[h] = uint32_t(w);
+      }
+      if (slot >= 0) {
+        *reinterpret_cast<u32x2*>(to + c * 8) = code;
+        if ((c & 3) == 0) to[a.latent_dim + (c >> 2)] = uint8_t(scale);
+      }
     }
   }
 }
@@ -190,7 +193,7 @@ __global__ __launch_bounds__(kThreads) void k_latent_read(LatentReadArgs a) {
 }  // namespace
 
 hipError_t launch_latent_write(const LatentWriteArgs& a, hipStream_t stream) {
-  const int grid = (a.n_tokens + kWriteTokens - 1) / kWriteTokens;
+  const int turns = (a.n_tokens + kWriteTokens - 1) / kWriteTokens, grid = turns < kWriteGroups ? turns : kWriteGroups;
   k_latent_write<<<dim3(grid), dim3(kThreads), 0, stream>>>(a);
   return hipGetLastError();
 }
