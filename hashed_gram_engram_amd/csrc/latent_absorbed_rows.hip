@@ -450,6 +450,19 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed_rows(A
         }
         acc_from_memory(acc, mem);
       }
+      float scale = a.scale_log2;
+      bool big = false;
+#pragma unroll
+      for (int mb = 0; mb < RB; ++mb) big |= m_run[mb] != -kInf && !(__builtin_fabsf(m_run[mb]) < kBigScore);
+      if (__builtin_expect(__any(big), 0)) {
+#pragma unroll
+        for (int mb = 0; mb < RB; ++mb)
+#pragma unroll
+          for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[tb][mb][e] *= scale;
+        scale = 1.0f;
+      }
 #pragma unroll
       for (int mb = 0; mb < RB; ++mb) {
         const float ref = m_run[mb] == -kInf ? 0.0f : m_run[mb];
@@ -457,7 +470,7 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed_rows(A
         for (int tb = 0; tb < 2; ++tb) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            s[tb][mb][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[tb][mb][e], a.scale_log2, -ref));
+            s[tb][mb][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[tb][mb][e], scale, -ref));
             l_own[mb] += s[tb][mb][e];
           }
           p[mb][2 * tb] = pack_bf16x2(s[tb][mb][0], s[tb][mb][1]);

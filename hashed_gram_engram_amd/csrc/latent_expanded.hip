@@ -289,6 +289,7 @@ __global__ __launch_bounds__(NW* kWave, 2) void k_expanded(ExpandedArgs a) {
       }
     }
   };
+  bool big = false;  // any of the references
   auto softmax = [&]() {
     float m_new[RB];
     bool grow = false;
@@ -304,6 +305,7 @@ __global__ __launch_bounds__(NW* kWave, 2) void k_expanded(ExpandedArgs a) {
       grow |= m > m_run[mb] + kGrow;
     }
     if (__any(grow)) {
+      bool high = false;
 #pragma unroll
       for (int mb = 0; mb < RB; ++mb) {
         const float m = fmaxf(m_run[mb], m_new[mb]);
@@ -312,7 +314,19 @@ __global__ __launch_bounds__(NW* kWave, 2) void k_expanded(ExpandedArgs a) {
         l_own[mb] *= alpha;
 #pragma unroll
         for (int fb = 0; fb < HD / 16; ++fb) acc[fb][mb] *= alpha;
+        high |= m != -kInf && !(__builtin_fabsf(m) < kBigScore);
       }
+      big = __any(high);
+    }
+    float scale = a.scale_log2;
+    if (__builtin_expect(big, 0)) {
+#pragma unroll
+      for (int mb = 0; mb < RB; ++mb)
+#pragma unroll
+        for (int tb = 0; tb < kTB / 16; ++tb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[tb][mb][e] *= scale;
+      scale = 1.0f;
     }
 #pragma unroll
     for (int mb = 0; mb < RB; ++mb) {
@@ -321,7 +335,7 @@ __global__ __launch_bounds__(NW* kWave, 2) void k_expanded(ExpandedArgs a) {
       for (int tb = 0; tb < kTB / 16; ++tb) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          s[tb][mb][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[tb][mb][e], a.scale_log2, -ref));
+          s[tb][mb][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[tb][mb][e], scale, -ref));
           l_own[mb] += s[tb][mb][e];
         }
         p[tb >> 1][mb][(tb & 1) * 2] = pack_bf16x2(s[tb][mb][0], s[tb][mb][1]);

@@ -17,6 +17,11 @@ constexpr float kInf = __builtin_inff();
 // and bf16 weights, and accumulators are rarely scaled.
 constexpr float kGrow = 16.0f;
 
+// Scores times the scale are taken to a reference of more than 2^24 rounded: the reference is the rounded product of the highest
+// score, and a fused product less it would be that rounding's error, which from 2^31 on passes the exponents of fp32 (weights
+// of infinity, or all zero).  Below 2^24 the error is at most 1 and the same for all weights.
+constexpr float kBigScore = 16777216.0f;
+
 // 16-byte chunk c of row r lies at position c ^ swizzle(r): 16 rows' reads of one chunk cover all 64 banks once
 // (rows start at even multiples of 128 bytes or odd ones by turns), and so do 8 rows' transposed reads of
 // a pair of chunks.
