@@ -5,8 +5,8 @@
 // exactly), read twice: along the features for the scores, and transposed (ds_read_tr16) for the values.
 //  scores   S^T = C Q^T: a wave takes 16 of the positions and keeps all queries in registers; a lane then holds 4
 //           consecutive positions of one query.
-//  softmax  running maximum and sum in the base 2; the waves share each stage's maxima through LDS; a maximum
-//           that grows by less than 2^16 leaves the reference where it is.
+//  softmax  running maximum and sum in the base 2; the waves share each stage's maxima through LDS; the
+//           reference lies up to 2^16 above it, and moves when it is passed.
 //  values   out^T += C^T P^T: a wave takes a quarter of the latent's features for every query; the weights
 //           pass through LDS, rounded to bf16 for the product (their sum is of the unrounded ones), the order of
 //           positions in the product being that of the score fragments.
@@ -232,7 +232,7 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
         float m = -kInf;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          s[mb][e] *= a.scale_log2;
+          s[mb][e] = rounded_product(s[mb][e], a.scale_log2);
           if (edge) {
             const int row = wv * 16 + 4 * g + e, pos = j0 + row;
             const bool seen = ((on >> row) & 1) && pos <= qpos[mb] && (a.rq.window <= 0 || pos > qpos[mb] - a.rq.window);
@@ -255,12 +255,12 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed(Absorb
 #pragma unroll
         for (int k = 1; k < 4; ++k) m = fmaxf(m, smax[k * S::M + mb * 16 + i16]);
         m_new[mb] = m;
-        grow |= m > m_run[mb] + kGrow;
+        grow |= m > m_run[mb];
       }
       if (__any(grow)) {
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
-          const float m = fmaxf(m_run[mb], m_new[mb]);
+          const float m = moved_reference(m_run[mb], m_new[mb]);
           const float alpha = m == -kInf ? 1.0f : __builtin_amdgcn_exp2f(m_run[mb] - m);
           m_run[mb] = m;
 #pragma unroll

@@ -425,16 +425,16 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed_rows(A
       for (int mb = 0; mb < RB; ++mb) {
         float m = fmaxf(fmaxf(fmaxf(s[0][mb][0], s[0][mb][1]), fmaxf(s[0][mb][2], s[0][mb][3])),
                         fmaxf(fmaxf(s[1][mb][0], s[1][mb][1]), fmaxf(s[1][mb][2], s[1][mb][3])));
-        m_new[mb] = quad_max(m) * a.scale_log2;  // (the scale is positive: its sign is in the queries)
-        if (m_run[mb] == -kInf) m_run[mb] = m_new[mb];  // (nothing is summed yet)
-        grow |= m_new[mb] > m_run[mb] + kGrow;
+        m_new[mb] = rounded_product(quad_max(m), a.scale_log2);  // (the scale is positive: its sign is in the queries)
+        if (m_run[mb] == -kInf) m_run[mb] = m_new[mb] + kGrow;  // (nothing is summed yet)
+        grow |= m_new[mb] > m_run[mb];
       }
       if (__any(grow)) {
         char* mem = acc_memory();
         acc_to_memory(acc, mem);
 #pragma unroll
         for (int mb = 0; mb < RB; ++mb) {
-          const float m = fmaxf(m_run[mb], m_new[mb]);
+          const float m = moved_reference(m_run[mb], m_new[mb]);
           const float alpha = m == -kInf ? 1.0f : __builtin_amdgcn_exp2f(m_run[mb] - m);
           m_run[mb] = m;
           l_own[mb] *= alpha;
@@ -460,7 +460,7 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed_rows(A
 #pragma unroll
           for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[tb][mb][e] *= scale;
+            for (int e = 0; e < 4; ++e) s[tb][mb][e] = rounded_product(s[tb][mb][e], scale);
         scale = 1.0f;
       }
 #pragma unroll

@@ -5,8 +5,8 @@
 // memory.  S^T = K Q^T leaves a lane with 4 consecutive keys of one query, which is an operand
 // of out^T += V^T P^T as it stands if the keys of that product are counted in the same order: the weights never
 // leave the registers, and a query's maximum and sum are shared by 4 lanes of one wave.  Values are read
-// transposed (ds_read_tr16).  The softmax is in the base 2; a maximum that grows by less than 2^16 leaves the
-// reference where it is.  The weights are rounded to bf16 for the second product, their sum is of the unrounded ones.
+// transposed (ds_read_tr16).  The softmax is in the base 2; its reference is set 2^16 above the maximum and
+// moves when it is passed.  The weights are rounded to bf16 for the second product, their sum is of the unrounded ones.
 //
 // Large tiles: eight waves, two on each SIMD, the second four half a stage behind (a barrier after each half), so that one of
 // a SIMD's two is at its products while the other is at its softmax: 8192 tokens by 64 heads of 128 features take 1.48 ms
@@ -300,15 +300,15 @@ __global__ __launch_bounds__(NW* kWave, 2) void k_expanded(ExpandedArgs a) {
       for (int tb = 0; tb < kTB / 16; ++tb)
 #pragma unroll
         for (int e = 0; e < 4; ++e) m = fmaxf(m, s[tb][mb][e]);
-      m = quad_max(m) * a.scale_log2;  // (the scale is positive: its sign is in the queries)
+      m = rounded_product(quad_max(m), a.scale_log2);  // (the scale is positive: its sign is in the queries)
       m_new[mb] = m;
-      grow |= m > m_run[mb] + kGrow;
+      grow |= m > m_run[mb];
     }
     if (__any(grow)) {
       bool high = false;
 #pragma unroll
       for (int mb = 0; mb < RB; ++mb) {
-        const float m = fmaxf(m_run[mb], m_new[mb]);
+        const float m = moved_reference(m_run[mb], m_new[mb]);
         const float alpha = m == -kInf ? 1.0f : __builtin_amdgcn_exp2f(m_run[mb] - m);
         m_run[mb] = m;
         l_own[mb] *= alpha;
@@ -325,7 +325,7 @@ __global__ __launch_bounds__(NW* kWave, 2) void k_expanded(ExpandedArgs a) {
 #pragma unroll
         for (int tb = 0; tb < kTB / 16; ++tb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[tb][mb][e] *= scale;
+          for (int e = 0; e < 4; ++e) s[tb][mb][e] = rounded_product(s[tb][mb][e], scale);
       scale = 1.0f;
     }
 #pragma unroll

@@ -13,9 +13,17 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4_t;
 
 constexpr float kInf = __builtin_inff();
-// A reference maximum moves when it is passed by more than a factor 2^16: weights up to that cost nothing in fp32 sums
-// and bf16 weights, and accumulators are rarely scaled.
+// The reference of a softmax is set 2^16 above the highest score and moves when a score passes it, so accumulators are rarely
+// scaled.  Weights are 1 at most (whatever values fp32 can add up stay in range), and 2^-16 costs nothing in fp32 sums and
+// bf16 weights.
 constexpr float kGrow = 16.0f;
+__device__ __forceinline__ float moved_reference(float m_run, float m_new) { return m_new > m_run ? m_new + kGrow : m_run; }
+
+// A product that is rounded by itself, not fused into what it is added to.
+__device__ __forceinline__ float rounded_product(float a, float b) {
+#pragma clang fp contract(off)
+  return a * b;
+}
 
 // Scores times the scale are taken to a reference of more than 2^24 rounded: the reference is the rounded product of the highest
 // score, and a fused product less it would be that rounding's error, which from 2^31 on passes the exponents of fp32 (weights
