@@ -21,6 +21,10 @@ COMMON = ["--offload-arch=" + ARCH, "-O3", "-fPIC", "-std=c++17",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
           "-fno-gpu-flush-denormals-to-zero", "-Wno-unused-command-line-argument"]
 
+# Results of matrix instructions in either half of the register file, not all in accumulation registers: at 512 features and
+# 128 rows the outputs fill those (64 requests of 128 heads: 174 us, 190 without)
+EXTRA = {"latent_absorbed_rows.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+
 ENGRAM_SRC = ["engram_api.hip", "gather_gate.hip", "hash.hip", "stream.hip", "tiled.hip",
               "serving_api.hip", "batch_plan.hip", "hash_paged.hip", "residual_norm.hip", "linear.hip",
               "latent_api.hip", "latent_cache.hip", "latent_absorbed.hip", "latent_absorbed_rows.hip",
@@ -48,7 +52,7 @@ def build(verbose: bool = False) -> None:
     jobs = []
     for s in ENGRAM_SRC:
         o = os.path.join(obj_dir, s.replace(".hip", ".o"))
-        jobs.append((o, [HIPCC] + COMMON + ["-I", os.path.join(ROOT, "include"), "-c",
+        jobs.append((o, [HIPCC] + COMMON + EXTRA.get(s, []) + ["-I", os.path.join(ROOT, "include"), "-c",
                                             os.path.join(csrc, s), "-o", o]))
     synth_o = os.path.join(obj_dir, "synth_fill.o")
     jobs.append((synth_o, [HIPCC] + COMMON + ["-ffp-contract=off", "-c",

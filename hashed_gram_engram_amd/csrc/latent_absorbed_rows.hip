@@ -30,44 +30,17 @@ __device__ __forceinline__ void wait_copies() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// Scores of two blocks of positions (k0, k1) and two of queries (q0, q1): s += k q^T.  In assembly, for the results to lie
-// in vector registers: the compiler keeps every MFMA's result of a kernel in accumulation registers, and at 512
-// features the 256 of them hold the outputs.  The first wait covers operands that a vector instruction wrote last.
-__device__ __forceinline__ void first_scores(f32x4 (&s)[2][2], u32x4 k0, u32x4 k1, u32x4 q0, u32x4 q1) {
-  asm("s_nop 1\n\t"
-      "v_mfma_f32_16x16x32_bf16 %0, %4, %6, 0\n\t"
-      "v_mfma_f32_16x16x32_bf16 %1, %4, %7, 0\n\t"
-      "v_mfma_f32_16x16x32_bf16 %2, %5, %6, 0\n\t"
-      "v_mfma_f32_16x16x32_bf16 %3, %5, %7, 0"
-      : "=&v"(s[0][0]), "=&v"(s[0][1]), "=&v"(s[1][0]), "=&v"(s[1][1])
-      : "v"(k0), "v"(k1), "v"(q0), "v"(q1));
-}
-__device__ __forceinline__ void add_scores(f32x4 (&s)[2][2], u32x4 k0, u32x4 k1, u32x4 q0, u32x4 q1) {
-  asm("s_nop 1\n\t"
-      "v_mfma_f32_16x16x32_bf16 %0, %4, %6, %0\n\t"
-      "v_mfma_f32_16x16x32_bf16 %1, %4, %7, %1\n\t"
-      "v_mfma_f32_16x16x32_bf16 %2, %5, %6, %2\n\t"
-      "v_mfma_f32_16x16x32_bf16 %3, %5, %7, %3"
-      : "+v"(s[0][0]), "+v"(s[0][1]), "+v"(s[1][0]), "+v"(s[1][1])
-      : "v"(k0), "v"(k1), "v"(q0), "v"(q1));
-}
-// Before a vector instruction reads them: an MFMA of 16 passes takes 19 wait states, these have fewer.
-__device__ __forceinline__ void finish_scores(f32x4 (&s)[2][2]) {
-  asm("s_nop 15\n\ts_nop 4" : "+v"(s[0][0]), "+v"(s[0][1]), "+v"(s[1][0]), "+v"(s[1][1]));
-}
-
 // What is seldom done to the accumulators (scaling them, adding a single row) is done in memory, in the part of the
-// workspace that the segment may write: touched by vector instructions anywhere in the loop over the stages, copies
-// of them all would be kept around it.  One store or load of 16 bytes a lane for each block; the stores take
-// them from accumulation registers, behind the waits that an MFMA's results need.
+// workspace that the segment may write: done in registers it takes some from the loop over the stages (512 features, 128
+// rows, FP8: 33 that go through memory there instead of 27).  One store or load of 16 bytes a lane for each block.
 template <int N, int RB>
 __device__ __forceinline__ void acc_to_memory(const f32x4 (&acc)[N][RB], char* to) {
-  asm volatile("s_nop 15\n\ts_nop 4" ::: "memory");
+  asm volatile("" : "+v"(to)::"memory");
 #pragma unroll
   for (int mb = 0; mb < RB; ++mb)
 #pragma unroll
     for (int fb = 0; fb < N; ++fb) {
-      asm volatile("global_store_dwordx4 %0, %1, off" ::"v"(to), "a"(acc[fb][mb]) : "memory");
+      *reinterpret_cast<f32x4*>(to) = acc[fb][mb];
       to += kWave * 16;
     }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -373,7 +346,6 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed_rows(A
           kf[kb][0] = key(kb, 0);
           kf[kb][1] = key(kb, 1);
         }
-        if constexpr (RB == 1) s[0][0] = s[1][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         constexpr int kSteps = S::kKB + 2;
         int from[2];
         const Copies cp = copies_of(c + kCopyStage);
@@ -390,19 +362,16 @@ __global__ __launch_bounds__(kThreads, DC == 128 ? 2 : 1) void k_absorbed_rows(A
           }
           side(kb);
           if (kb < S::kKB + 1 || rkb == 2) {
-            if constexpr (RB == 2) {
-              if (kb == 0) first_scores(s, kf[0][0], kf[0][1], qf[0][0], qf[1][0]);
-              else add_scores(s, kf[kb % kDeep][0], kf[kb % kDeep][1], qf[0][kb], qf[1][kb]);
-            } else {
 #pragma unroll
-              for (int tb = 0; tb < 2; ++tb) s[tb][0] = mfma16x16x32(kf[kb % kDeep][tb], qf[0][kb], s[tb][0]);
-            }
+            for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+              for (int mb = 0; mb < RB; ++mb)
+                s[tb][mb] = mfma16x16x32(kf[kb % kDeep][tb], qf[mb][kb], kb == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : s[tb][mb]);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int kb = kSteps; kb < S::kCopies + 2; ++kb) side(kb);  // what small latents leave
-        if constexpr (RB == 2) finish_scores(s);
       }
       copy_pages(c + kCopyStage + 3);
 
