@@ -126,8 +126,9 @@ _lib.engram_latent_attention_expanded.argtypes = [_LL, _vp, _i64, _vp, _i64, _vp
                                                   _i64, _vp, _vp, _sz, _vp]
 _lib.engram_latent_attention_workspace_bytes.argtypes = [_LL]
 _lib.engram_latent_attention_expanded_workspace_bytes.argtypes = [_LL, _i64, _i64, _i64]
+_lib.engram_latent_attention_expanded_workspace_bytes_up_to.argtypes = [_LL, _i64, _i64]
 for _f in (_lib.engram_latent_row_bytes, _lib.engram_latent_attention_workspace_bytes,
-           _lib.engram_latent_attention_expanded_workspace_bytes):
+           _lib.engram_latent_attention_expanded_workspace_bytes, _lib.engram_latent_attention_expanded_workspace_bytes_up_to):
     _f.restype = _sz
 for _f in (_lib.engram_latent_layout_check, _lib.engram_latent_write, _lib.engram_latent_read, _lib.engram_latent_attention,
            _lib.engram_latent_attention_expanded):
@@ -149,7 +150,7 @@ EXPORTED = ["engram_layout_check", "engram_param_counts", "engram_forward_worksp
             "engram_page_layout_check", "engram_norm_layout_check", "engram_linear_layout_check",
             "engram_latent_layout_check", "engram_latent_row_bytes", "engram_latent_write", "engram_latent_read",
             "engram_latent_attention", "engram_latent_attention_workspace_bytes", "engram_latent_attention_expanded",
-            "engram_latent_attention_expanded_workspace_bytes"]
+            "engram_latent_attention_expanded_workspace_bytes", "engram_latent_attention_expanded_workspace_bytes_up_to"]
 
 
 SCALE_FP32, SCALE_E8M0 = 0, 1  # engram_scale_format
@@ -999,6 +1000,11 @@ def engram_latent_attention_expanded_workspace_bytes(layout: LatentLayout, R: in
     return int(_lib.engram_latent_attention_expanded_workspace_bytes(ctypes.byref(layout), R, n_tokens, n_rows))
 
 
+def engram_latent_attention_expanded_workspace_bytes_up_to(layout: LatentLayout, n_tokens: int, n_rows: int) -> int:
+    """Enough for every call with 1 .. n_tokens tokens over 0 .. n_rows rows on the current device."""
+    return int(_lib.engram_latent_attention_expanded_workspace_bytes_up_to(ctypes.byref(layout), n_tokens, n_rows))
+
+
 def _attention_out(q: torch.Tensor, out: Optional[torch.Tensor], n: int, row: tuple, dev: int):
     """(out, its stride)."""
     if out is None:
@@ -1056,7 +1062,8 @@ def engram_latent_attention_expanded(layout: LatentLayout, q: torch.Tensor, kv: 
     [plan.max_tokens, heads, head_dim] bf16 of q [plan.max_tokens, heads, head_dim + rope_dim], kv [n_rows, heads,
     2 * head_dim] (of each head the key part, then the value), rope [n_rows, rope_dim] and row_start [R + 1] as
     engram_latent_read gives it, for requests with at least min_tokens new tokens.  q, kv, rope and out may be slices of
-    wider rows; rows of other tokens, lse and workspace as in engram_latent_attention."""
+    wider rows; rows of other tokens, lse and workspace as in engram_latent_attention.  A workspace that is kept for steps of
+    different lengths is sized by engram_latent_attention_expanded_workspace_bytes_up_to."""
     _no_grad("engram_latent_attention_expanded", q=q, kv=kv, rope=rope, out=out, lse=lse)
     (R, n), dev, H, D, bf16 = plan._sizes, q.get_device(), layout.heads, layout.head_dim, torch.bfloat16
     at = _plan_on(plan, dev)._out

@@ -97,6 +97,7 @@ struct ExpandedArgs {
   int tiles, parts;
 };
 int64_t expanded_workspace_bytes(int64_t R, int64_t n_tokens, int64_t n_rows, int heads, int head_dim, int cus);
+int64_t expanded_workspace_bytes_up_to(int64_t n_tokens, int64_t n_rows, int heads, int head_dim, int cus);  // for fewer, too
 hipError_t launch_latent_expanded(ExpandedArgs a, int cus, hipStream_t stream);
 
 }  // namespace engram

@@ -199,6 +199,15 @@ size_t engram_latent_attention_expanded_workspace_bytes(const engram_latent_layo
   return size_t(expanded_workspace_bytes(R, n_tokens, n_rows, l->heads, l->head_dim, cus));
 }
 
+size_t engram_latent_attention_expanded_workspace_bytes_up_to(const engram_latent_layout* l, int64_t n_tokens, int64_t n_rows) {
+  if (engram_latent_layout_check(l) != ENGRAM_OK || n_tokens < 1 || n_tokens > (int64_t(1) << 30) / l->heads || n_rows < 0 ||
+      n_rows > (int64_t(1) << 30))
+    return 0;
+  DeviceInfo di;
+  const int cus = device_info(&di) == ENGRAM_OK ? di.cus : 256;
+  return size_t(expanded_workspace_bytes_up_to(n_tokens, n_rows, l->heads, l->head_dim, cus));
+}
+
 engram_status engram_latent_attention_expanded(const engram_latent_layout* l, const uint16_t* q, int64_t q_stride,
                                                const uint16_t* kv, int64_t kv_stride, const uint16_t* rope,
                                                int64_t rope_stride, const int32_t* row_start, int64_t n_rows,

@@ -587,6 +587,17 @@ int64_t expanded_workspace_bytes(int64_t R, int64_t n_tokens, int64_t n_rows, in
   return c.parts > 1 ? int64_t(c.parts) * n_tokens * heads * (head_dim + 2) * 4 : 0;
 }
 
+// For all of 1 .. n_tokens tokens and 0 .. n_rows rows of any requests.  Parts are 32 at most, with four stages each at least,
+// and (2 cus - 1) / tiles + 1 at most where there are fewer tiles than CUs; a call's rows (tokens times heads) are tiles of 256
+// rows at most each.  So parts times rows are 256 (2 cus - 1 + tiles) at most, and tiles cus - 1.
+int64_t expanded_workspace_bytes_up_to(int64_t n_tokens, int64_t n_rows, int heads, int head_dim, int cus) {
+  int64_t parts = n_rows / kTB / 4;
+  if (parts < 2) return 0;
+  if (parts > 32) parts = 32;
+  const int64_t rows = parts * n_tokens * heads, most = int64_t(256) * (3 * cus - 2);
+  return (rows < most ? rows : most) * (head_dim + 2) * 4;
+}
+
 hipError_t launch_latent_expanded(ExpandedArgs a, int cus, hipStream_t stream) {
   const Choice c = choose(a.rq.R, a.rq.n_tokens, a.n_rows, a.heads, a.head_dim, cus);
   a.tiles = c.tiles;

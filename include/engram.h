@@ -525,9 +525,15 @@ engram_status engram_latent_attention_expanded(const engram_latent_layout* layou
                                                int64_t out_stride, float* lse, void* workspace,
                                                size_t workspace_bytes, engram_stream_t stream);
 
-/* The same for engram_latent_attention_expanded with n_tokens tokens of R requests over n_rows rows. */
+/* The same for engram_latent_attention_expanded with n_tokens tokens of R requests over n_rows rows.  It does not grow
+ * with the tokens: few tokens have few tiles, whose rows are then divided (512 tokens of 16 heads over 16,896 rows need
+ * 68 MB, 8192 none), and a call whose workspace is too small is refused. */
 size_t engram_latent_attention_expanded_workspace_bytes(const engram_latent_layout* layout, int64_t R,
                                                         int64_t n_tokens, int64_t n_rows);
+/* Enough for every call with 1 .. n_tokens tokens over 0 .. n_rows rows, whatever its requests: for a workspace that is
+ * kept for steps of different lengths (about 100 MB at most for head_dim 128). */
+size_t engram_latent_attention_expanded_workspace_bytes_up_to(const engram_latent_layout* layout, int64_t n_tokens,
+                                                              int64_t n_rows);
 
 /* Host-only checks of the layouts above; no device work. */
 engram_status engram_latent_layout_check(const engram_latent_layout* layout);
