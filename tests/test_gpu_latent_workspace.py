@@ -10,7 +10,7 @@ from gpu_common import eg, say  # noqa: E402
 from test_gpu_latent_attention import Expanded, normal  # noqa: E402
 
 
-@pytest.mark.parametrize("hd,H", [(128, 8), (64, 16)])
+@pytest.mark.parametrize("hd,H", [(128, 8), (64, 24)])
 def test_one_workspace_for_steps_of_every_length(hd, H):
     say(f"[gpu] expanded: one workspace for steps of 1 .. 3000 tokens, {H} heads of {hd}")
     rng = np.random.default_rng(61)
