@@ -66,7 +66,7 @@ engram_status engram_latent_layout_check(const engram_latent_layout* l) {
   if (l->rope_dim != 32 && l->rope_dim != 64) return ENGRAM_E_LAYOUT;
   if (l->head_dim != 64 && l->head_dim != 128) return ENGRAM_E_LAYOUT;
   if (l->cache_format != ENGRAM_CACHE_BF16 && l->cache_format != ENGRAM_CACHE_MXFP8) return ENGRAM_E_LAYOUT;
-  if (l->window < 0 || !isfinite(l->scale)) return ENGRAM_E_LAYOUT;
+  if (l->window < 0 || !(fabsf(l->scale) < 0x1p127f)) return ENGRAM_E_LAYOUT;  // (times log2 e it stays finite)
   return ENGRAM_OK;
 }
 

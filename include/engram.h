@@ -447,7 +447,7 @@ typedef struct {
   int32_t head_dim;     /* expanded form: features of a head's own key part and of its value, 64 or 128 */
   int32_t cache_format; /* engram_cache_format                                                      */
   int32_t window;       /* 0: a token sees every position up to its own; w > 0: the last w of them  */
-  float scale;          /* of the scores; finite                                                    */
+  float scale;          /* of the scores; below 2^127 in magnitude                                   */
 } engram_latent_layout;
 
 /* Bytes of a cache row (0 on an invalid layout).  A cache is [n_blocks, block_size, row bytes]. */
