@@ -221,6 +221,8 @@ engram_status engram_latent_attention_expanded(const engram_latent_layout* l, co
   memset(&a, 0, sizeof(a));
   if ((st = requests(l, token_start, start_pos, R, n_tokens, &a.rq)) != ENGRAM_OK) return st;
   if (min_tokens < 1 || n_rows < 0 || n_rows > (int64_t(1) << 30)) return ENGRAM_E_SHAPE;
+  // a launch of 2^32 threads and more loses some without an error: at most 256 for each tile of 64 tokens and head
+  if ((n_tokens / 64 + (R < n_tokens ? R : n_tokens)) * l->heads >= int64_t(1) << 24) return ENGRAM_E_SHAPE;
   if (R == 0 || n_tokens == 0) return ENGRAM_OK;
   if (!q || !row_start || !out || (n_rows > 0 && (!kv || !rope))) return ENGRAM_E_NULL;
   if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(rope, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(row_start, 4))

@@ -429,8 +429,9 @@ size_t engram_linear_workspace_bytes_up_to(const engram_linear_layout* layout, i
  * token_start, start_pos, slots are a plan's (engram_batch_plan_out); the new tokens of request r are flat
  * tokens token_start[r] .. token_start[r + 1] - 1, at positions start_pos[r] .. .  Whatever these arrays
  * hold, no access leaves the tensors: token ranges are cut to n_tokens, positions to max_blocks * block_size.
- * The ranges of different requests must not overlap (a plan's do not).  At most 4096 requests, and 2^31 - 1 slots
- * (n_blocks * block_size) in a cache, else ENGRAM_E_LAYOUT.  Strides are 2^28 at most.
+ * The ranges of different requests must not overlap (a plan's do not).  At most 4096 requests, 2^30 tokens (of
+ * attentions 2^30 / heads) and strides of 2^28, else ENGRAM_E_SHAPE; at most 2^31 - 1 slots (n_blocks * block_size) in a
+ * cache, else ENGRAM_E_LAYOUT.
  * The conventions above hold; calls that write different buffers may overlap in time. */
 
 /* A cache row (one slot of a page), engram_latent_row_bytes() bytes.
@@ -515,7 +516,8 @@ size_t engram_latent_attention_workspace_bytes(const engram_latent_layout* layou
  *   out  [n_tokens, heads, head_dim] bf16, out_stride (a multiple of 8); lse as above
  * s_j = scale * q . (key part of row j and head, rope_j) over the request's rows at positions j <= p
  * (window: j > p - window), out = sum_j softmax(s)_j value_j; empty rows, masked rows, precision and other
- * tokens as above. */
+ * tokens as above.  (n_tokens / 64 + min(R, n_tokens)) * heads has to be below 2^24, else
+ * ENGRAM_E_SHAPE. */
 engram_status engram_latent_attention_expanded(const engram_latent_layout* layout, const uint16_t* q,
                                                int64_t q_stride, const uint16_t* kv, int64_t kv_stride,
                                                const uint16_t* rope, int64_t rope_stride,
