@@ -176,6 +176,7 @@ __global__ __launch_bounds__(256) void k_gather_mx(GatherArgs a, uint8_t* codes8
 hipError_t launch_gather_mx(const GatherArgs& a, uint8_t* codes8, uint8_t* scales8, hipStream_t stream) {
   const int64_t threads = a.n_pairs * (a.head_dim >> 4);
   const int64_t blocks = (threads + 255) / 256;
+  if (!launch_fits(blocks, 256)) return hipErrorInvalidValue;
   hipLaunchKernelGGL(k_gather_mx, dim3(unsigned(blocks)), dim3(256), 0, stream, a, codes8, scales8);
   return hipGetLastError();
 }
@@ -203,6 +204,7 @@ hipError_t launch_expand_mxfp8(const uint8_t* codes, const uint8_t* scales, int6
                                hipStream_t stream) {
   const int64_t n16 = N * K / 16;
   const int64_t blocks = (n16 + 255) / 256;
+  if (!launch_fits(blocks, 256)) return hipErrorInvalidValue;
   hipLaunchKernelGGL(k_expand_mxfp8, dim3(unsigned(blocks)), dim3(256), 0, stream, codes, scales, n16, K, out);
   return hipGetLastError();
 }
@@ -211,11 +213,13 @@ hipError_t launch_gather_dequant(const GatherArgs& a, hipStream_t stream) {
   const int64_t pairs = a.frag_cols > 0 && a.n_fill > a.n_pairs ? a.n_fill : a.n_pairs;
   const int64_t threads = pairs * (a.head_dim >> 4);
   const int64_t blocks = (threads + 255) / 256;
+  if (!launch_fits(blocks, 256)) return hipErrorInvalidValue;
   hipLaunchKernelGGL(k_gather_dequant, dim3(unsigned(blocks)), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
 hipError_t launch_gate_apply(const GateArgs& a, hipStream_t stream) {
+  if (!launch_fits(a.M, 256)) return hipErrorInvalidValue;
   hipLaunchKernelGGL(k_gate_apply, dim3(unsigned(a.M)), dim3(256), 0, stream, a);
   return hipGetLastError();
 }

@@ -76,7 +76,7 @@ hipError_t launch_hash_ids(const HashArgs& a, hipStream_t stream) {
   if (n <= 0) return hipSuccess;
   if (a.max_ngram < 2 || a.max_ngram > kMaxNgram) return hipErrorInvalidValue;
   const int64_t grid = (n + 255) / 256;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (!launch_fits(grid, 256)) return hipErrorInvalidValue;
   HashArgs args = a;
   void* params[] = {&args};
   return hipLaunchKernel(reinterpret_cast<const void*>(&k_hash_ids), dim3(unsigned(grid)), dim3(256), params, 0,

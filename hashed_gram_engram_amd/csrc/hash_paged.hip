@@ -117,7 +117,7 @@ hipError_t launch_hash_ids_paged(const HashPagedArgs& a, hipStream_t stream) {
   if (a.max_ngram < 2 || a.max_ngram > kMaxLookBack) return hipErrorInvalidValue;
   int per_group = a.n_tokens >= 2048 ? kHashTokens : 8;
   const int64_t grid = (a.n_tokens + per_group - 1) / per_group;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (!launch_fits(grid, kHashThreads)) return hipErrorInvalidValue;
   HashPagedArgs args = a;
   void* params[] = {&args, &per_group};
   return hipLaunchKernel(reinterpret_cast<const void*>(&k_hash_ids_paged), dim3(unsigned(grid)), dim3(kHashThreads),

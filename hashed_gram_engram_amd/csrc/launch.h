@@ -15,6 +15,9 @@ struct DeviceInfo {
 };
 engram_status device_info(DeviceInfo* out);  // of the current device; ENGRAM_E_DEVICE: not gfx950
 
+// A launch of 2^32 threads and more loses some without an error.
+inline bool launch_fits(int64_t groups, int64_t threads) { return groups < (int64_t(1) << 32) / threads; }
+
 struct GatherArgs {
   const uint8_t* table;
   const void* scales;  // fp32, or E8M0 bytes when scale_e8m0

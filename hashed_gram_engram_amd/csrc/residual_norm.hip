@@ -11,6 +11,7 @@
 // round trips for a decode step (64 such tokens 4.7 us).  r and h are stored past the caches (nothing of
 // this launch reads them again): 244 -> 231 us.
 #include "common.h"
+#include "launch.h"
 #include "serving.h"
 
 namespace engram {
@@ -199,7 +200,7 @@ template <int T, int NV>
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
   constexpr int kRows = (T < 256 ? 256 : T) / T;
   const int64_t grid = (a.M * a.hc + kRows - 1) / kRows;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (!launch_fits(grid, T < 256 ? 256 : T)) return hipErrorInvalidValue;
   NormArgs args = a;
   void* params[] = {&args};
   const void* fn = a.fp32 ? reinterpret_cast<const void*>(&k_residual_norm<T, NV, true>)

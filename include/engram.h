@@ -39,7 +39,7 @@ typedef enum {
   ENGRAM_E_SHAPE = -3,     /* negative B or T, or a size that overflows          */
   ENGRAM_E_ALIGN = -4,     /* a tensor pointer is not aligned as required        */
   ENGRAM_E_WORKSPACE = -5, /* workspace missing or smaller than required         */
-  ENGRAM_E_HIP = -6,       /* the HIP runtime refused a launch or query          */
+  ENGRAM_E_HIP = -6,       /* the HIP runtime refused a launch or query, or a launch would need 2^32 threads or more */
   ENGRAM_E_DEVICE = -7,    /* the current device is not gfx950                   */
   ENGRAM_E_TIMEOUT = -8    /* a cross-workgroup wait of engram_forward gave up: the outputs of
                               the calls since the last engram_forward_check are wrong         */
