@@ -12,7 +12,8 @@
 //           positions in the product being that of the score fragments.
 //
 // For 32 rows a request and fewer, where the cache's bytes are what costs: 128 requests of up to 8192 positions, 16 heads,
-// BF16 rows of 512 + 64: 175 us for 793 MB, 4.5 TB/s.
+// BF16 rows of 512 + 64: 177 to 189 us by the device for 793 MB, 4.2 to 4.5 TB/s (62% of the waves' cycles wait, for
+// memory: stages are copied one ahead).
 //
 // Work is shared out in units of one stage of one tile: workgroup w of G takes units [w U / G, (w + 1) U / G) of
 // the step's U, whatever the requests' lengths, so every CU has the same share.  What a workgroup holds of a
@@ -447,8 +448,8 @@ hipError_t run(const AbsorbedArgs& a, int cus, hipStream_t stream) {
   if (rows <= 32) return run<DC, 2>(a, G, stream);
   // Tiles of 128 rows read LDS half as often, but leave parts of twice the size: they pay where workgroups go over many
   // stages each.  The lengths are not known here; at most, the requests fill the table.  (64 requests of up to 8192
-  // positions, 128 heads: 196 us, 217 us in tiles of 64 rows; 32 of up to 3001, 5 tokens of 32 heads: 54 us and 51;
-  // one of 65,536, 128 heads: 74 us and 59.)
+  // positions, 128 heads: 174 us a pass, 204 us in tiles of 64 rows; 32 of up to 3001, 5 tokens of 32 heads: 51 us and 48;
+  // one of 65,536, 128 heads: 69 us and 57.)
   const int64_t stages = (rows + 127) / 128 * a.rq.R * (int64_t(a.rq.max_blocks) * a.rq.block_size / 32);
   return launch_absorbed_rows(a, G, rows > 64 && stages >= 32 * int64_t(G), stream);
 }

@@ -1,8 +1,9 @@
 // Absorbed latent attention for many rows a request (tokens times heads): tiles of M = 64 RB rows.
 //
 // Each of the four waves takes 16 RB rows of the tile and all of the latent: its queries and its accumulators
-// (512 features: 144 and 256 registers a lane at RB 2) stay in registers, and a stage of 32 positions goes through
-// LDS as bf16, read twice by every wave: along the features for the scores, transposed for the values.
+// (512 features: 144 and 256 registers a lane at RB 2, where the compiler keeps some 20 of the others in memory, outside
+// the products) stay in registers, and a stage of 32 positions goes through LDS as bf16, read twice by every wave: along
+// the features for the scores, transposed for the values.
 // S^T = C Q^T leaves a lane with 4 consecutive positions of one query, which is an operand of out^T += C^T P^T
 // as it stands if that product counts its positions in the same order; so weights, maxima and sums never leave a wave.
 // (latent_absorbed.hip has the form for few rows, where the waves share the latent instead.)
@@ -10,10 +11,12 @@
 // FP8 rows are copied to LDS as they are, three stages ahead, and converted one stage ahead by the lanes that
 // copied them; BF16 rows are copied two stages ahead to where they are read.
 //
-// What bounds it: a wave has its SIMD to itself, so its products wait for its softmax.  64 requests of up to 8192 positions,
-// 128 heads, 512 + 64 features in FP8: 179 us, 0.57 PFLOP/s; a stage of 32 positions takes 2780 cycles for the scores with
-// the copies (1152 are products), 720 for the softmax, 2600 for the second product with the next stage's conversion
-// (1024 are products).  One request of 65,536: 45 us; 32 of up to 3001, 5 tokens, 32 heads, 256 + 64 features, window 2000: 42 us.
+// What bounds it: a wave has its SIMD to itself, and nothing issues while it waits.  64 requests of up to 8192 positions,
+// 128 heads, 512 + 64 features in FP8: 172 us, 0.59 PFLOP/s; of a wave's cycles 30% are matrix instructions, 35% issue vector
+// ones (conversion, softmax, addresses) and 23% wait.  Part of the waits is the compiler's: the rare branches end in
+// loads into the accumulators, and where they meet the common path, at the start of the second product, it waits for all
+// memory, the copies that the stage has just issued included.  One request of 65,536: 45 us (18% matrix, 21% vector, 33%
+// waits; a workgroup has 16 stages); 32 of up to 3001, 5 tokens, 32 heads, 256 + 64 features, window 2000: 41 us (14%, 21%, 35%).
 #include "latent_units.h"
 
 namespace engram {
